@@ -9,10 +9,20 @@ allocated with torch when not passed in.
     px, _ = moe_dispatch(x, plan.tok_map)          # packed_x[off[e] + slot]
     y     = experts(px, plan)                      # caller's expert stage
     out   = moe_combine(y, topk_w, plan.tok_map)   # sum_k w * y[tok_map]
+
+The experts' products and the way back:
+
+    y      = moe_expert_gemm(px, w, plan)              # y[r] = w[e] px[r]
+    dy, dw = moe_combine_backward(dout, y, topk_w, plan)
+    dpx    = moe_expert_gemm_dgrad(dy, w, plan)
+    dwe    = moe_expert_gemm_wgrad(dy, px, plan)
+    dx     = moe_dispatch_backward(dpx, plan)          # sum_k dpx[tok_map]
+    norm   = moe_clip_grad_norm([dwe, ...], 1.0)       # in place
 """
 from __future__ import annotations
 
-from typing import NamedTuple, Optional
+import ctypes
+from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
 
@@ -23,6 +33,8 @@ __all__ = [
     "moe_plan", "moe_group_plan", "moe_dispatch", "moe_plan_dispatch", "moe_dispatch_dedup", "moe_dispatch_quant_fp8",
     "moe_combine", "moe_combine_fold",
     "moe_combine_dedup", "moe_plan_workspace_size", "moe_group_plan_workspace_size",
+    "moe_combine_backward", "moe_dispatch_backward", "moe_expert_gemm", "moe_expert_gemm_dgrad",
+    "moe_expert_gemm_wgrad", "moe_grad_norm", "moe_clip_grad_norm",
     "moe_device_errors", "moe_plan_capacity", "Plan", "GroupPlan", "CapacityPlan", "MoeError",
     "MoeOp", "Routing", "lib",
 ]
@@ -359,11 +371,175 @@ def moe_combine_fold(y: torch.Tensor, topk_w: Optional[torch.Tensor], token_map:
     return out, out_weights
 
 
+def moe_dispatch_backward(dpacked: torch.Tensor, plan: Union[Plan, CapacityPlan], *,
+                          out_dtype: torch.dtype = torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_dispatch: dx[s] = sum over valid k of
+    dpacked[tok_map[s,k]], in f32, increasing k."""
+    return moe_combine_fold(dpacked, None, plan.tok_map, weighted=False, fold=False,
+                            out_dtype=out_dtype, out=out, stream=stream)[0]
+
+
+def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tensor,
+                         plan: Union[Plan, CapacityPlan], *, dy: Optional[torch.Tensor] = None,
+                         dw: Optional[torch.Tensor] = None, stream=None):
+    """Gradient of moe_combine: dy[tok_map[s,k]] = topk_w[s,k] * dout[s], zero
+    on rows that no entry fills, and dw[s,k] = <dout[s], y[tok_map[s,k]]>,
+    zero without a row.  Returns (dy in y's type, dw f32 [S, K])."""
+    S, K = plan.tok_map.shape
+    E = plan.cnt.numel()
+    if y.dim() != 2 or tuple(dout.shape) != (S, y.shape[1]):
+        raise ValueError("dout must be [S, H] and y [rows, H]")
+    if topk_w.dtype != torch.float32 or tuple(topk_w.shape) != (S, K):
+        raise TypeError("topk_w must be float32 with the shape of tok_map")
+    if dy is None:
+        dy = torch.empty_like(y)
+    elif dy.dtype != y.dtype or dy.shape != y.shape:
+        raise ValueError("dy must have y's type and shape")
+    if dw is None:
+        dw = torch.empty(S, K, dtype=torch.float32, device=y.device)
+    elif dw.dtype != torch.float32 or tuple(dw.shape) != (S, K):
+        raise ValueError("dw must be float32 [S, K]")
+    _abi.check("moe_combine_backward", lib().moe_combine_backward(
+        _ptr(dout), _dt(dout), _ptr(y), y.shape[0], _dt(y), _ptr(topk_w), _ptr(plan.tok_map),
+        _ptr(plan.cnt), _ptr(plan.off), S, y.shape[1], K, E, _ptr(dy), _ptr(dw),
+        _stream(stream, y)))
+    return dy, dw
+
+
+def _expert_args(rows: torch.Tensor, name: str, w: torch.Tensor, width: int, plan):
+    if rows.dtype != torch.bfloat16 or w.dtype != torch.bfloat16:
+        raise TypeError(f"{name} and w must be bfloat16")
+    if w.dim() != 3 or rows.dim() != 2 or rows.shape[1] != w.shape[width]:
+        raise ValueError(f"w must be [E, N, D] and {name} [rows, {'N' if width == 1 else 'D'}]")
+    if plan.cnt.numel() != w.shape[0]:
+        raise ValueError("the plan and w must have the same number of experts")
+
+
+def _expert_out(out, shape, dtype, device):
+    if out is None:
+        if dtype not in _TORCH_DT.values():
+            raise TypeError(f"unsupported output dtype {dtype}")
+        return torch.empty(shape, dtype=dtype, device=device)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"out must be {list(shape)}")
+    if out.dtype not in _TORCH_DT.values():
+        raise TypeError(f"unsupported output dtype {out.dtype}")
+    return out
+
+
+def moe_expert_gemm(x: torch.Tensor, w: torch.Tensor, plan: Union[Plan, CapacityPlan], *,
+                    out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """y[r] = w[e] x[r] for the rows of each bucket e of the plan, zero on rows
+    in no bucket.  x bf16 [rows, D], w bf16 [E, N, D]; y [rows, N]."""
+    _expert_args(x, "x", w, 2, plan)
+    E, N, D = w.shape
+    out = _expert_out(out, (x.shape[0], N), out_dtype, x.device)
+    _abi.check("moe_expert_gemm", lib().moe_expert_gemm(
+        _ptr(x), x.shape[0], _ptr(w), N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),
+        _dt(out), _stream(stream, x)))
+    return out
+
+
+def moe_expert_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, plan: Union[Plan, CapacityPlan], *,
+                          out_dtype: torch.dtype = torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_expert_gemm for its rows: dx[r] = w[e]^T dy[r], zero on
+    rows in no bucket.  dy bf16 [rows, N]; dx [rows, D]."""
+    _expert_args(dy, "dy", w, 1, plan)
+    E, N, D = w.shape
+    out = _expert_out(out, (dy.shape[0], D), out_dtype, dy.device)
+    _abi.check("moe_expert_gemm_dgrad", lib().moe_expert_gemm_dgrad(
+        _ptr(dy), dy.shape[0], _ptr(w), N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),
+        _dt(out), _stream(stream, dy)))
+    return out
+
+
+def moe_expert_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, plan: Union[Plan, CapacityPlan], *,
+                          out_dtype: torch.dtype = torch.float32,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Gradient of moe_expert_gemm for its weights: dw[e] = sum over the rows
+    of bucket e of dy[r] x[r]^T, zero for an empty bucket.  Returns
+    [E, N, D]."""
+    if dy.dtype != torch.bfloat16 or x.dtype != torch.bfloat16:
+        raise TypeError("dy and x must be bfloat16")
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
+        raise ValueError("dy must be [rows, N] and x [rows, D]")
+    E, N, D = plan.cnt.numel(), dy.shape[1], x.shape[1]
+    out = _expert_out(out, (E, N, D), out_dtype, x.device)
+    _abi.check("moe_expert_gemm_wgrad", lib().moe_expert_gemm_wgrad(
+        _ptr(dy), _ptr(x), x.shape[0], N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),
+        _dt(out), _stream(stream, x)))
+    return out
+
+
+def _grad_list(name: str, tensors: Sequence[torch.Tensor]):
+    """Host arrays of the tensors' addresses, sizes and types."""
+    n = len(tensors)
+    for t in tensors:
+        if t.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name} must be float32 or bfloat16")
+    return ((ctypes.c_void_p * n)(*[_ptr(t) for t in tensors]),
+            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int * n)(*[_dt(t) for t in tensors]))
+
+
+def _grad_call(grads: Sequence[torch.Tensor], norm, workspace, stream):
+    """(device, norm, workspace) of a call over `grads`."""
+    if not grads:
+        raise ValueError("no gradients")
+    like = grads[0]
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=like.device)
+    elif norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be float32 [1]")
+    ws = _workspace(int(lib().moe_grad_norm_workspace_size()), like.device, workspace)
+    if ws is not workspace and stream is not None:
+        # made on the current stream, used on another
+        s = stream if isinstance(stream, torch.cuda.Stream) else \
+            torch.cuda.ExternalStream(_stream(stream, like), device=like.device)
+        ws.record_stream(s)
+    return like, norm, ws
+
+
+def moe_grad_norm(grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The L2 norm over all gradients (float32 or bfloat16, any mix), as a
+    float32 [1] device tensor."""
+    like, norm, ws = _grad_call(grads, norm, workspace, stream)
+    ptrs, numel, types = _grad_list("grads", grads)
+    _abi.check("moe_grad_norm", lib().moe_grad_norm(
+        ptrs, numel, types, len(grads), _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(),
+        _stream(stream, like)))
+    return norm
+
+
+def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *,
+                       out: Optional[Sequence[torch.Tensor]] = None,
+                       norm: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
+    into `out`.  Returns the norm before it, float32 [1] on the device."""
+    like, norm, ws = _grad_call(grads, norm, workspace, stream)
+    if out is None:
+        out = grads
+    elif len(out) != len(grads) or any(o.dtype != g.dtype or o.shape != g.shape
+                                       for o, g in zip(out, grads)):
+        raise ValueError("out must have the types and shapes of grads")
+    ptrs, numel, types = _grad_list("grads", grads)
+    outs = ptrs if out is grads else (ctypes.c_void_p * len(out))(*[_ptr(t) for t in out])
+    _abi.check("moe_clip_grad_norm", lib().moe_clip_grad_norm(
+        ptrs, outs, numel, types, len(grads), float(max_norm), _ptr(norm), _ptr(ws),
+        ws.numel() * ws.element_size(), _stream(stream, like)))
+    return norm
+
+
 def moe_device_errors() -> int:
     """Reads and clears the kernels' device error bits (synchronous): bit 0
     dispatch wait timeout, bit 1 dispatch row index out of range, bit 2
-    combine row index out of range."""
-    import ctypes
+    combine row index out of range, bit 4 expert product wait timeout, bit 5
+    expert product bucket out of range."""
     v = ctypes.c_uint32(0)
     _abi.check("moe_device_errors", lib().moe_device_errors(ctypes.byref(v)))
     return int(v.value)

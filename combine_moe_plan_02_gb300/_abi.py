@@ -41,6 +41,14 @@ SIGNATURES = {
     "moe_plan_dispatch_fused_max": (I64, []),
     "moe_plan_dispatch": (I32, [P, P, I64, I64, I32, I32, I32, P, I64, P, P, P, P, P, P, I64, P,
                                 P, SZ, P]),
+    "moe_combine_backward": (I32, [P, I32, P, I64, I32, P, P, P, P, I64, I64, I32, I32, P, P,
+                                   P]),
+    "moe_expert_gemm": (I32, [P, I64, P, I64, I64, I32, P, P, P, I32, P]),
+    "moe_expert_gemm_dgrad": (I32, [P, I64, P, I64, I64, I32, P, P, P, I32, P]),
+    "moe_expert_gemm_wgrad": (I32, [P, P, I64, I64, I64, I32, P, P, P, I32, P]),
+    "moe_grad_norm_workspace_size": (SZ, []),
+    "moe_grad_norm": (I32, [P, P, P, I32, P, P, SZ, P]),
+    "moe_clip_grad_norm": (I32, [P, P, P, P, I32, ctypes.c_float, P, P, SZ, P]),
     "moe_device_errors": (I32, [P]),
     "moe_selftest_wait_timeout": (I32, [I64, P]),
     "moe_selftest_convert": (I32, [ctypes.c_uint32, I64, P, P, P]),

@@ -77,10 +77,14 @@ enum : uint32_t {
     kErrDispatchIndex = 2u,    // dispatch met a row index outside its buffers
     kErrCombineIndex = 4u,     // combine met a row index outside its buffers
     kErrCombineTimeout = 8u,   // a bounded wait for staged rows in combine ran out of time
+    kErrExpertTimeout = 16u,   // a bounded wait in an expert product ran out of time
+    kErrExpertBucket = 32u,    // an expert product met a bucket outside its rows
 };
 cudaError_t read_dispatch_errors(uint32_t *flags);
 cudaError_t read_combine_errors(uint32_t *flags);
 cudaError_t read_plan_dispatch_errors(uint32_t *flags);
+cudaError_t read_backward_errors(uint32_t *flags);
+cudaError_t read_expert_errors(uint32_t *flags);
 
 // moe_dispatch's body; early_src: the source rows were complete before the
 // previous kernel of the stream started waiting (see CopyArgs::early_src).
@@ -304,6 +308,38 @@ __device__ __forceinline__ void st16(void *p, uint4 v)
     asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y),
                  "r"(v.z), "r"(v.w)
                  : "memory");
+}
+
+// Clears the rows that hold no entry: from cnt[e] filled rows to the end of
+// each bucket, and from off[E] to `rows`.  Called by whole warps; warp gw of W
+// takes every W-th such row.  Bounds are clamped to the buffer.
+__device__ __forceinline__ void zero_gaps(uint8_t *base, int64_t row_bytes, int64_t rows,
+                                          const int32_t *cnt, const int64_t *off, int E, int gw,
+                                          int W)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t seen = 0;
+    for (int e0 = 0; e0 <= E; e0 += 32) {
+        const int e = e0 + lane;
+        int64_t first = 0, n = 0;
+        if (e <= E) {
+            const int64_t b = __ldg(off + e);
+            first = e < E ? b + max(__ldg(cnt + e), 0) : b;
+            first = min(max(first, (int64_t)0), rows);
+            const int64_t end = e < E ? min(__ldg(off + e + 1), rows) : rows;
+            n = max(end - first, (int64_t)0);
+        }
+        for (unsigned m = __ballot_sync(0xffffffffu, n > 0); m; m &= m - 1) {
+            const int64_t f = __shfl_sync(0xffffffffu, first, __ffs(m) - 1);
+            const int64_t c = __shfl_sync(0xffffffffu, n, __ffs(m) - 1);
+            for (int64_t i = (gw - seen % W + W) % W; i < c; i += W) {
+                uint8_t *row = base + (f + i) * row_bytes;
+                for (int64_t o = lane * 16; o < row_bytes; o += 512)
+                    st16(row + o, make_uint4(0, 0, 0, 0));
+            }
+            seen += c;
+        }
+    }
 }
 
 } // namespace moe

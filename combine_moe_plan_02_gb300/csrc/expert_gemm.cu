@@ -1,0 +1,614 @@
+// The experts' products over packed rows, and their gradients.
+//
+// Bucket e is the rows off[e] .. off[e] + cnt[e] of a plan.  With w [E, N, D]:
+//   forward   y[r, n]    = sum_d x[r, d] * w[e, n, d]          r in bucket e
+//   rows'     dx[r, d]   = sum_n dy[r, n] * w[e, n, d]
+//   weights'  dw[e, n, d] = sum_{r in e} dy[r, n] * x[r, d]
+// bf16 operands, f32 sums (tensor memory), one rounding to the output's type.
+//
+// One tcgen05 kernel does all three.  The M side of the matrix instruction
+// (128 TMEM lanes) is always the dimension that is contiguous in the output:
+// weight rows n (forward), d (the gradients).  The N side (up to 256 TMEM
+// columns) is the tokens of one bucket, or the rows n of dw.  A bucket of c
+// tokens is cut into ceil(c / 256) equal parts rounded up to 16 columns, so a
+// ragged bucket costs at most 15 idle columns a part and one token costs 16
+// columns instead of a padded tile of rows.  Rows of other buckets that a
+// copied box holds land in columns that are never stored; columns are
+// independent, so nothing they hold (NaN included) matters.  The weights'
+// gradient reduces over the tokens: there the rows past the bucket's end are
+// cleared in shared memory before the matrix instruction reads them.
+//
+// A CTA is persistent (one per SM) and walks the tiles of all buckets, which
+// it lists itself from cnt and off: the sizes stay on the device.  Warp 0
+// copies operand blocks of 64 along the reduction with TMA into a ring of
+// stages, warp 1 issues the matrix instructions, warps 2 and 3 clear the rows
+// of the output that belong to no bucket, warps 4 to 7 store.  Two
+// accumulators of 256 columns let the stores of a tile overlap the next
+// tile's products.  Every wait is bounded.
+
+#include "common.cuh"
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kM = 128;             // TMEM lanes: outputs along the contiguous dimension
+constexpr int kN = 256;             // TMEM columns of one accumulator
+constexpr int kK = 64;              // reduction block: 128 bytes of bf16
+constexpr int kStages = 4;
+constexpr int kABytes = kM * kK * 2;
+constexpr int kBBytes = kN * kK * 2;
+constexpr int kStageBytes = kABytes + kBBytes;
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
+
+__device__ uint32_t g_expert_error;  // kErrExpertTimeout | kErrExpertBucket
+
+enum Mode { kForward = 0, kRowGrad = 1, kWeightGrad = 2 };
+
+struct ExpertArgs {
+    const int32_t *cnt;   // [E]
+    const int64_t *off;   // [E + 1]
+    int64_t rows;
+    int E;
+    int M;                // contiguous output dimension
+    int N;                // rows of a weight (weights' gradient)
+    int K;                // reduction length (the other two)
+    uint8_t *out;
+};
+
+// --- tcgen05 ---------------------------------------------------------------
+
+__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(slot)),
+                 "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+}
+
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+// Arrives on `bar` when the matrix instructions issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_u32(bar))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// 32 columns of this warp's 32 lanes: thread = lane, register = column.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle.  Rows along the
+// reduction (K-major): 8 rows of 128 bytes are 1024 bytes, the next 8 follow.
+// Across it (MN-major): 64 outputs are one 128-byte row, 8 reduction steps are
+// 1024 bytes and the next 64 outputs start kK rows (8192 bytes) further on.
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn_major)
+{
+    const uint64_t lead = mn_major ? (kK * 128) >> 4 : 1;
+    return ((uint64_t)(addr & 0x3ffff) >> 4) | (lead << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: f32 accumulator, bf16 operands.
+__device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+           ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
+}
+
+// --- TMA -------------------------------------------------------------------
+
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                       int y)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                       int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// --- bounded waits -----------------------------------------------------------
+
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Waits for phase `parity`; false once the limit ran out here or, with
+// `stop`, in another warp of the CTA.
+__device__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
+{
+    const uint64_t t0 = now_ns();
+    for (;;) {
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if ((stop && *stop) || now_ns() - t0 > kWaitLimitNs) return false;
+    }
+}
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *stop)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    if (wait_slow(bar, parity, stop)) return true;
+    *stop = 1;
+    return false;
+}
+
+// --- tiles -------------------------------------------------------------------
+
+struct Tile {
+    int e, m0;
+    int n0;       // first column: a row of the packed rows, or a row of dw[e]
+    int n;        // columns that are stored
+    int blocks;   // reduction blocks
+    int last;     // reduction length of the last block (1..64)
+    int row;      // first row of the bucket (weights' gradient)
+};
+
+__host__ __device__ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// The tiles of all buckets, in shared memory.
+struct Schedule {
+    int *start;   // [E + 1] first tile of each bucket
+    int *first;   // [E] first row
+    int *fill;    // [E] rows
+    int cursor;   // bucket of the last tile asked for; tiles are asked for in order
+};
+
+template <int MODE>
+__device__ __forceinline__ int bucket_tiles(const ExpertArgs &a, int fill)
+{
+    const int mt = ceil_div(a.M, kM);
+    return MODE == kWeightGrad ? mt * ceil_div(a.N, kN) : mt * ceil_div(fill, kN);
+}
+
+template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a, Schedule &s, int t)
+{
+    while (t >= s.start[s.cursor + 1]) ++s.cursor;
+    Tile r;
+    r.e = s.cursor;
+    const int local = t - s.start[r.e], fill = s.fill[r.e];
+    r.row = s.first[r.e];
+    if (MODE == kWeightGrad) {
+        const int mt = ceil_div(a.M, kM);
+        r.m0 = local % mt * kM;
+        r.n0 = local / mt * kN;
+        r.n = min(kN, a.N - r.n0);
+        r.blocks = ceil_div(fill, kK);
+        r.last = fill - (r.blocks - 1) * kK;
+    } else {
+        const int parts = ceil_div(fill, kN);
+        const int per = ceil_div(ceil_div(fill, parts), 16) * 16;
+        const int i = local % parts;
+        r.m0 = local / parts * kM;
+        r.n0 = r.row + i * per;
+        r.n = min(per, fill - i * per);
+        r.blocks = ceil_div(a.K, kK);
+        r.last = a.K - (r.blocks - 1) * kK;
+    }
+    return r;
+}
+
+// Lists the tiles: every thread of the CTA takes part.
+template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Schedule &s)
+{
+    __shared__ int s_warp[kThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += kThreads) {
+        const int e = e0 + tid;
+        int tiles = 0;
+        if (e < a.E) {
+            int64_t f = __ldg(a.off + e), c = __ldg(a.cnt + e);
+            if (f < 0 || c < 0 || f + c > a.rows) {
+                // never outside the rows: the bucket is left out and reported
+                atomicOr(&g_expert_error, kErrExpertBucket);
+                f = c = 0;
+            }
+            s.first[e] = (int)f;
+            s.fill[e] = (int)c;
+            tiles = bucket_tiles<MODE>(a, (int)c);
+        }
+        int sum = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) s_warp[warp] = sum;
+        __syncthreads();
+        int before = base, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += s_warp[w];
+            total += s_warp[w];
+        }
+        if (e < a.E) s.start[e + 1] = before + sum;
+        base += total;
+        __syncthreads();
+    }
+    if (tid == 0) s.start[0] = 0;
+    __syncthreads();
+}
+
+// --- the kernel ----------------------------------------------------------------
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    volatile int stop;
+};
+
+template <int MODE, typename Tout>
+__global__ void __launch_bounds__(kThreads, 1)
+expert_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+              const __grid_constant__ CUtensorMap map_b16, ExpertArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    int *lists = reinterpret_cast<int *>(ring + kStages * kStageBytes);
+    Schedule sched = {lists, lists + a.E + 1, lists + 2 * a.E + 1, 0};
+    __shared__ Shared sh;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(&sh.tmem, 2 * kN);
+    griddep_wait();  // the plan and the operands come from earlier stream work
+    griddep_launch_dependents();
+    build_schedule<MODE>(a, sched);  // ends with a CTA barrier
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int tiles = sched.start[a.E];
+    constexpr bool kAMn = MODE != kForward, kBMn = MODE == kWeightGrad;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int64_t j = 0;  // blocks copied
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile c = tile_of<MODE>(a, sched, t);
+                const int n16 = ceil_div(c.n, 16) * 16;
+                const int wide = MODE == kWeightGrad ? ceil_div(n16, 64) : n16 / 64;
+                const int narrow = MODE == kWeightGrad ? 0 : n16 % 64 / 16;
+                const uint32_t bytes = kABytes + wide * 8192 + narrow * 2048;
+                for (int b = 0; b < c.blocks; ++b, ++j) {
+                    const int st = (int)(j % kStages);
+                    if (j >= kStages &&
+                        !wait(&sh.empty[st], (uint32_t)(j / kStages - 1) & 1, &sh.stop)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = ring + st * kStageBytes, *sb = sa + kABytes;
+                    uint64_t *bar = &sh.full[st];
+                    mbar_arrive_expect_tx(bar, bytes);
+                    const int k = b * kK;
+                    if (MODE == kForward) {
+                        tma_3d(sa, &map_a, bar, k, c.m0, c.e);
+                    } else if (MODE == kRowGrad) {
+                        tma_3d(sa, &map_a, bar, c.m0, k, c.e);
+                        tma_3d(sa + 8192, &map_a, bar, c.m0 + 64, k, c.e);
+                    } else {
+                        tma_2d(sa, &map_a, bar, c.m0, c.row + k);
+                        tma_2d(sa + 8192, &map_a, bar, c.m0 + 64, c.row + k);
+                    }
+                    for (int i = 0; i < wide; ++i) {
+                        if (MODE == kWeightGrad)
+                            tma_2d(sb + i * 8192, &map_b, bar, c.n0 + i * 64, c.row + k);
+                        else
+                            tma_2d(sb + i * 8192, &map_b, bar, k, c.n0 + i * 64);
+                    }
+                    for (int i = 0; i < narrow; ++i)
+                        tma_2d(sb + wide * 8192 + i * 2048, &map_b16, bar, k,
+                               c.n0 + wide * 64 + i * 16);
+                }
+            }
+            if (!ok) {  // leave no copy in flight
+                for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
+                    (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
+            }
+        }
+    } else if (warp == 1) {
+        int64_t j = 0;
+        int i = 0;  // tiles done
+        bool ok = true;
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+            const Tile c = tile_of<MODE>(a, sched, t);
+            const int buf = i & 1;
+            if (i >= 2 && !wait(&sh.acc_empty[buf], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) break;
+            tc_fence_after();
+            const int n16 = ceil_div(c.n, 16) * 16;
+            const uint32_t idesc = instr_desc(n16, kAMn, kBMn);
+            for (int b = 0; b < c.blocks; ++b, ++j) {
+                const int st = (int)(j % kStages);
+                if (!wait(&sh.full[st], (uint32_t)(j / kStages) & 1, &sh.stop)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *sa = ring + st * kStageBytes;
+                const int len = b + 1 == c.blocks ? c.last : kK;
+                const int steps = ceil_div(len, 16);
+                if (MODE == kWeightGrad && len % 16) {
+                    // rows past the bucket's end: 128 bytes of each box of 64
+                    const int boxes = 2 + ceil_div(n16, 64);
+                    const int quads = (steps * 16 - len) * 8;
+                    for (int x = lane; x < boxes * quads; x += 32)
+                        *reinterpret_cast<uint4 *>(sa + x / quads * 8192 + len * 128 +
+                                                   x % quads * 16) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t da = operand_desc(smem_u32(sa), kAMn);
+                    const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
+                    for (int s = 0; s < steps; ++s)
+                        mma_bf16(tmem + buf * kN, da + s * (kAMn ? 128 : 2),
+                                 db + s * (kBMn ? 128 : 2), idesc, b > 0 || s > 0);
+                    mma_commit(&sh.empty[st]);
+                }
+                __syncwarp();
+            }
+            if (ok && lane == 0) mma_commit(&sh.acc_full[buf]);
+            __syncwarp();
+        }
+        if (lane == 0) mma_commit(&sh.drain);  // nothing is issued after this
+        __syncwarp();
+        (void)wait_slow(&sh.drain, 0, nullptr);
+    } else if (warp < 4) {
+        if (MODE != kWeightGrad)
+            zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
+                      blockIdx.x * 2 + warp - 2, gridDim.x * 2);
+    } else {
+        const int q = warp & 3;
+        int i = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+            const Tile c = tile_of<MODE>(a, sched, t);
+            const int buf = i & 1;
+            if (!wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)) break;
+            tc_fence_after();
+            const int m = c.m0 + q * 32 + lane;
+            const int64_t first = MODE == kWeightGrad ? (int64_t)c.e * a.N + c.n0 : c.n0;
+            Tout *out = reinterpret_cast<Tout *>(a.out) + first * a.M + m;
+            for (int n = 0; n < c.n; n += 32) {
+                uint32_t r[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kN + n, r);
+                if (m < a.M) {
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        if (n + x >= c.n) break;
+                        // a bucket without rows: no product was issued
+                        const float f = c.blocks ? __uint_as_float(r[x]) : 0.0f;
+                        if (sizeof(Tout) == 2)
+                            reinterpret_cast<__nv_bfloat16 *>(out)[(int64_t)(n + x) * a.M] =
+                                __float2bfloat16_rn(f);
+                        else
+                            reinterpret_cast<float *>(out)[(int64_t)(n + x) * a.M] = f;
+                    }
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && sh.stop) atomicOr(&g_expert_error, kErrExpertTimeout);
+    if (warp == 1) tmem_free(tmem, 2 * kN);
+}
+
+// --- host ----------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult got = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &got) != cudaSuccess ||
+            got != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// A map over bf16 [depth, rows, width] (2-D when depth is 0), boxes of
+// 64 x box_rows with the 128-byte swizzle; what lies outside reads as zero.
+cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t rows,
+                     int64_t depth, int box_rows)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)depth};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * rows * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth ? 3 : 2,
+                          const_cast<void *>(base), dims, strides, box, step,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int MODE, typename Tout>
+int launch_expert(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mb16,
+                  const ExpertArgs &a, int grid, cudaStream_t stream)
+{
+    static KernelCache kc;
+    const size_t smem = 1024 + kStages * kStageBytes + (3 * (size_t)a.E + 1) * sizeof(int);
+    cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout>, smem, kThreads, kc, nullptr);
+    if (e == cudaSuccess)
+        e = launch_pdl(expert_kernel<MODE, Tout>, dim3(grid), dim3(kThreads), smem, stream, ma, mb,
+                       mb16, a);
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    return check_launch();
+}
+
+// ra: the rows that the reduction or the columns come from; rb: the other
+// rows (weights' gradient) or the weights.
+template <int MODE>
+int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, int64_t D, int E,
+               const int32_t *cnt, const int64_t *off, void *out, int out_dtype,
+               cudaStream_t stream)
+{
+    if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_EINVAL;
+    if (rows < 0 || rows >= ((int64_t)1 << 31) || E < 1 || E > 1024) return MOE_EINVAL;
+    if (N < 1 || D < 1 || N >= (1 << 24) || D >= (1 << 24)) return MOE_EINVAL;
+    if (!cnt || !off || !out || (rows > 0 && (!rows_a || !other))) return MOE_EINVAL;
+    if (MODE != kWeightGrad && !other) return MOE_EINVAL;
+    const int64_t M = MODE == kForward ? N : D;
+    const int64_t mt = (M + kM - 1) / kM;
+    const int64_t most = MODE == kWeightGrad ? mt * ((N + kN - 1) / kN) * E
+                                             : mt * (rows / kN + (rows < E ? rows : E));
+    if (most >= ((int64_t)1 << 31)) return MOE_EINVAL;
+    if (N % 8 || D % 8 || !aligned16(rows_a) || !aligned16(other) || !aligned16(out))
+        return MOE_EALIGN;
+    if (MODE != kWeightGrad && rows == 0) return MOE_OK;
+    ExpertArgs a = {};
+    a.cnt = cnt;
+    a.off = off;
+    a.rows = rows;
+    a.E = E;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)(MODE == kForward ? D : N);
+    a.out = static_cast<uint8_t *>(out);
+    CUtensorMap ma = {}, mb = {}, mb16 = {};
+    cudaError_t e = cudaSuccess;
+    if (MODE == kWeightGrad) {
+        // without rows there is nothing to copy, and no address to describe
+        if (rows > 0) e = make_map(&ma, other, D, rows, 0, 64);
+        if (rows > 0 && e == cudaSuccess) e = make_map(&mb, rows_a, N, rows, 0, 64);
+    } else {
+        e = make_map(&ma, other, D, N, E, MODE == kForward ? kM : 64);
+        if (e == cudaSuccess) e = make_map(&mb, rows_a, a.K, rows, 0, 64);
+        if (e == cudaSuccess) e = make_map(&mb16, rows_a, a.K, rows, 0, 16);
+    }
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    const int sms = sm_count();
+    const int grid = (int)(most < sms ? most : sms);
+    return out_dtype == MOE_BF16
+               ? launch_expert<MODE, __nv_bfloat16>(ma, mb, mb16, a, grid, stream)
+               : launch_expert<MODE, float>(ma, mb, mb16, a, grid, stream);
+}
+
+} // namespace
+} // namespace moe
+
+using namespace moe;
+
+MOE_EXPORT int moe_expert_gemm(const void *x, int64_t rows, const void *w, int64_t N, int64_t D,
+                               int E, const int32_t *cnt, const int64_t *off, void *y,
+                               int y_dtype, moe_stream_t stream)
+{
+    MOE_TRACE("moe_expert_gemm");
+    return run_expert<kForward>(x, w, rows, N, D, E, cnt, off, y, y_dtype, (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_expert_gemm_dgrad(const void *dy, int64_t rows, const void *w, int64_t N,
+                                     int64_t D, int E, const int32_t *cnt, const int64_t *off,
+                                     void *dx, int dx_dtype, moe_stream_t stream)
+{
+    MOE_TRACE("moe_expert_gemm_dgrad");
+    return run_expert<kRowGrad>(dy, w, rows, N, D, E, cnt, off, dx, dx_dtype,
+                                (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N,
+                                     int64_t D, int E, const int32_t *cnt, const int64_t *off,
+                                     void *dw, int dw_dtype, moe_stream_t stream)
+{
+    MOE_TRACE("moe_expert_gemm_wgrad");
+    return run_expert<kWeightGrad>(dy, x, rows, N, D, E, cnt, off, dw, dw_dtype,
+                                   (cudaStream_t)stream);
+}
+
+namespace moe {
+// Reads and clears this file's device error bits.
+cudaError_t read_expert_errors(uint32_t *flags)
+{
+    uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_expert_error, sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_expert_error, &zero, sizeof(uint32_t));
+    return e;
+}
+} // namespace moe

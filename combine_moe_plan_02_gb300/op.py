@@ -33,6 +33,10 @@ combined_wts[s,i] is the sum of topk_w[s,i] over the token's valid copies
 (the weight fold).  In dedup mode the weights are applied inside each group
 row and the group rows are summed unweighted; the fold there takes a second
 pass over the group rows.
+
+Training: combine_backward and dispatch_backward are the gradients of the two
+calls, from the same handle, in every mode (the quantising dispatch passes
+gradients straight through).
 """
 from __future__ import annotations
 
@@ -40,8 +44,8 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (GroupPlan, moe_combine_dedup, moe_combine_fold, moe_dispatch,
-               moe_dispatch_dedup, moe_dispatch_quant_fp8, moe_group_plan, moe_plan,
+from . import (GroupPlan, moe_combine_backward, moe_combine_dedup, moe_combine_fold,
+               moe_dispatch, moe_dispatch_backward, moe_dispatch_dedup, moe_dispatch_quant_fp8, moe_group_plan, moe_plan,
                moe_plan_capacity, moe_plan_dispatch)
 
 __all__ = ["MoeOp", "Routing"]
@@ -147,3 +151,18 @@ class MoeOp:
         return moe_combine_fold(y, routing.topk_w, routing.plan.tok_map,
                                 weighted=self.weighted, fold=self.fold,
                                 out_dtype=self.out_dtype, stream=stream)
+
+    def combine_backward(self, dout: torch.Tensor, y: torch.Tensor, routing: Routing, *,
+                         stream=None):
+        """Gradient of combine's sum: (dy in y's type, dw f32 [S, K]); dw is
+        None for an unweighted op."""
+        weighted = self.weighted or routing.group is not None
+        w = routing.topk_w if weighted else torch.ones_like(routing.topk_w)
+        dy, dw = moe_combine_backward(dout, y, w, routing.plan, stream=stream)
+        return dy, dw if weighted else None
+
+    def dispatch_backward(self, dpacked: torch.Tensor, routing: Routing, *,
+                          out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
+        """Gradient of dispatch: the sum of the gradients of a token's packed
+        rows, [S, H]."""
+        return moe_dispatch_backward(dpacked, routing.plan, out_dtype=out_dtype, stream=stream)

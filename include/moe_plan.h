@@ -12,7 +12,12 @@
  *                 of the forwarded weight vectors)
  * with a dedup variant (moe_group_plan, moe_dispatch_dedup,
  * moe_combine_dedup) that sends each token once per virtual expert group and
- * expands per expert from there.
+ * expands per expert from there.  Around that step:
+ *   moe_expert_gemm        the experts' product over packed rows
+ *   moe_expert_gemm_dgrad, moe_expert_gemm_wgrad   its gradients
+ *   moe_combine_backward   the gradient of the combine (the dispatch's is
+ *                          moe_combine_fold, unweighted, over the same map)
+ *   moe_grad_norm, moe_clip_grad_norm   the global norm over many gradients
  *
  * Sources (page title and the note on it):
  *   ROCm/mori "Draft: cco + flydsl dispatch/combine #448": PR description
@@ -90,10 +95,14 @@ int moe_last_cuda_error(void);
  *   bit 1  dispatch (moe_dispatch*, moe_plan_dispatch): a map entry pointed
  *          outside the source or destination buffer (that row was not
  *          copied)
- *   bit 2  combine: a map entry pointed outside y, or a group row's source
+ *   bit 2  combine and its gradient: a map entry pointed outside y, or a group row's source
  *          entry outside topk_w (that term was dropped)
  *   bit 3  reserved for a combine that waits on staged rows; the combine
  *          kernels of this version never wait and never set it
+ *   bit 4  expert products: a bounded wait ran out of time (the kernel stopped
+ *          early; its output is incomplete)
+ *   bit 5  expert products: a bucket of the plan lies outside the rows (that
+ *          bucket was left out)
  * flags: HOST pointer to one uint32.  Synchronous: waits for the device. */
 int moe_device_errors(uint32_t *flags);
 
@@ -410,6 +419,83 @@ int moe_combine_dedup(const void *y, int64_t y_rows, int in_dtype, const float *
 int moe_combine_fold(const void *y, int64_t y_rows, int in_dtype, const float *topk_w,
                      int weighted, const int64_t *map, int64_t S, int64_t H, int K,
                      void *out, int out_dtype, float *out_weights, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Gradient of the weighted combine.  With dout the gradient of
+ * out[s] = sum_k topk_w[s,k] * y[tok_map[s,k]]:
+ *   dy[tok_map[s,k], j] = round_y( topk_w[s,k] * dout[s, j] )
+ *   dw[s, k] = sum_j dout[s, j] * y[tok_map[s,k], j]   (f32; 0 where
+ *              tok_map[s,k] < 0)
+ *   dy[r, :] = 0 on rows that no entry fills: from off[e] + cnt[e] to
+ *              off[e + 1] in every bucket, and from off[E] to y_rows
+ * (The gradient of moe_dispatch, dx[s] = sum_k dpacked[tok_map[s,k]], is
+ * moe_combine_fold with weighted = 0 over the same map.)
+ *
+ * dout     [S, H] of dout_dtype; y, dy [y_rows, H] of y_dtype (each MOE_BF16
+ *          or MOE_F32); rows of y that no entry fills are not read
+ * cnt, off, tok_map  from moe_plan or moe_plan_capacity; an entry outside
+ *          [-1, y_rows) drops its terms and is flagged (bit 2)
+ * dw       f32 [S, K].  The sum's order is fixed: results are reproducible.
+ * S = 0 clears the unfilled rows of dy.  1 <= y_rows < 2^31, S*K < 2^31.
+ * Alignment: dout, y, dy 16-byte aligned; H a multiple of 8.
+ * ---------------------------------------------------------------------- */
+int moe_combine_backward(const void *dout, int dout_dtype, const void *y, int64_t y_rows,
+                         int y_dtype, const float *topk_w, const int64_t *tok_map,
+                         const int32_t *cnt, const int64_t *off, int64_t S, int64_t H, int K,
+                         int E, void *dy, float *dw, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' products over packed rows.  Bucket e is the rows off[e] ..
+ * off[e] + cnt[e] of a plan (moe_plan or moe_plan_capacity):
+ *   moe_expert_gemm        y[r, n]     = sum_d x[r, d]  * w[e, n, d]
+ *   moe_expert_gemm_dgrad  dx[r, d]    = sum_n dy[r, n] * w[e, n, d]
+ *   moe_expert_gemm_wgrad  dw[e, n, d] = sum_{r in bucket e} dy[r, n] * x[r, d]
+ * bf16 operands, f32 sums, rounded once to the output's type (MOE_BF16 or
+ * MOE_F32).  Output rows in no bucket are zero; dw[e] of an empty bucket is
+ * zero.  Rows in no bucket and experts without rows are never used, whatever
+ * they hold.  A bucket outside [0, rows) is left out and flagged (bit 5).
+ *
+ * x [rows, D], dy [rows, N] bf16; w bf16 [E, N, D]; y [rows, N], dx [rows, D],
+ * dw [E, N, D] of the given output type.  cnt and off are read on the device:
+ * the host never needs the bucket sizes.  0 <= rows < 2^31, N, D < 2^24.
+ * Alignment: all row pointers 16-byte aligned; N and D multiples of 8.
+ * ---------------------------------------------------------------------- */
+int moe_expert_gemm(const void *x, int64_t rows, const void *w, int64_t N, int64_t D, int E,
+                    const int32_t *cnt, const int64_t *off, void *y, int y_dtype,
+                    moe_stream_t stream);
+int moe_expert_gemm_dgrad(const void *dy, int64_t rows, const void *w, int64_t N, int64_t D,
+                          int E, const int32_t *cnt, const int64_t *off, void *dx, int dx_dtype,
+                          moe_stream_t stream);
+int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N, int64_t D,
+                          int E, const int32_t *cnt, const int64_t *off, void *dw, int dw_dtype,
+                          moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Global L2 norm over many gradients, and clipping to a limit:
+ *   norm[0] = sqrt(sum over all tensors of g^2)
+ *   out[i]  = min(1, max_norm / (norm + 1e-6)) * grads[i], rounded once
+ * Squares are summed in f32 within a thread and f64 across threads, in a
+ * fixed order.  An infinite norm scales by 0 (an infinity becomes NaN); a NaN
+ * anywhere makes every output NaN; the host sees neither without reading norm.
+ *
+ * grads, out  HOST arrays of n DEVICE pointers (copied before the call
+ *             returns); out[i] may be grads[i], and may not overlap any other
+ *             tensor.  numel, dtype: HOST arrays, MOE_BF16 or MOE_F32; out has
+ *             the types of grads.  Any alignment of the element type;
+ *             pointers are ignored where numel is 0.
+ * norm        f32 [1] device, written
+ * workspace   moe_grad_norm_workspace_size() bytes, 256-byte aligned, dead
+ *             after the call
+ * max_norm    >= 0 (infinity: nothing is scaled).  n <= MOE_GRAD_TENSORS_MAX.
+ * ---------------------------------------------------------------------- */
+#define MOE_GRAD_TENSORS_MAX 65536
+
+size_t moe_grad_norm_workspace_size(void);
+int moe_grad_norm(const void *const *grads, const int64_t *numel, const int *dtype, int n,
+                  float *norm, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+int moe_clip_grad_norm(const void *const *grads, void *const *out, const int64_t *numel,
+                       const int *dtype, int n, float max_norm, float *norm, void *workspace,
+                       size_t workspace_bytes, moe_stream_t stream);
 
 #ifdef __cplusplus
 }
