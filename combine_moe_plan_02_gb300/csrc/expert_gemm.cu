@@ -7,24 +7,31 @@
 // bf16 operands, f32 sums (tensor memory), one rounding to the output's type.
 //
 // One tcgen05 kernel does all three.  The M side of the matrix instruction
-// (128 TMEM lanes) is always the dimension that is contiguous in the output:
-// weight rows n (forward), d (the gradients).  The N side (up to 256 TMEM
-// columns) is the tokens of one bucket, or the rows n of dw.  A bucket of c
-// tokens is cut into ceil(c / 256) equal parts rounded up to 16 columns, so a
-// ragged bucket costs at most 15 idle columns a part and one token costs 16
-// columns instead of a padded tile of rows.  Rows of other buckets that a
-// copied box holds land in columns that are never stored; columns are
-// independent, so nothing they hold (NaN included) matters.  The weights'
-// gradient reduces over the tokens: there the rows past the bucket's end are
-// cleared in shared memory before the matrix instruction reads them.
+// (256 TMEM lanes of a pair of CTAs) is always the dimension that is
+// contiguous in the output: weight rows n (forward), d (the gradients).  The N
+// side (up to 256 TMEM columns) is the tokens of one bucket, or the rows n of
+// dw.  A bucket of c tokens is cut into ceil(c / 256) equal parts rounded up to
+// 32 columns, so a ragged bucket costs at most 31 idle columns a part and one
+// token costs 32 columns instead of a padded tile of rows.  Rows of other
+// buckets that a copied box holds land in columns that are never stored;
+// columns are independent, so nothing they hold (NaN included) matters.  The
+// weights' gradient reduces over the tokens: there the rows past the bucket's
+// end are cleared in shared memory before the matrix instruction reads them.
 //
-// A CTA is persistent (one per SM) and walks the tiles of all buckets, which
-// it lists itself from cnt and off: the sizes stay on the device.  Warp 0
-// copies operand blocks of 64 along the reduction with TMA into a ring of
-// stages, warp 1 issues the matrix instructions, warps 2 and 3 clear the rows
-// of the output that belong to no bucket, warps 4 to 7 store.  Two
-// accumulators of 256 columns let the stores of a tile overlap the next
-// tile's products.  Every wait is bounded.
+// Two CTAs on neighbouring SMs work on one tile of 256 x 256 (cta_group::2):
+// each holds its 128 lanes of the M side and half of the N side in shared
+// memory, so a pair reads 64 KB per block of 64 along the reduction where two
+// single CTAs of 128 x 256 read 96 KB.
+//
+// A pair is persistent (one per two SMs) and walks the tiles of all buckets,
+// which it lists itself from cnt and off: the sizes stay on the device.  Warps
+// 0 and 2 copy the operands' blocks of 64 along the reduction with TMA into a
+// ring of stages (one warp each: issuing a copy takes 60 to 100 cycles and a
+// wait and an arrival as much again, against 512 cycles of products a block),
+// warp 1 of the first CTA issues the matrix instructions, warp 3 clears the
+// rows of the output that belong to no bucket, warps 4 to 7 store.  Two
+// accumulators of 256 columns let the stores of a tile overlap the next tile's
+// products.  Every wait is bounded.
 
 #include "common.cuh"
 
@@ -35,12 +42,14 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kM = 128;             // TMEM lanes: outputs along the contiguous dimension
+constexpr int kLanes = 128;         // TMEM lanes of a CTA: outputs along the contiguous dimension
+constexpr int kM = 2 * kLanes;      // of the pair
 constexpr int kN = 256;             // TMEM columns of one accumulator
 constexpr int kK = 64;              // reduction block: 128 bytes of bf16
-constexpr int kStages = 4;
-constexpr int kABytes = kM * kK * 2;
-constexpr int kBBytes = kN * kK * 2;
+constexpr int kStep = 32;           // columns come in these steps, half of them from each CTA
+constexpr int kStages = 6;
+constexpr int kABytes = kLanes * kK * 2;
+constexpr int kBBytes = kN / 2 * kK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
 
@@ -63,16 +72,16 @@ struct ExpertArgs {
 
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols)
 {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(slot)),
                  "r"(cols)
                  : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
 }
 
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
 {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
 }
 
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -81,17 +90,19 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
 }
 
-// Arrives on `bar` when the matrix instructions issued so far are done.
+// Arrives on `bar` of both CTAs when the matrix instructions issued so far are
+// done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
     asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-            smem_u32(bar))
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
         : "memory");
 }
 
@@ -138,25 +149,81 @@ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn)
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
 }
 
-// --- TMA -------------------------------------------------------------------
+// --- the pair ----------------------------------------------------------------
 
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(p));
+    return p != 0;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// The address of a shared variable in the first CTA of the pair.
+__device__ __forceinline__ uint32_t leader_addr(const void *p)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+                 "barrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+// Arrivals at a barrier of either CTA.  Those that only hand over tensor
+// memory or a copy's byte count order nothing (the copy and the tcgen05 fences
+// do); the one behind cleared shared memory releases it.  A release at
+// cluster scope on every block costs about 0.4 us of it: 1745 against 885 us.
+__device__ __forceinline__ void arrive_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void arrive_release_at(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
+                     bar),
+                 "r"(bytes)
+                 : "memory");
+}
+
+// TMA copies into this CTA; `bar` may be either CTA's barrier.
+__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, uint32_t bar, int x,
                                        int y)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y)
         : "memory");
 }
 
-__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, uint32_t bar, int x,
                                        int y, int z)
 {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
+        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
 }
 
@@ -171,13 +238,17 @@ __device__ __forceinline__ uint64_t now_ns()
 
 // Waits for phase `parity`; false once the limit ran out here or, with
 // `stop`, in another warp of the CTA.
-__device__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
 {
-    const uint64_t t0 = now_ns();
+    // reading the timer costs about as much as a block of products: probe
+    // first
+    uint64_t t0 = 0;
     for (;;) {
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < 256; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-        if ((stop && *stop) || now_ns() - t0 > kWaitLimitNs) return false;
+        const uint64_t t = now_ns();
+        if (t0 == 0) t0 = t;
+        if ((stop && *stop) || t - t0 > kWaitLimitNs) return false;
     }
 }
 
@@ -188,6 +259,19 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     *stop = 1;
     return false;
 }
+
+// A place in the ring and the parity of its current round.
+struct Ring {
+    int at = 0;
+    uint32_t round = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == kStages) {
+            at = 0;
+            round ^= 1;
+        }
+    }
+};
 
 // --- tiles -------------------------------------------------------------------
 
@@ -233,7 +317,7 @@ template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a,
         r.last = fill - (r.blocks - 1) * kK;
     } else {
         const int parts = ceil_div(fill, kN);
-        const int per = ceil_div(ceil_div(fill, parts), 16) * 16;
+        const int per = ceil_div(ceil_div(fill, parts), kStep) * kStep;
         const int i = local % parts;
         r.m0 = local / parts * kM;
         r.n0 = r.row + i * per;
@@ -287,17 +371,35 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Sc
 
 // --- the kernel ----------------------------------------------------------------
 
+// Operand maps: the M side's, and the N side's with boxes of 16, 32, 64 and 128
+// rows (weights' gradient: the first only, boxes of 64 x 64).
+struct Maps {
+    CUtensorMap a, b[4];
+};
+
 struct Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2], drain;
+    uint64_t tail[kStages];  // a last block whose rows this CTA clears before it tells the first
     uint32_t tmem;
     volatile int stop;
 };
 
+// Clears the rows past a bucket's end in a staged block (weights' gradient):
+// 128 bytes of each box of 64, up to the last row that is multiplied.
+__device__ __forceinline__ void clear_tail(uint8_t *stage, int len, int boxes)
+{
+    const int quads = (ceil_div(len, 16) * 16 - len) * 8;
+    for (int x = threadIdx.x & 31; x < boxes * quads; x += 32)
+        *reinterpret_cast<uint4 *>(stage + x / quads * 8192 + len * 128 + x % quads * 16) =
+            make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
 template <int MODE, typename Tout>
-__global__ void __launch_bounds__(kThreads, 1)
-expert_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-              const __grid_constant__ CUtensorMap map_b16, ExpertArgs a)
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -306,14 +408,17 @@ expert_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.full[i], 4);   // both operands of both CTAs
             mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.tail[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 4);
+            mbar_init(&sh.acc_empty[i], 8);  // the storing warps of both CTAs
         }
         mbar_init(&sh.drain, 1);
         sh.stop = 0;
@@ -323,128 +428,153 @@ expert_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
     griddep_wait();  // the plan and the operands come from earlier stream work
     griddep_launch_dependents();
     build_schedule<MODE>(a, sched);  // ends with a CTA barrier
+    cluster_sync();                  // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int tiles = sched.start[a.E];
     constexpr bool kAMn = MODE != kForward, kBMn = MODE == kWeightGrad;
 
-    if (warp == 0) {
-        if (lane == 0) {
+    if (warp == 0 || warp == 2) {
+        const bool weights = warp == 0;  // the M side's operand, or the N side's
+        if (elect_one()) {
+            const uint32_t full = leader_addr(sh.full);
+            Ring r;
             int64_t j = 0;  // blocks copied
             bool ok = true;
-            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+            for (int t = pair; t < tiles && ok; t += pairs) {
                 const Tile c = tile_of<MODE>(a, sched, t);
-                const int n16 = ceil_div(c.n, 16) * 16;
-                const int wide = MODE == kWeightGrad ? ceil_div(n16, 64) : n16 / 64;
-                const int narrow = MODE == kWeightGrad ? 0 : n16 % 64 / 16;
-                const uint32_t bytes = kABytes + wide * 8192 + narrow * 2048;
+                const int half = ceil_div(c.n, kStep) * (kStep / 2);
+                const int m = c.m0 + rank * kLanes, n = c.n0 + rank * half;
+                // the shortest box that holds this CTA's half of the columns
+                const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+                const int boxes = ceil_div(half, 64);
+                const uint32_t bytes = weights              ? kABytes
+                                       : MODE == kWeightGrad ? boxes * 8192
+                                                             : 2048 << size;
                 for (int b = 0; b < c.blocks; ++b, ++j) {
-                    const int st = (int)(j % kStages);
-                    if (j >= kStages &&
-                        !wait(&sh.empty[st], (uint32_t)(j / kStages - 1) & 1, &sh.stop)) {
+                    if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = ring + st * kStageBytes, *sb = sa + kABytes;
-                    uint64_t *bar = &sh.full[st];
-                    mbar_arrive_expect_tx(bar, bytes);
-                    const int k = b * kK;
-                    if (MODE == kForward) {
-                        tma_3d(sa, &map_a, bar, k, c.m0, c.e);
-                    } else if (MODE == kRowGrad) {
-                        tma_3d(sa, &map_a, bar, c.m0, k, c.e);
-                        tma_3d(sa + 8192, &map_a, bar, c.m0 + 64, k, c.e);
+                    uint8_t *sa = ring + r.at * kStageBytes, *sb = sa + kABytes;
+                    uint32_t bar = full + r.at * 8;
+                    if (MODE == kWeightGrad && rank == 1 && b + 1 == c.blocks && c.last % 16) {
+                        bar = smem_u32(&sh.tail[r.at]);  // warp 1 clears rows and then arrives
+                        mbar_arrive_expect_tx(&sh.tail[r.at], bytes);
                     } else {
-                        tma_2d(sa, &map_a, bar, c.m0, c.row + k);
-                        tma_2d(sa + 8192, &map_a, bar, c.m0 + 64, c.row + k);
+                        arrive_expect_at(bar, bytes);
                     }
-                    for (int i = 0; i < wide; ++i) {
-                        if (MODE == kWeightGrad)
-                            tma_2d(sb + i * 8192, &map_b, bar, c.n0 + i * 64, c.row + k);
-                        else
-                            tma_2d(sb + i * 8192, &map_b, bar, k, c.n0 + i * 64);
+                    const int k = b * kK;
+                    if (weights) {
+                        if (MODE == kForward) {
+                            tma_3d(sa, &maps.a, bar, k, m, c.e);
+                        } else if (MODE == kRowGrad) {
+                            tma_3d(sa, &maps.a, bar, m, k, c.e);
+                            tma_3d(sa + 8192, &maps.a, bar, m + 64, k, c.e);
+                        } else {
+                            tma_2d(sa, &maps.a, bar, m, c.row + k);
+                            tma_2d(sa + 8192, &maps.a, bar, m + 64, c.row + k);
+                        }
+                    } else if (MODE == kWeightGrad) {
+                        for (int i = 0; i < boxes; ++i)
+                            tma_2d(sb + i * 8192, &maps.b[0], bar, n + i * 64, c.row + k);
+                    } else {
+                        tma_2d(sb, &maps.b[size], bar, k, n);
                     }
-                    for (int i = 0; i < narrow; ++i)
-                        tma_2d(sb + wide * 8192 + i * 2048, &map_b16, bar, k,
-                               c.n0 + wide * 64 + i * 16);
+                    r.next();
                 }
             }
-            if (!ok) {  // leave no copy in flight
+            if (!ok && rank == 0) {
+                // leave no copy in flight: both CTAs' copies arrive here
                 for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
                     (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
             }
         }
-    } else if (warp == 1) {
-        int64_t j = 0;
+        __syncwarp();
+    } else if (warp == 1 && rank == 0) {
+        Ring r;
         int i = 0;  // tiles done
         bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+        for (int t = pair; t < tiles && ok; t += pairs, ++i) {
             const Tile c = tile_of<MODE>(a, sched, t);
             const int buf = i & 1;
             if (i >= 2 && !wait(&sh.acc_empty[buf], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) break;
             tc_fence_after();
-            const int n16 = ceil_div(c.n, 16) * 16;
-            const uint32_t idesc = instr_desc(n16, kAMn, kBMn);
-            for (int b = 0; b < c.blocks; ++b, ++j) {
-                const int st = (int)(j % kStages);
-                if (!wait(&sh.full[st], (uint32_t)(j / kStages) & 1, &sh.stop)) {
+            const int cols = ceil_div(c.n, kStep) * kStep;
+            const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
+            for (int b = 0; b < c.blocks; ++b) {
+                if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
                     ok = false;
                     break;
                 }
-                uint8_t *sa = ring + st * kStageBytes;
+                uint8_t *sa = ring + r.at * kStageBytes;
                 const int len = b + 1 == c.blocks ? c.last : kK;
                 const int steps = ceil_div(len, 16);
                 if (MODE == kWeightGrad && len % 16) {
-                    // rows past the bucket's end: 128 bytes of each box of 64
-                    const int boxes = 2 + ceil_div(n16, 64);
-                    const int quads = (steps * 16 - len) * 8;
-                    for (int x = lane; x < boxes * quads; x += 32)
-                        *reinterpret_cast<uint4 *>(sa + x / quads * 8192 + len * 128 +
-                                                   x % quads * 16) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                    // after what the other CTA cleared
+                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+                    clear_tail(sa, len, 2 + ceil_div(cols / 2, 64));
                 }
                 tc_fence_after();
-                if (lane == 0) {
+                if (elect_one()) {
                     const uint64_t da = operand_desc(smem_u32(sa), kAMn);
                     const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
                     for (int s = 0; s < steps; ++s)
                         mma_bf16(tmem + buf * kN, da + s * (kAMn ? 128 : 2),
                                  db + s * (kBMn ? 128 : 2), idesc, b > 0 || s > 0);
-                    mma_commit(&sh.empty[st]);
+                    mma_commit(&sh.empty[r.at]);
                 }
                 __syncwarp();
+                r.next();
             }
-            if (ok && lane == 0) mma_commit(&sh.acc_full[buf]);
+            if (ok && elect_one()) mma_commit(&sh.acc_full[buf]);
             __syncwarp();
         }
-        if (lane == 0) mma_commit(&sh.drain);  // nothing is issued after this
+        if (elect_one()) mma_commit(&sh.drain);  // nothing is issued after this
         __syncwarp();
-        (void)wait_slow(&sh.drain, 0, nullptr);
-    } else if (warp < 4) {
+    } else if (warp == 1) {
+        if (MODE == kWeightGrad) {
+            Ring r;
+            uint32_t rounds = 0;  // parity of each stage's next tail
+            for (int t = pair; t < tiles; t += pairs) {
+                const Tile c = tile_of<MODE>(a, sched, t);
+                if (c.blocks && c.last % 16) {
+                    for (int b = 1; b < c.blocks; ++b) r.next();
+                    if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
+                    rounds ^= 1u << r.at;
+                    clear_tail(ring + r.at * kStageBytes, c.last,
+                               2 + ceil_div(ceil_div(c.n, kStep) * (kStep / 2), 64));
+                    if (lane < 2) arrive_release_at(leader_addr(&sh.full[r.at]));
+                    r.next();
+                } else {
+                    for (int b = 0; b < c.blocks; ++b) r.next();
+                }
+            }
+        }
+    } else if (warp == 3) {
         if (MODE != kWeightGrad)
             zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
-                      blockIdx.x * 2 + warp - 2, gridDim.x * 2);
+                      blockIdx.x, gridDim.x);
     } else {
         const int q = warp & 3;
         int i = 0;
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+        for (int t = pair; t < tiles; t += pairs, ++i) {
             const Tile c = tile_of<MODE>(a, sched, t);
             const int buf = i & 1;
             if (!wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)) break;
             tc_fence_after();
-            const int m = c.m0 + q * 32 + lane;
+            const int m = c.m0 + rank * kLanes + q * 32 + lane;
             const int64_t first = MODE == kWeightGrad ? (int64_t)c.e * a.N + c.n0 : c.n0;
             Tout *out = reinterpret_cast<Tout *>(a.out) + first * a.M + m;
             for (int n = 0; n < c.n; n += 32) {
-                uint32_t r[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kN + n, r);
+                uint32_t v[32];
+                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kN + n, v);
                 if (m < a.M) {
 #pragma unroll
                     for (int x = 0; x < 32; ++x) {
                         if (n + x >= c.n) break;
                         // a bucket without rows: no product was issued
-                        const float f = c.blocks ? __uint_as_float(r[x]) : 0.0f;
+                        const float f = c.blocks ? __uint_as_float(v[x]) : 0.0f;
                         if (sizeof(Tout) == 2)
                             reinterpret_cast<__nv_bfloat16 *>(out)[(int64_t)(n + x) * a.M] =
                                 __float2bfloat16_rn(f);
@@ -456,11 +586,14 @@ expert_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+            if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (warp == 1) (void)wait_slow(&sh.drain, 0, nullptr);  // the last matrix instruction
+    __syncwarp();
+    cluster_sync();  // no arrival or product of the other CTA is under way
     if (tid == 0 && sh.stop) atomicOr(&g_expert_error, kErrExpertTimeout);
     if (warp == 1) tmem_free(tmem, 2 * kN);
 }
@@ -504,15 +637,14 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t 
 }
 
 template <int MODE, typename Tout>
-int launch_expert(const CUtensorMap &ma, const CUtensorMap &mb, const CUtensorMap &mb16,
-                  const ExpertArgs &a, int grid, cudaStream_t stream)
+int launch_expert(const Maps &maps, const ExpertArgs &a, int grid, cudaStream_t stream)
 {
     static KernelCache kc;
     const size_t smem = 1024 + kStages * kStageBytes + (3 * (size_t)a.E + 1) * sizeof(int);
     cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess)
-        e = launch_pdl(expert_kernel<MODE, Tout>, dim3(grid), dim3(kThreads), smem, stream, ma, mb,
-                       mb16, a);
+        e = launch_pdl(expert_kernel<MODE, Tout>, dim3(grid), dim3(kThreads), smem, stream, maps,
+                       a);
     if (e != cudaSuccess) {
         set_cuda_error(e);
         return MOE_ECUDA;
@@ -549,26 +681,26 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
     a.N = (int)N;
     a.K = (int)(MODE == kForward ? D : N);
     a.out = static_cast<uint8_t *>(out);
-    CUtensorMap ma = {}, mb = {}, mb16 = {};
+    Maps maps = {};
     cudaError_t e = cudaSuccess;
     if (MODE == kWeightGrad) {
         // without rows there is nothing to copy, and no address to describe
-        if (rows > 0) e = make_map(&ma, other, D, rows, 0, 64);
-        if (rows > 0 && e == cudaSuccess) e = make_map(&mb, rows_a, N, rows, 0, 64);
+        if (rows > 0) e = make_map(&maps.a, other, D, rows, 0, 64);
+        if (rows > 0 && e == cudaSuccess) e = make_map(&maps.b[0], rows_a, N, rows, 0, 64);
     } else {
-        e = make_map(&ma, other, D, N, E, MODE == kForward ? kM : 64);
-        if (e == cudaSuccess) e = make_map(&mb, rows_a, a.K, rows, 0, 64);
-        if (e == cudaSuccess) e = make_map(&mb16, rows_a, a.K, rows, 0, 16);
+        e = make_map(&maps.a, other, D, N, E, MODE == kForward ? kLanes : 64);
+        for (int i = 0; i < 4 && e == cudaSuccess; ++i)
+            e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 << i);
     }
     if (e != cudaSuccess) {
         set_cuda_error(e);
         return MOE_ECUDA;
     }
-    const int sms = sm_count();
-    const int grid = (int)(most < sms ? most : sms);
+    const int pairs = sm_count() / 2;
+    const int grid = 2 * (int)(most < pairs ? most : pairs);
     return out_dtype == MOE_BF16
-               ? launch_expert<MODE, __nv_bfloat16>(ma, mb, mb16, a, grid, stream)
-               : launch_expert<MODE, float>(ma, mb, mb16, a, grid, stream);
+               ? launch_expert<MODE, __nv_bfloat16>(maps, a, grid, stream)
+               : launch_expert<MODE, float>(maps, a, grid, stream);
 }
 
 } // namespace
