@@ -10,8 +10,8 @@
 // (256 TMEM lanes of a pair of CTAs) is always the dimension that is
 // contiguous in the output: weight rows n (forward), d (the gradients).  The N
 // side (up to 256 TMEM columns) is the tokens of one bucket, or the rows n of
-// dw.  A bucket of c tokens is cut into ceil(c / 256) equal parts rounded up to
-// 32 columns, so a ragged bucket costs at most 31 idle columns a part and one
+// dw.  A bucket of c tokens is cut into ceil(c / 256) parts of nearly equal
+// numbers of 32-column steps, so a bucket costs at most 31 idle columns and one
 // token costs 32 columns instead of a padded tile of rows.  Rows of other
 // buckets that a copied box holds land in columns that are never stored;
 // columns are independent, so nothing they hold (NaN included) matters.  The
@@ -47,7 +47,6 @@ constexpr int kM = 2 * kLanes;      // of the pair
 constexpr int kN = 256;             // TMEM columns of one accumulator
 constexpr int kK = 64;              // reduction block: 128 bytes of bf16
 constexpr int kStep = 32;           // columns come in these steps, half of them from each CTA
-constexpr int kStages = 6;
 constexpr int kABytes = kLanes * kK * 2;
 constexpr int kBBytes = kN / 2 * kK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
@@ -66,6 +65,20 @@ struct ExpertArgs {
     int N;                // rows of a weight (weights' gradient)
     int K;                // reduction length (the other two)
     uint8_t *out;
+};
+
+// Shared memory: six stages of operands, and 4 KB for each storing warp.  The
+// weights' gradient has few products for each output (a bucket of 512 tokens:
+// 2.2 us a tile) and is bound by its stores, which need more bytes in flight:
+// five stages and 12 KB.
+template <int MODE, typename Tout> struct Layout {
+    static constexpr bool kStores = MODE == kWeightGrad;
+    static constexpr int kStages = kStores ? 5 : 6;
+    static constexpr int kArea = kStores ? 12288 : 4096;
+    static constexpr int kBoxRows = kStores ? 32 : 16;  // a stored box is 32 outputs wide
+    static constexpr int kBoxBytes = kBoxRows * 32 * (int)sizeof(Tout);
+    static constexpr int kTurns = kArea / kBoxBytes;
+    static constexpr int kBytes = kStages * kStageBytes + 4 * kArea;
 };
 
 // --- tcgen05 ---------------------------------------------------------------
@@ -115,20 +128,34 @@ __device__ __forceinline__ void tc_fence_after()
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// 32 columns of this warp's 32 lanes: thread = lane, register = column.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32])
+// 32 columns of this warp's 32 lanes: thread = lane, register = column.  The
+// values may be used after tmem_wait, which the compiler sees to write them.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32])
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-          "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
         : "r"(addr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 
 // Shared-memory operand descriptor, 128-byte swizzle.  Rows along the
@@ -227,6 +254,24 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, uint32
         : "memory");
 }
 
+// A box from this CTA's shared memory to global memory; what lies outside the
+// tensor is not written.
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int x, int y,
+                                          int z, bool depth)
+{
+    if (depth)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+            ::"l"(map), "r"(smem_u32(src)), "r"(x), "r"(y), "r"(z)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                map),
+            "r"(smem_u32(src)), "r"(x), "r"(y)
+            : "memory");
+}
+
 // --- bounded waits -----------------------------------------------------------
 
 __device__ __forceinline__ uint64_t now_ns()
@@ -261,7 +306,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
 }
 
 // A place in the ring and the parity of its current round.
-struct Ring {
+template <int kStages> struct Ring {
     int at = 0;
     uint32_t round = 0;
     __device__ __forceinline__ void next()
@@ -317,11 +362,13 @@ template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a,
         r.last = fill - (r.blocks - 1) * kK;
     } else {
         const int parts = ceil_div(fill, kN);
-        const int per = ceil_div(ceil_div(fill, parts), kStep) * kStep;
+        const int steps = ceil_div(fill, kStep);
         const int i = local % parts;
+        const int from = (int)((int64_t)steps * i / parts) * kStep;
+        const int to = (int)((int64_t)steps * (i + 1) / parts) * kStep;
         r.m0 = local / parts * kM;
-        r.n0 = r.row + i * per;
-        r.n = min(per, fill - i * per);
+        r.n0 = r.row + from;
+        r.n = min(to, fill) - from;
         r.blocks = ceil_div(a.K, kK);
         r.last = a.K - (r.blocks - 1) * kK;
     }
@@ -375,9 +422,10 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Sc
 // rows (weights' gradient: the first only, boxes of 64 x 64).
 struct Maps {
     CUtensorMap a, b[4];
+    CUtensorMap out;   // stored boxes
 };
 
-struct Shared {
+template <int kStages> struct Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint64_t tail[kStages];  // a last block whose rows this CTA clears before it tells the first
@@ -397,15 +445,25 @@ __device__ __forceinline__ void clear_tail(uint8_t *stage, int len, int boxes)
     __syncwarp();
 }
 
+template <typename T> __device__ __forceinline__ T round_to(float f);
+template <> __device__ __forceinline__ float round_to<float>(float f) { return f; }
+template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(float f)
+{
+    return __float2bfloat16_rn(f);
+}
+
 template <int MODE, typename Tout>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    int *lists = reinterpret_cast<int *>(ring + kStages * kStageBytes);
+    using L = Layout<MODE, Tout>;
+    constexpr int kStages = L::kStages;
+    uint8_t *boxes = ring + kStages * kStageBytes;
+    int *lists = reinterpret_cast<int *>(ring + L::kBytes);
     Schedule sched = {lists, lists + a.E + 1, lists + 2 * a.E + 1, 0};
-    __shared__ Shared sh;
+    __shared__ Shared<kStages> sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
@@ -438,7 +496,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         const bool weights = warp == 0;  // the M side's operand, or the N side's
         if (elect_one()) {
             const uint32_t full = leader_addr(sh.full);
-            Ring r;
+            Ring<kStages> r;
             int64_t j = 0;  // blocks copied
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
@@ -447,9 +505,9 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 const int m = c.m0 + rank * kLanes, n = c.n0 + rank * half;
                 // the shortest box that holds this CTA's half of the columns
                 const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
-                const int boxes = ceil_div(half, 64);
+                const int chunks = ceil_div(half, 64);
                 const uint32_t bytes = weights              ? kABytes
-                                       : MODE == kWeightGrad ? boxes * 8192
+                                       : MODE == kWeightGrad ? chunks * 8192
                                                              : 2048 << size;
                 for (int b = 0; b < c.blocks; ++b, ++j) {
                     if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
@@ -476,7 +534,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                             tma_2d(sa + 8192, &maps.a, bar, m + 64, c.row + k);
                         }
                     } else if (MODE == kWeightGrad) {
-                        for (int i = 0; i < boxes; ++i)
+                        for (int i = 0; i < chunks; ++i)
                             tma_2d(sb + i * 8192, &maps.b[0], bar, n + i * 64, c.row + k);
                     } else {
                         tma_2d(sb, &maps.b[size], bar, k, n);
@@ -492,7 +550,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
-        Ring r;
+        Ring<kStages> r;
         int i = 0;  // tiles done
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, ++i) {
@@ -534,7 +592,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         __syncwarp();
     } else if (warp == 1) {
         if (MODE == kWeightGrad) {
-            Ring r;
+            Ring<kStages> r;
             uint32_t rounds = 0;  // parity of each stage's next tail
             for (int t = pair; t < tiles; t += pairs) {
                 const Tile c = tile_of<MODE>(a, sched, t);
@@ -557,37 +615,69 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                       blockIdx.x, gridDim.x);
     } else {
         const int q = warp & 3;
-        int i = 0;
+        constexpr int kBoxRows = L::kBoxRows;
+        Tout *box = reinterpret_cast<Tout *>(boxes + q * L::kArea);
+        int i = 0, turn = 0;
         for (int t = pair; t < tiles; t += pairs, ++i) {
             const Tile c = tile_of<MODE>(a, sched, t);
             const int buf = i & 1;
             if (!wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)) break;
             tc_fence_after();
-            const int m = c.m0 + rank * kLanes + q * 32 + lane;
-            const int64_t first = MODE == kWeightGrad ? (int64_t)c.e * a.N + c.n0 : c.n0;
-            Tout *out = reinterpret_cast<Tout *>(a.out) + first * a.M + m;
-            for (int n = 0; n < c.n; n += 32) {
-                uint32_t v[32];
-                tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kN + n, v);
-                if (m < a.M) {
+            const int m = c.m0 + rank * kLanes + q * 32;
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kN;
+            uint32_t v[2][32];
+            tmem_load(acc, v[0]);
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        if (n + x >= c.n) break;
-                        // a bucket without rows: no product was issued
-                        const float f = c.blocks ? __uint_as_float(v[x]) : 0.0f;
-                        if (sizeof(Tout) == 2)
-                            reinterpret_cast<__nv_bfloat16 *>(out)[(int64_t)(n + x) * a.M] =
-                                __float2bfloat16_rn(f);
-                        else
-                            reinterpret_cast<float *>(out)[(int64_t)(n + x) * a.M] = f;
+            for (int k = 0; k < kN / 32; ++k) {
+                const int n = k * 32;
+                if (n >= c.n) break;
+                uint32_t(&r)[32] = v[k & 1];
+                tmem_wait(r);
+                if (n + 32 < c.n) {
+                    tmem_load(acc + n + 32, v[(k + 1) & 1]);
+                } else {  // the accumulator is read: the next products may have it
+                    tc_fence_before();
+                    if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                }
+                if (MODE == kWeightGrad && c.blocks == 0) {
+                    // an expert without rows: no product was issued
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) r[x] = 0;
+                }
+                if (m >= a.M) continue;
+#pragma unroll
+                for (int h = 0; h < 32; h += kBoxRows) {
+                    if (n + h >= c.n) break;
+                    if (MODE == kWeightGrad || n + h + kBoxRows <= c.n) {
+                        Tout *b = box + turn * (kBoxRows * 32);
+                        if (++turn == L::kTurns) turn = 0;
+                        if (lane == 0) bulk_wait_read<L::kTurns - 1>();
+                        __syncwarp();
+#pragma unroll
+                        for (int x = 0; x < kBoxRows; ++x)
+                            b[x * 32 + lane] = round_to<Tout>(__uint_as_float(r[h + x]));
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            tma_store(&maps.out, b, m, c.n0 + n + h, c.e, MODE == kWeightGrad);
+                            bulk_commit();
+                        }
+                    } else if (m + lane < a.M) {
+                        // the bucket ends inside the box: the rows after it are not ours
+                        Tout *out = reinterpret_cast<Tout *>(a.out) +
+                                    (int64_t)(c.n0 + n + h) * a.M + m + lane;
+#pragma unroll
+                        for (int x = 0; x < kBoxRows; ++x)
+                            if (n + h + x < c.n)
+                                out[(int64_t)x * a.M] =
+                                    round_to<Tout>(__uint_as_float(r[h + x]));
                     }
                 }
-                __syncwarp();
             }
-            tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
         }
+        if (lane == 0) bulk_wait_all();
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
@@ -619,28 +709,39 @@ EncodeFn encode_fn()
     return fn;
 }
 
-// A map over bf16 [depth, rows, width] (2-D when depth is 0), boxes of
-// 64 x box_rows with the 128-byte swizzle; what lies outside reads as zero.
-cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t rows,
-                     int64_t depth, int box_rows)
+// A map over [depth, rows, width] (2-D when depth is 0).
+cudaError_t encode(CUtensorMap *map, const void *base, bool f32, int64_t width, int64_t rows,
+                   int64_t depth, int box_width, int box_rows, bool swizzle)
 {
     EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
+    const int size = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)depth};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * rows * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, depth ? 3 : 2,
-                          const_cast<void *>(base), dims, strides, box, step,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t strides[2] = {(cuuint64_t)width * size, (cuuint64_t)width * rows * size};
+    const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r =
+        fn(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+           depth ? 3 : 2, const_cast<void *>(base), dims, strides, box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE,
+           swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// An operand: bf16 in boxes of 64 x box_rows with the 128-byte swizzle; what
+// lies outside reads as zero.
+cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t rows,
+                     int64_t depth, int box_rows)
+{
+    return encode(map, base, false, width, rows, depth, 64, box_rows, true);
 }
 
 template <int MODE, typename Tout>
 int launch_expert(const Maps &maps, const ExpertArgs &a, int grid, cudaStream_t stream)
 {
     static KernelCache kc;
-    const size_t smem = 1024 + kStages * kStageBytes + (3 * (size_t)a.E + 1) * sizeof(int);
+    const size_t smem = 1024 + Layout<MODE, Tout>::kBytes + (3 * (size_t)a.E + 1) * sizeof(int);
     cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess)
         e = launch_pdl(expert_kernel<MODE, Tout>, dim3(grid), dim3(kThreads), smem, stream, maps,
@@ -692,6 +793,11 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         for (int i = 0; i < 4 && e == cudaSuccess; ++i)
             e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 << i);
     }
+    const int box_rows = Layout<MODE, float>::kBoxRows;
+    if (e == cudaSuccess)
+        e = MODE == kWeightGrad
+                ? encode(&maps.out, out, out_dtype == MOE_F32, D, N, E, 32, box_rows, false)
+                : encode(&maps.out, out, out_dtype == MOE_F32, M, rows, 0, 32, box_rows, false);
     if (e != cudaSuccess) {
         set_cuda_error(e);
         return MOE_ECUDA;
