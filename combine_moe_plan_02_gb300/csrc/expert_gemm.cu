@@ -29,7 +29,7 @@
 // ring of stages (one warp each: issuing a copy takes 60 to 100 cycles and a
 // wait and an arrival as much again, against 512 cycles of products a block),
 // warp 1 of the first CTA issues the matrix instructions, warp 3 clears the
-// rows of the output that belong to no bucket, warps 4 to 7 store.  Two
+// rows of the output that belong to no bucket, warps 4 to 11 store.  Two
 // accumulators of 256 columns let the stores of a tile overlap the next tile's
 // products.  Every wait is bounded.
 
@@ -41,7 +41,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kStoreWarps = 8;      // two for each quarter of the lanes
+constexpr int kThreads = 128 + 32 * kStoreWarps;
 constexpr int kLanes = 128;         // TMEM lanes of a CTA: outputs along the contiguous dimension
 constexpr int kM = 2 * kLanes;      // of the pair
 constexpr int kN = 256;             // TMEM columns of one accumulator
@@ -67,18 +68,19 @@ struct ExpertArgs {
     uint8_t *out;
 };
 
-// Shared memory: six stages of operands, and 4 KB for each storing warp.  The
+// Shared memory: six stages of operands, and 2 KB for each storing warp.  The
 // weights' gradient has few products for each output (a bucket of 512 tokens:
 // 2.2 us a tile) and is bound by its stores, which need more bytes in flight:
-// five stages and 12 KB.
+// five stages and 6 KB.
 template <int MODE, typename Tout> struct Layout {
     static constexpr bool kStores = MODE == kWeightGrad;
     static constexpr int kStages = kStores ? 5 : 6;
-    static constexpr int kArea = kStores ? 12288 : 4096;
-    static constexpr int kBoxRows = kStores ? 32 : 16;  // a stored box is 32 outputs wide
+    static constexpr int kArea = kStores ? 6144 : 2048;
+    // a stored box is 32 outputs wide
+    static constexpr int kBoxRows = kStores && sizeof(Tout) == 2 ? 32 : 16;
     static constexpr int kBoxBytes = kBoxRows * 32 * (int)sizeof(Tout);
     static constexpr int kTurns = kArea / kBoxBytes;
-    static constexpr int kBytes = kStages * kStageBytes + 4 * kArea;
+    static constexpr int kBytes = kStages * kStageBytes + kStoreWarps * kArea;
 };
 
 // --- tcgen05 ---------------------------------------------------------------
@@ -476,7 +478,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
-            mbar_init(&sh.acc_empty[i], 8);  // the storing warps of both CTAs
+            mbar_init(&sh.acc_empty[i], 2 * kStoreWarps);  // the storing warps of both CTAs
         }
         mbar_init(&sh.drain, 1);
         sh.stop = 0;
@@ -616,7 +618,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     } else {
         const int q = warp & 3;
         constexpr int kBoxRows = L::kBoxRows;
-        Tout *box = reinterpret_cast<Tout *>(boxes + q * L::kArea);
+        const int odd = warp >> 2 & 1;  // this warp's blocks of 32 columns: even or odd ones
+        Tout *box = reinterpret_cast<Tout *>(boxes + (warp - 4) * L::kArea);
         int i = 0, turn = 0;
         for (int t = pair; t < tiles; t += pairs, ++i) {
             const Tile c = tile_of<MODE>(a, sched, t);
@@ -625,16 +628,22 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             tc_fence_after();
             const int m = c.m0 + rank * kLanes + q * 32;
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kN;
+            const int last = (ceil_div(c.n, 32) - 1 - odd) / 2;  // the last one, if any
             uint32_t v[2][32];
-            tmem_load(acc, v[0]);
+            if (c.n > odd * 32) {
+                tmem_load(acc + odd * 32, v[0]);
+            } else {
+                tc_fence_before();
+                if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+            }
 #pragma unroll
-            for (int k = 0; k < kN / 32; ++k) {
-                const int n = k * 32;
+            for (int k = 0; k < kN / 64; ++k) {
+                const int n = k * 64 + odd * 32;
                 if (n >= c.n) break;
                 uint32_t(&r)[32] = v[k & 1];
                 tmem_wait(r);
-                if (n + 32 < c.n) {
-                    tmem_load(acc + n + 32, v[(k + 1) & 1]);
+                if (k < last) {
+                    tmem_load(acc + n + 64, v[(k + 1) & 1]);
                 } else {  // the accumulator is read: the next products may have it
                     tc_fence_before();
                     if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
@@ -793,7 +802,8 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         for (int i = 0; i < 4 && e == cudaSuccess; ++i)
             e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 << i);
     }
-    const int box_rows = Layout<MODE, float>::kBoxRows;
+    const int box_rows = out_dtype == MOE_F32 ? Layout<MODE, float>::kBoxRows
+                                              : Layout<MODE, __nv_bfloat16>::kBoxRows;
     if (e == cudaSuccess)
         e = MODE == kWeightGrad
                 ? encode(&maps.out, out, out_dtype == MOE_F32, D, N, E, 32, box_rows, false)
