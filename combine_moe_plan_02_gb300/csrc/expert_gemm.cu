@@ -29,7 +29,8 @@
 // ring of stages (one warp each: issuing a copy takes 60 to 100 cycles and a
 // wait and an arrival as much again, against 512 cycles of products a block),
 // warp 1 of the first CTA issues the matrix instructions, warp 3 clears the
-// rows of the output that belong to no bucket, warps 4 to 11 store.  Two
+// rows of the output that belong to no bucket (weights' gradient: the staged
+// rows past a bucket's end), warps 4 to 11 store.  Two
 // accumulators of 256 columns let the stores of a tile overlap the next tile's
 // products.  Every wait is bounded.
 
@@ -51,6 +52,8 @@ constexpr int kStep = 32;           // columns come in these steps, half of them
 constexpr int kABytes = kLanes * kK * 2;
 constexpr int kBBytes = kN / 2 * kK * 2;
 constexpr int kStageBytes = kABytes + kBBytes;
+constexpr int kStages = 6;
+constexpr int kBoxArea = 2048;      // of each storing warp
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
 
 __device__ uint32_t g_expert_error;  // kErrExpertTimeout | kErrExpertBucket
@@ -68,19 +71,17 @@ struct ExpertArgs {
     uint8_t *out;
 };
 
-// Shared memory: six stages of operands, and 2 KB for each storing warp.  The
-// weights' gradient has few products for each output (a bucket of 512 tokens:
-// 2.2 us a tile) and is bound by its stores, which need more bytes in flight:
-// five stages and 6 KB.
-template <int MODE, typename Tout> struct Layout {
-    static constexpr bool kStores = MODE == kWeightGrad;
-    static constexpr int kStages = kStores ? 5 : 6;
-    static constexpr int kArea = kStores ? 6144 : 2048;
-    // a stored box is 32 outputs wide
-    static constexpr int kBoxRows = kStores && sizeof(Tout) == 2 ? 32 : 16;
-    static constexpr int kBoxBytes = kBoxRows * 32 * (int)sizeof(Tout);
-    static constexpr int kTurns = kArea / kBoxBytes;
-    static constexpr int kBytes = kStages * kStageBytes + kStoreWarps * kArea;
+// Stored boxes: 32 outputs wide, kBoxRows columns of the accumulator high, each
+// storing warp with room for kTurns of them.  The weights' gradient has few
+// products for each output and is often bound by these stores.  Its bf16 rows
+// are 64 bytes, so a box costs its fixed part: 256 buckets of 33 rows, 1024 x
+// 2048, take 186 us in boxes of 32 rows and 250 us in two of 16 (f32: 361 us
+// in boxes of 8, 379 us in 16).  Where rows are columns, a box holds whole
+// columns of one bucket and the rest leaves row by row: 16.
+template <int MODE, typename Tout> struct Boxes {
+    static constexpr int kRows = MODE != kWeightGrad ? 16 : sizeof(Tout) == 2 ? 32 : 8;
+    static constexpr int kBytes = kRows * 32 * (int)sizeof(Tout);
+    static constexpr int kTurns = kBoxArea / kBytes;
 };
 
 // --- tcgen05 ---------------------------------------------------------------
@@ -213,8 +214,11 @@ __device__ __forceinline__ void cluster_sync()
 
 // Arrivals at a barrier of either CTA.  Those that only hand over tensor
 // memory or a copy's byte count order nothing (the copy and the tcgen05 fences
-// do); the one behind cleared shared memory releases it.  A release at
-// cluster scope on every block costs about 0.4 us of it: 1745 against 885 us.
+// do).  The one behind cleared rows is ordered after the clearing CTA's
+// fence.proxy.async; the rows lie in that CTA's own shared memory and are read
+// there by its half of the matrix instruction.  A release at cluster scope
+// costs 0.4 us of every block (1745 against 885 us for 64 buckets of 512 rows,
+// 2048 x 7168) and 0.8 us of every cleared one (768 against 636 us).
 __device__ __forceinline__ void arrive_at(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
@@ -223,7 +227,7 @@ __device__ __forceinline__ void arrive_at(uint32_t bar)
 
 __device__ __forceinline__ void arrive_release_at(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 
@@ -307,8 +311,21 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     return false;
 }
 
+// Orders what follows after the pair's writes before a phase that has passed.
+__device__ __forceinline__ void acquire_pair(uint64_t *bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+}
+
 // A place in the ring and the parity of its current round.
-template <int kStages> struct Ring {
+struct Ring {
     int at = 0;
     uint32_t round = 0;
     __device__ __forceinline__ void next()
@@ -317,6 +334,10 @@ template <int kStages> struct Ring {
             at = 0;
             round ^= 1;
         }
+    }
+    __device__ __forceinline__ void skip(int n)
+    {
+        at = (at + n) % kStages;  // the round is not kept
     }
 };
 
@@ -427,22 +448,23 @@ struct Maps {
     CUtensorMap out;   // stored boxes
 };
 
-template <int kStages> struct Shared {
+struct Shared {
     uint64_t full[kStages], empty[kStages];
     uint64_t acc_full[2], acc_empty[2], drain;
-    uint64_t tail[kStages];  // a last block whose rows this CTA clears before it tells the first
+    uint64_t tail[kStages];  // a last block, until the rows past its end are cleared
     uint32_t tmem;
     volatile int stop;
 };
 
-// Clears the rows past a bucket's end in a staged block (weights' gradient):
-// 128 bytes of each box of 64, up to the last row that is multiplied.
-__device__ __forceinline__ void clear_tail(uint8_t *stage, int len, int boxes)
+// Clears the rows past a bucket's end in a staged block (weights' gradient),
+// up to the last row that is multiplied: 128 bytes of each of the four boxes of
+// 64, eight lanes a box.
+__device__ __forceinline__ void clear_tail(uint8_t *stage, int len)
 {
-    const int quads = (ceil_div(len, 16) * 16 - len) * 8;
-    for (int x = threadIdx.x & 31; x < boxes * quads; x += 32)
-        *reinterpret_cast<uint4 *>(stage + x / quads * 8192 + len * 128 + x % quads * 16) =
-            make_uint4(0, 0, 0, 0);
+    const int lane = threadIdx.x & 31;
+    uint8_t *at = stage + (lane >> 3) * 8192 + (lane & 7) * 16;
+    for (int row = len; row & 15; ++row)
+        *reinterpret_cast<uint4 *>(at + row * 128) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncwarp();
 }
@@ -460,12 +482,11 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    using L = Layout<MODE, Tout>;
-    constexpr int kStages = L::kStages;
+    using B = Boxes<MODE, Tout>;
     uint8_t *boxes = ring + kStages * kStageBytes;
-    int *lists = reinterpret_cast<int *>(ring + L::kBytes);
+    int *lists = reinterpret_cast<int *>(boxes + kStoreWarps * kBoxArea);
     Schedule sched = {lists, lists + a.E + 1, lists + 2 * a.E + 1, 0};
-    __shared__ Shared<kStages> sh;
+    __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
@@ -498,7 +519,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         const bool weights = warp == 0;  // the M side's operand, or the N side's
         if (elect_one()) {
             const uint32_t full = leader_addr(sh.full);
-            Ring<kStages> r;
+            Ring r;
             int64_t j = 0;  // blocks copied
             bool ok = true;
             for (int t = pair; t < tiles && ok; t += pairs) {
@@ -518,8 +539,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     }
                     uint8_t *sa = ring + r.at * kStageBytes, *sb = sa + kABytes;
                     uint32_t bar = full + r.at * 8;
-                    if (MODE == kWeightGrad && rank == 1 && b + 1 == c.blocks && c.last % 16) {
-                        bar = smem_u32(&sh.tail[r.at]);  // warp 1 clears rows and then arrives
+                    if (MODE == kWeightGrad && b + 1 == c.blocks && c.last % 16) {
+                        bar = smem_u32(&sh.tail[r.at]);  // warp 3 clears rows and then arrives
                         mbar_arrive_expect_tx(&sh.tail[r.at], bytes);
                     } else {
                         arrive_expect_at(bar, bytes);
@@ -552,7 +573,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
-        Ring<kStages> r;
+        Ring r;
         int i = 0;  // tiles done
         bool ok = true;
         for (int t = pair; t < tiles && ok; t += pairs, ++i) {
@@ -570,11 +591,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 uint8_t *sa = ring + r.at * kStageBytes;
                 const int len = b + 1 == c.blocks ? c.last : kK;
                 const int steps = ceil_div(len, 16);
-                if (MODE == kWeightGrad && len % 16) {
-                    // after what the other CTA cleared
-                    asm volatile("fence.acq_rel.cluster;" ::: "memory");
-                    clear_tail(sa, len, 2 + ceil_div(cols / 2, 64));
-                }
+                if (MODE == kWeightGrad && len % 16)
+                    acquire_pair(&sh.full[r.at], r.round);  // what either CTA cleared
                 tc_fence_after();
                 if (elect_one()) {
                     const uint64_t da = operand_desc(smem_u32(sa), kAMn);
@@ -592,34 +610,32 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         }
         if (elect_one()) mma_commit(&sh.drain);  // nothing is issued after this
         __syncwarp();
-    } else if (warp == 1) {
-        if (MODE == kWeightGrad) {
-            Ring<kStages> r;
+    } else if (warp == 3) {
+        if (MODE != kWeightGrad) {
+            zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
+                      blockIdx.x, gridDim.x);
+        } else {
+            Ring r;
             uint32_t rounds = 0;  // parity of each stage's next tail
             for (int t = pair; t < tiles; t += pairs) {
                 const Tile c = tile_of<MODE>(a, sched, t);
                 if (c.blocks && c.last % 16) {
-                    for (int b = 1; b < c.blocks; ++b) r.next();
+                    r.skip(c.blocks - 1);
                     if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
                     rounds ^= 1u << r.at;
-                    clear_tail(ring + r.at * kStageBytes, c.last,
-                               2 + ceil_div(ceil_div(c.n, kStep) * (kStep / 2), 64));
+                    clear_tail(ring + r.at * kStageBytes, c.last);
                     if (lane < 2) arrive_release_at(leader_addr(&sh.full[r.at]));
                     r.next();
                 } else {
-                    for (int b = 0; b < c.blocks; ++b) r.next();
+                    r.skip(c.blocks);
                 }
             }
         }
-    } else if (warp == 3) {
-        if (MODE != kWeightGrad)
-            zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
-                      blockIdx.x, gridDim.x);
-    } else {
+    } else if (warp >= 4) {
         const int q = warp & 3;
-        constexpr int kBoxRows = L::kBoxRows;
+        constexpr int kBoxRows = B::kRows;
         const int odd = warp >> 2 & 1;  // this warp's blocks of 32 columns: even or odd ones
-        Tout *box = reinterpret_cast<Tout *>(boxes + (warp - 4) * L::kArea);
+        Tout *box = reinterpret_cast<Tout *>(boxes + (warp - 4) * kBoxArea);
         int i = 0, turn = 0;
         for (int t = pair; t < tiles; t += pairs, ++i) {
             const Tile c = tile_of<MODE>(a, sched, t);
@@ -659,8 +675,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     if (n + h >= c.n) break;
                     if (MODE == kWeightGrad || n + h + kBoxRows <= c.n) {
                         Tout *b = box + turn * (kBoxRows * 32);
-                        if (++turn == L::kTurns) turn = 0;
-                        if (lane == 0) bulk_wait_read<L::kTurns - 1>();
+                        if (++turn == B::kTurns) turn = 0;
+                        if (lane == 0) bulk_wait_read<B::kTurns - 1>();
                         __syncwarp();
 #pragma unroll
                         for (int x = 0; x < kBoxRows; ++x)
@@ -750,7 +766,8 @@ template <int MODE, typename Tout>
 int launch_expert(const Maps &maps, const ExpertArgs &a, int grid, cudaStream_t stream)
 {
     static KernelCache kc;
-    const size_t smem = 1024 + Layout<MODE, Tout>::kBytes + (3 * (size_t)a.E + 1) * sizeof(int);
+    const size_t smem = 1024 + kStages * kStageBytes + kStoreWarps * kBoxArea +
+                        (3 * (size_t)a.E + 1) * sizeof(int);
     cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess)
         e = launch_pdl(expert_kernel<MODE, Tout>, dim3(grid), dim3(kThreads), smem, stream, maps,
@@ -802,8 +819,8 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         for (int i = 0; i < 4 && e == cudaSuccess; ++i)
             e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 << i);
     }
-    const int box_rows = out_dtype == MOE_F32 ? Layout<MODE, float>::kBoxRows
-                                              : Layout<MODE, __nv_bfloat16>::kBoxRows;
+    const int box_rows = out_dtype == MOE_F32 ? Boxes<MODE, float>::kRows
+                                              : Boxes<MODE, __nv_bfloat16>::kRows;
     if (e == cudaSuccess)
         e = MODE == kWeightGrad
                 ? encode(&maps.out, out, out_dtype == MOE_F32, D, N, E, 32, box_rows, false)
