@@ -22,6 +22,8 @@ The experts' products and the way back:
 from __future__ import annotations
 
 import ctypes
+from array import array
+from operator import attrgetter
 from typing import NamedTuple, Optional, Sequence, Union
 
 import torch
@@ -386,23 +388,23 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tens
     """Gradient of moe_combine: dy[tok_map[s,k]] = topk_w[s,k] * dout[s], zero
     on rows that no entry fills, and dw[s,k] = <dout[s], y[tok_map[s,k]]>,
     zero without a row.  Returns (dy in y's type, dw f32 [S, K])."""
-    S, K = plan.tok_map.shape
-    E = plan.cnt.numel()
-    if y.dim() != 2 or tuple(dout.shape) != (S, y.shape[1]):
+    S, K = shape = plan.tok_map.shape
+    if y.dim() != 2 or dout.shape != (S, y.shape[1]):
         raise ValueError("dout must be [S, H] and y [rows, H]")
-    if topk_w.dtype != torch.float32 or tuple(topk_w.shape) != (S, K):
+    rows, H = y.shape
+    if topk_w.dtype != torch.float32 or topk_w.shape != shape:
         raise TypeError("topk_w must be float32 with the shape of tok_map")
     if dy is None:
         dy = torch.empty_like(y)
     elif dy.dtype != y.dtype or dy.shape != y.shape:
         raise ValueError("dy must have y's type and shape")
     if dw is None:
-        dw = torch.empty(S, K, dtype=torch.float32, device=y.device)
-    elif dw.dtype != torch.float32 or tuple(dw.shape) != (S, K):
+        dw = torch.empty_like(topk_w)
+    elif dw.dtype != torch.float32 or dw.shape != shape:
         raise ValueError("dw must be float32 [S, K]")
     _abi.check("moe_combine_backward", lib().moe_combine_backward(
-        _ptr(dout), _dt(dout), _ptr(y), y.shape[0], _dt(y), _ptr(topk_w), _ptr(plan.tok_map),
-        _ptr(plan.cnt), _ptr(plan.off), S, y.shape[1], K, E, _ptr(dy), _ptr(dw),
+        _ptr(dout), _dt(dout), _ptr(y), rows, _dt(y), _ptr(topk_w), _ptr(plan.tok_map),
+        _ptr(plan.cnt), _ptr(plan.off), S, H, K, plan.cnt.numel(), _ptr(dy), _ptr(dw),
         _stream(stream, y)))
     return dy, dw
 
@@ -474,45 +476,65 @@ def moe_expert_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, plan: Union[Plan, C
     return out
 
 
-def _grad_list(name: str, tensors: Sequence[torch.Tensor]):
-    """Host arrays of the tensors' addresses, sizes and types."""
-    n = len(tensors)
-    for t in tensors:
-        if t.dtype not in (torch.float32, torch.bfloat16):
-            raise TypeError(f"{name} must be float32 or bfloat16")
-    return ((ctypes.c_void_p * n)(*[_ptr(t) for t in tensors]),
-            (ctypes.c_int64 * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int * n)(*[_dt(t) for t in tensors]))
+_dtype_of = attrgetter("dtype")
 
 
-def _grad_call(grads: Sequence[torch.Tensor], norm, workspace, stream):
-    """(device, norm, workspace) of a call over `grads`."""
+def _addresses(name: str, tensors: Sequence[torch.Tensor], device: int):
+    if device < 0 or set(map(torch.Tensor.get_device, tensors)) != {device}:
+        raise ValueError(f"{name} must live on one CUDA device")
+    if not all(map(torch.Tensor.is_contiguous, tensors)):
+        raise ValueError(f"{name} must be contiguous")
+    return array("Q", list(map(torch.Tensor.data_ptr, tensors)))
+
+
+def _grad_call(fn: str, grads: Sequence[torch.Tensor], max_norm, out, norm, workspace, stream):
+    # one attribute of all tensors at a time: a call over 40 tensors costs the
+    # host a third of what one tensor at a time does
     if not grads:
         raise ValueError("no gradients")
+    dtypes = list(map(_dtype_of, grads))
+    n, n32 = len(dtypes), dtypes.count(torch.float32)
+    if n32 + dtypes.count(torch.bfloat16) != n:
+        raise TypeError("grads must be float32 or bfloat16")
+    sizes = list(map(torch.Tensor.numel, grads))
+    if out is grads:
+        out = None
+    if out is not None and (list(map(_dtype_of, out)) != dtypes or
+                            list(map(torch.Tensor.numel, out)) != sizes):
+        raise ValueError("out must have the types and sizes of grads")
     like = grads[0]
+    device = like.get_device()
+    ptrs = _addresses("grads", grads, device)
+    outs = ptrs if out is None else _addresses("out", out, device)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=like.device)
     elif norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be float32 [1]")
-    ws = _workspace(int(lib().moe_grad_norm_workspace_size()), like.device, workspace)
+    L = lib()
+    ws = _workspace(int(L.moe_grad_norm_workspace_size()), like.device, workspace)
     if ws is not workspace and stream is not None:
         # made on the current stream, used on another
-        s = stream if isinstance(stream, torch.cuda.Stream) else \
-            torch.cuda.ExternalStream(_stream(stream, like), device=like.device)
-        ws.record_stream(s)
-    return like, norm, ws
+        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                         torch.cuda.ExternalStream(int(stream), device=like.device))
+    numel = array("q", sizes)
+    codes = array("i", [MOE_F32 if n32 == n else MOE_BF16]) * n if n32 in (0, n) else \
+        array("i", [MOE_F32 if d is torch.float32 else MOE_BF16 for d in dtypes])
+    args = (ptrs.buffer_info()[0],)
+    if max_norm is not None:
+        args += (outs.buffer_info()[0],)
+    args += (numel.buffer_info()[0], codes.buffer_info()[0], n)
+    if max_norm is not None:
+        args += (float(max_norm),)
+    _abi.check(fn, getattr(L, fn)(*args, _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(),
+                                  _stream(stream, like)))
+    return norm
 
 
 def moe_grad_norm(grads: Sequence[torch.Tensor], *, norm: Optional[torch.Tensor] = None,
                   workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The L2 norm over all gradients (float32 or bfloat16, any mix), as a
     float32 [1] device tensor."""
-    like, norm, ws = _grad_call(grads, norm, workspace, stream)
-    ptrs, numel, types = _grad_list("grads", grads)
-    _abi.check("moe_grad_norm", lib().moe_grad_norm(
-        ptrs, numel, types, len(grads), _ptr(norm), _ptr(ws), ws.numel() * ws.element_size(),
-        _stream(stream, like)))
-    return norm
+    return _grad_call("moe_grad_norm", grads, None, None, norm, workspace, stream)
 
 
 def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *,
@@ -520,19 +542,9 @@ def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *,
                        norm: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)), in place or
-    into `out`.  Returns the norm before it, float32 [1] on the device."""
-    like, norm, ws = _grad_call(grads, norm, workspace, stream)
-    if out is None:
-        out = grads
-    elif len(out) != len(grads) or any(o.dtype != g.dtype or o.shape != g.shape
-                                       for o, g in zip(out, grads)):
-        raise ValueError("out must have the types and shapes of grads")
-    ptrs, numel, types = _grad_list("grads", grads)
-    outs = ptrs if out is grads else (ctypes.c_void_p * len(out))(*[_ptr(t) for t in out])
-    _abi.check("moe_clip_grad_norm", lib().moe_clip_grad_norm(
-        ptrs, outs, numel, types, len(grads), float(max_norm), _ptr(norm), _ptr(ws),
-        ws.numel() * ws.element_size(), _stream(stream, like)))
-    return norm
+    into `out` (tensors of the same types and sizes).  Returns the norm before
+    it, float32 [1] on the device."""
+    return _grad_call("moe_clip_grad_norm", grads, max_norm, out, norm, workspace, stream)
 
 
 def moe_device_errors() -> int:

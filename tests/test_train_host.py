@@ -114,6 +114,6 @@ def test_binding_checks():
     with pytest.raises(TypeError, match="float32 or bfloat16"):
         moe.moe_grad_norm([torch.zeros(4, dtype=torch.float16)],
                           workspace=torch.zeros(1 << 20, dtype=torch.uint8))
-    with pytest.raises(ValueError, match="types and shapes"):
+    with pytest.raises(ValueError, match="types and sizes"):
         moe.moe_clip_grad_norm([torch.zeros(4)], 1.0, out=[torch.zeros(5)],
                                workspace=torch.zeros(1 << 20, dtype=torch.uint8))
