@@ -8,9 +8,12 @@
 // over twice: one launch sums squares, one scales.  Both walk the same chunks
 // (32 KB of one tensor each); the tensors' addresses, sizes and first chunks
 // travel in the kernel's parameters, so any mix of sizes is one launch and
-// nothing is copied to the device first.  Squares are summed in f32 inside a
-// thread and in f64 across threads, each CTA writes one partial sum, and
-// every CTA of the second launch adds the partials in the same order: the
+// nothing is copied to the device first.  Squares are summed in f32 in a fixed
+// tree: four sums a thread, then lanes, warps and CTAs (one partial sum each,
+// which every CTA of the second launch adds in the same order).  All terms are
+// positive and the longest chain is a few hundred additions at 4 GB, so the
+// norm is off by about 1e-7 of itself; f64 sums of the partials would cost the
+// second launch 110 us there (this part adds few f64 values a cycle).  The
 // result does not depend on timing and no CTA waits for another.  The second
 // pass walks the chunks backwards, so that what the first pass read last is
 // still in L2.
@@ -25,8 +28,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunkBytes = 32768;   // of a gradient, per CTA and step
-constexpr int kMaxPartials = 1216;   // partial sums of one call: 8 CTAs on 152 SMs
-constexpr double kEps = 1e-6;
+// CTAs of a launch, and partial sums of one call: four waves of 8 CTAs on 152
+// SMs.  SMs of this part do not move data at the same rate, so one wave waits
+// for the slowest: 4.54 GB of f32 gradients take 625 us for the norm (7.27
+// TB/s) and 1976 us for norm and clipping, against 741 and 2164 us in one.
+constexpr int kMaxPartials = 4 * 1216;
+constexpr float kEps = 1e-6f;
 
 // The tensors of one launch, passed by value.  Two sizes: a short parameter
 // block costs the launch less.
@@ -38,6 +45,7 @@ template <int N> struct Table {
     uint8_t f32[N];
     int64_t chunks;
     int n;
+    bool in_place;       // every output is its input
 };
 constexpr int kShort = 64, kLong = 512;
 
@@ -123,14 +131,14 @@ __device__ __forceinline__ void split(const Chunk &k, int &head, int &groups)
     groups = (k.n - head) / (16 / size);
 }
 
-__device__ __forceinline__ double block_sum(double v)
+__device__ __forceinline__ float block_sum(float v)
 {
-    __shared__ double s_warp[kThreads / 32];
+    __shared__ float s_warp[kThreads / 32];
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) s_warp[threadIdx.x >> 5] = v;
     __syncthreads();
-    double sum = 0.0;
+    float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) sum += s_warp[i];
     return sum;
@@ -138,7 +146,7 @@ __device__ __forceinline__ double block_sum(double v)
 
 template <int N>
 __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant__ Table<N> t,
-                                                           double *partial)
+                                                           float *partial)
 {
     griddep_wait();
     griddep_launch_dependents();
@@ -170,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
             s[2] = fmaf(f, f, s[2]);
         }
     }
-    const double sum = block_sum(((double)s[0] + s[1]) + ((double)s[2] + s[3]));
+    const float sum = block_sum((s[0] + s[1]) + (s[2] + s[3]));
     if (tid == 0) partial[blockIdx.x] = sum;
 }
 
@@ -178,22 +186,22 @@ __global__ void __launch_bounds__(kThreads) squares_kernel(const __grid_constant
 // scales.  max_norm < 0: the norm alone.
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-scale_kernel(const __grid_constant__ Table<N> t, const double *partial, int n_partial,
+scale_kernel(const __grid_constant__ Table<N> t, const float *partial, int n_partial,
              float max_norm, float *norm_out)
 {
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x;
-    double v = 0.0;
+    float v = 0.0f;
     for (int i = tid; i < n_partial; i += kThreads) v += partial[i];
-    const float norm = (float)sqrt(block_sum(v));
+    const float norm = sqrtf(block_sum(v));
     if (norm_out && blockIdx.x == 0 && tid == 0) *norm_out = norm;
     if (max_norm < 0.0f) return;
-    float c = (float)((double)max_norm / ((double)norm + kEps));
+    float c = max_norm / (norm + kEps);
     if (c > 1.0f) c = 1.0f;  // a NaN stays
+    if (c == 1.0f && t.in_place) return;  // the values are already there
     for (int64_t b = blockIdx.x; b < t.chunks; b += gridDim.x) {
         const Chunk k = chunk_of(t, t.chunks - 1 - b);
-        if (c == 1.0f && k.out == k.in) continue;  // the values are already there
         const int size = k.f32 ? 4 : 2;
         if ((reinterpret_cast<uintptr_t>(k.in) ^ reinterpret_cast<uintptr_t>(k.out)) & 15) {
             // input and output start at different places of a 16-byte group
@@ -230,12 +238,14 @@ int fill(Table<N> &t, const void *const *in, void *const *out, const int64_t *nu
 {
     t.n = 0;
     t.chunks = 0;
+    t.in_place = true;
     int i = i0;
     for (; i < n && t.n < N; ++i) {
         if (numel[i] == 0) continue;
         const bool f32 = dtype[i] == MOE_F32;
         t.in[t.n] = static_cast<const uint8_t *>(in[i]);
         t.out[t.n] = out ? static_cast<uint8_t *>(out[i]) : nullptr;
+        t.in_place = t.in_place && t.out[t.n] == t.in[t.n];
         t.numel[t.n] = numel[i];
         t.first[t.n] = t.chunks;
         t.f32[t.n] = f32;
@@ -248,7 +258,7 @@ int fill(Table<N> &t, const void *const *in, void *const *out, const int64_t *nu
 
 template <int N>
 int run(const void *const *in, void *const *out, const int64_t *numel, const int *dtype, int n,
-        float max_norm, float *norm, double *partial, cudaStream_t stream)
+        float max_norm, float *norm, float *partial, cudaStream_t stream)
 {
     const int launches = n <= N ? 1 : (n + N - 1) / N;
     const int per = kMaxPartials / launches > 0 ? kMaxPartials / launches : 1;
@@ -270,7 +280,7 @@ int run(const void *const *in, void *const *out, const int64_t *numel, const int
             grid = 1;  // the norm of nothing
         }
         e = launch_pdl(scale_kernel<N>, dim3(grid), dim3(kThreads), 0, stream, t,
-                       (const double *)partial, used, max_norm, l == 0 ? norm : nullptr);
+                       (const float *)partial, used, max_norm, l == 0 ? norm : nullptr);
         if (!out) break;
     }
     if (e != cudaSuccess) {
@@ -300,7 +310,7 @@ int check_and_run(const void *const *in, void *const *out, const int64_t *numel,
                              (out && (reinterpret_cast<uintptr_t>(out[i]) & mask))))
             return MOE_EALIGN;
     }
-    double *partial = static_cast<double *>(workspace);
+    float *partial = static_cast<float *>(workspace);
     return n <= kShort ? run<kShort>(in, out, numel, dtype, n, max_norm, norm, partial, stream)
                        : run<kLong>(in, out, numel, dtype, n, max_norm, norm, partial, stream);
 }
@@ -312,7 +322,7 @@ using namespace moe;
 
 MOE_EXPORT size_t moe_grad_norm_workspace_size(void)
 {
-    return (kMaxPartials * sizeof(double) + 255) / 256 * 256;
+    return (kMaxPartials * sizeof(float) + 255) / 256 * 256;
 }
 
 MOE_EXPORT int moe_grad_norm(const void *const *grads, const int64_t *numel, const int *dtype,

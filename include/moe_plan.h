@@ -474,9 +474,9 @@ int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N
  * Global L2 norm over many gradients, and clipping to a limit:
  *   norm[0] = sqrt(sum over all tensors of g^2)
  *   out[i]  = min(1, max_norm / (norm + 1e-6)) * grads[i], rounded once
- * Squares are summed in f32 within a thread and f64 across threads, in a
- * fixed order.  An infinite norm scales by 0 (an infinity becomes NaN); a NaN
- * anywhere makes every output NaN; the host sees neither without reading norm.
+ * Squares are summed in f32, in a fixed order.  An infinite norm scales by 0
+ * (an infinity becomes NaN); a NaN anywhere makes every output NaN; the host
+ * sees neither without reading norm.
  *
  * grads, out  HOST arrays of n DEVICE pointers (copied before the call
  *             returns); out[i] may be grads[i], and may not overlap any other

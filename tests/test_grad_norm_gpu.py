@@ -1,8 +1,8 @@
 """The global gradient norm and clipping against sums in 64 bits.
 
-A thread adds at most 64 squares to one f32 sum at these sizes (each addition
-off by 2^-24 of the sum, all terms positive) and the threads' sums are joined
-in 64 bits, so the norm is off by at most 64 * 2^-24 of itself; a clipped value
+A value passes through at most 64 f32 additions at these sizes (a thread's sum,
+then lanes, warps and CTAs), each off by 2^-24 of the sum, all terms positive,
+so the norm is off by at most 64 * 2^-24 of itself; a clipped value
 by that, four f32 roundings, and 2^-8 of it for bf16.
 """
 import math
