@@ -148,6 +148,26 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32])
         : "r"(addr));
 }
 
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+                 "%10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -289,7 +309,7 @@ __device__ __forceinline__ uint64_t now_ns()
 
 // Waits for phase `parity`; false once the limit ran out here or, with
 // `stop`, in another warp of the CTA.
-__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
 {
     // reading the timer costs about as much as a block of products: probe
     // first
@@ -314,13 +334,11 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
 // Orders what follows after the pair's writes before a phase that has passed.
 __device__ __forceinline__ void acquire_pair(uint64_t *bar, uint32_t parity)
 {
-    uint32_t done;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_u32(bar)), "r"(parity)
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "r"(parity)
         : "memory");
 }
 
@@ -340,6 +358,19 @@ struct Ring {
         at = (at + n) % kStages;  // the round is not kept
     }
 };
+
+// Parts of a tile's reduction that have an accumulator each.  The tensor core
+// cuts a sum's low bits off at every step of 16, which after 1048 products
+// leaves a relative error of 1e-6 in the 2-norm and grows with their number.
+// For f32 outputs at most 12 blocks (768 products) are summed there; the
+// storing warps add the parts in registers, rounding to nearest.  The bf16
+// outputs are rounded 1000 times more coarsely and take one accumulator.
+constexpr int kPartBlocks = 12;
+
+template <typename Tout> __device__ __forceinline__ int reduction_parts(int blocks)
+{
+    return sizeof(Tout) == 4 ? max(1, (blocks + kPartBlocks - 1) / kPartBlocks) : 1;
+}
 
 // --- tiles -------------------------------------------------------------------
 
@@ -515,161 +546,161 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     const int tiles = sched.start[a.E];
     constexpr bool kAMn = MODE != kForward, kBMn = MODE == kWeightGrad;
 
-    if (warp == 0 || warp == 2) {
-        const bool weights = warp == 0;  // the M side's operand, or the N side's
-        if (elect_one()) {
-            const uint32_t full = leader_addr(sh.full);
+    // In f32 a storing thread holds up to 128 sums.  The block starts with 384 x
+    // 168 = 64512 registers; 128 x 48 + 256 x 224 = 63488.
+    constexpr bool kSplit = sizeof(Tout) == 4;
+    if (warp < 4) {
+        if (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (warp == 0 || warp == 2) {
+            const bool weights = warp == 0;  // the M side's operand, or the N side's
+            if (elect_one()) {
+                const uint32_t full = leader_addr(sh.full);
+                Ring r;
+                int64_t j = 0;  // blocks copied
+                bool ok = true;
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                    const Tile c = tile_of<MODE>(a, sched, t);
+                    const int half = ceil_div(c.n, kStep) * (kStep / 2);
+                    const int m = c.m0 + rank * kLanes, n = c.n0 + rank * half;
+                    // the shortest box that holds this CTA's half of the columns
+                    const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+                    const int chunks = ceil_div(half, 64);
+                    const uint32_t bytes = weights              ? kABytes
+                                           : MODE == kWeightGrad ? chunks * 8192
+                                                                 : 2048 << size;
+                    for (int b = 0; b < c.blocks; ++b, ++j) {
+                        if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *sa = ring + r.at * kStageBytes, *sb = sa + kABytes;
+                        uint32_t bar = full + r.at * 8;
+                        if (MODE == kWeightGrad && b + 1 == c.blocks && c.last % 16) {
+                            bar = smem_u32(&sh.tail[r.at]);  // warp 3 clears rows and then arrives
+                            mbar_arrive_expect_tx(&sh.tail[r.at], bytes);
+                        } else {
+                            arrive_expect_at(bar, bytes);
+                        }
+                        const int k = b * kK;
+                        if (weights) {
+                            if (MODE == kForward) {
+                                tma_3d(sa, &maps.a, bar, k, m, c.e);
+                            } else if (MODE == kRowGrad) {
+                                tma_3d(sa, &maps.a, bar, m, k, c.e);
+                                tma_3d(sa + 8192, &maps.a, bar, m + 64, k, c.e);
+                            } else {
+                                tma_2d(sa, &maps.a, bar, m, c.row + k);
+                                tma_2d(sa + 8192, &maps.a, bar, m + 64, c.row + k);
+                            }
+                        } else if (MODE == kWeightGrad) {
+                            for (int i = 0; i < chunks; ++i)
+                                tma_2d(sb + i * 8192, &maps.b[0], bar, n + i * 64, c.row + k);
+                        } else {
+                            tma_2d(sb, &maps.b[size], bar, k, n);
+                        }
+                        r.next();
+                    }
+                }
+                if (!ok && rank == 0) {
+                    // leave no copy in flight: both CTAs' copies arrive here
+                    for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
+                        (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1 && rank == 0) {
             Ring r;
-            int64_t j = 0;  // blocks copied
+            int i = -1;  // accumulators begun, less one
             bool ok = true;
+            // an accumulator that the storing warps have read
+            auto begin = [&] {
+                ++i;
+                if (i >= 2 && !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop))
+                    return false;
+                tc_fence_after();
+                return true;
+            };
+            auto end = [&] {
+                if (elect_one()) mma_commit(&sh.acc_full[i & 1]);
+                __syncwarp();
+            };
             for (int t = pair; t < tiles && ok; t += pairs) {
                 const Tile c = tile_of<MODE>(a, sched, t);
-                const int half = ceil_div(c.n, kStep) * (kStep / 2);
-                const int m = c.m0 + rank * kLanes, n = c.n0 + rank * half;
-                // the shortest box that holds this CTA's half of the columns
-                const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
-                const int chunks = ceil_div(half, 64);
-                const uint32_t bytes = weights              ? kABytes
-                                       : MODE == kWeightGrad ? chunks * 8192
-                                                             : 2048 << size;
-                for (int b = 0; b < c.blocks; ++b, ++j) {
-                    if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
+                if (!begin()) break;
+                const int cols = ceil_div(c.n, kStep) * kStep;
+                const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
+                const int parts = reduction_parts<Tout>(c.blocks);
+                int part = 1, from = 0, until = c.blocks / parts;  // blocks of part 1
+                for (int b = 0; b < c.blocks; ++b) {
+                    if (sizeof(Tout) == 4 && b == until) {
+                        end();
+                        ++part;
+                        from = until;
+                        until = c.blocks * part / parts;
+                        ok = begin();
+                        if (!ok) break;
+                    }
+                    if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = ring + r.at * kStageBytes, *sb = sa + kABytes;
-                    uint32_t bar = full + r.at * 8;
-                    if (MODE == kWeightGrad && b + 1 == c.blocks && c.last % 16) {
-                        bar = smem_u32(&sh.tail[r.at]);  // warp 3 clears rows and then arrives
-                        mbar_arrive_expect_tx(&sh.tail[r.at], bytes);
-                    } else {
-                        arrive_expect_at(bar, bytes);
+                    uint8_t *sa = ring + r.at * kStageBytes;
+                    const int len = b + 1 == c.blocks ? c.last : kK;
+                    const int steps = ceil_div(len, 16);
+                    if (MODE == kWeightGrad && len % 16)
+                        acquire_pair(&sh.full[r.at], r.round);  // what either CTA cleared
+                    tc_fence_after();
+                    if (elect_one()) {
+                        const uint64_t da = operand_desc(smem_u32(sa), kAMn);
+                        const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
+                        for (int s = 0; s < steps; ++s)
+                            mma_bf16(tmem + (i & 1) * kN, da + s * (kAMn ? 128 : 2),
+                                     db + s * (kBMn ? 128 : 2), idesc, b > from || s > 0);
+                        mma_commit(&sh.empty[r.at]);
                     }
-                    const int k = b * kK;
-                    if (weights) {
-                        if (MODE == kForward) {
-                            tma_3d(sa, &maps.a, bar, k, m, c.e);
-                        } else if (MODE == kRowGrad) {
-                            tma_3d(sa, &maps.a, bar, m, k, c.e);
-                            tma_3d(sa + 8192, &maps.a, bar, m + 64, k, c.e);
-                        } else {
-                            tma_2d(sa, &maps.a, bar, m, c.row + k);
-                            tma_2d(sa + 8192, &maps.a, bar, m + 64, c.row + k);
-                        }
-                    } else if (MODE == kWeightGrad) {
-                        for (int i = 0; i < chunks; ++i)
-                            tma_2d(sb + i * 8192, &maps.b[0], bar, n + i * 64, c.row + k);
-                    } else {
-                        tma_2d(sb, &maps.b[size], bar, k, n);
-                    }
+                    __syncwarp();
                     r.next();
                 }
+                if (ok) end();
             }
-            if (!ok && rank == 0) {
-                // leave no copy in flight: both CTAs' copies arrive here
-                for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
-                    (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
-            }
-        }
-        __syncwarp();
-    } else if (warp == 1 && rank == 0) {
-        Ring r;
-        int i = 0;  // tiles done
-        bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs, ++i) {
-            const Tile c = tile_of<MODE>(a, sched, t);
-            const int buf = i & 1;
-            if (i >= 2 && !wait(&sh.acc_empty[buf], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) break;
-            tc_fence_after();
-            const int cols = ceil_div(c.n, kStep) * kStep;
-            const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
-            for (int b = 0; b < c.blocks; ++b) {
-                if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *sa = ring + r.at * kStageBytes;
-                const int len = b + 1 == c.blocks ? c.last : kK;
-                const int steps = ceil_div(len, 16);
-                if (MODE == kWeightGrad && len % 16)
-                    acquire_pair(&sh.full[r.at], r.round);  // what either CTA cleared
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t da = operand_desc(smem_u32(sa), kAMn);
-                    const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
-                    for (int s = 0; s < steps; ++s)
-                        mma_bf16(tmem + buf * kN, da + s * (kAMn ? 128 : 2),
-                                 db + s * (kBMn ? 128 : 2), idesc, b > 0 || s > 0);
-                    mma_commit(&sh.empty[r.at]);
-                }
-                __syncwarp();
-                r.next();
-            }
-            if (ok && elect_one()) mma_commit(&sh.acc_full[buf]);
+            if (elect_one()) mma_commit(&sh.drain);  // nothing is issued after this
             __syncwarp();
-        }
-        if (elect_one()) mma_commit(&sh.drain);  // nothing is issued after this
-        __syncwarp();
-    } else if (warp == 3) {
-        if (MODE != kWeightGrad) {
-            zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
-                      blockIdx.x, gridDim.x);
-        } else {
-            Ring r;
-            uint32_t rounds = 0;  // parity of each stage's next tail
-            for (int t = pair; t < tiles; t += pairs) {
-                const Tile c = tile_of<MODE>(a, sched, t);
-                if (c.blocks && c.last % 16) {
-                    r.skip(c.blocks - 1);
-                    if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
-                    rounds ^= 1u << r.at;
-                    clear_tail(ring + r.at * kStageBytes, c.last);
-                    if (lane < 2) arrive_release_at(leader_addr(&sh.full[r.at]));
-                    r.next();
-                } else {
-                    r.skip(c.blocks);
+        } else if (warp == 3) {
+            if (MODE != kWeightGrad) {
+                zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
+                          blockIdx.x, gridDim.x);
+            } else {
+                Ring r;
+                uint32_t rounds = 0;  // parity of each stage's next tail
+                for (int t = pair; t < tiles; t += pairs) {
+                    const Tile c = tile_of<MODE>(a, sched, t);
+                    if (c.blocks && c.last % 16) {
+                        r.skip(c.blocks - 1);
+                        if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
+                        rounds ^= 1u << r.at;
+                        clear_tail(ring + r.at * kStageBytes, c.last);
+                        if (lane < 2) arrive_release_at(leader_addr(&sh.full[r.at]));
+                        r.next();
+                    } else {
+                        r.skip(c.blocks);
+                    }
                 }
             }
         }
-    } else if (warp >= 4) {
+    } else {
+        if (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int q = warp & 3;
         constexpr int kBoxRows = B::kRows;
         const int odd = warp >> 2 & 1;  // this warp's blocks of 32 columns: even or odd ones
         Tout *box = reinterpret_cast<Tout *>(boxes + (warp - 4) * kBoxArea);
         int i = 0, turn = 0;
-        for (int t = pair; t < tiles; t += pairs, ++i) {
+        for (int t = pair; t < tiles; t += pairs) {
             const Tile c = tile_of<MODE>(a, sched, t);
-            const int buf = i & 1;
-            if (!wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)) break;
-            tc_fence_after();
             const int m = c.m0 + rank * kLanes + q * 32;
-            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kN;
-            const int last = (ceil_div(c.n, 32) - 1 - odd) / 2;  // the last one, if any
-            uint32_t v[2][32];
-            if (c.n > odd * 32) {
-                tmem_load(acc + odd * 32, v[0]);
-            } else {
-                tc_fence_before();
-                if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
-            }
-#pragma unroll
-            for (int k = 0; k < kN / 64; ++k) {
-                const int n = k * 64 + odd * 32;
-                if (n >= c.n) break;
-                uint32_t(&r)[32] = v[k & 1];
-                tmem_wait(r);
-                if (k < last) {
-                    tmem_load(acc + n + 64, v[(k + 1) & 1]);
-                } else {  // the accumulator is read: the next products may have it
-                    tc_fence_before();
-                    if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
-                }
-                if (MODE == kWeightGrad && c.blocks == 0) {
-                    // an expert without rows: no product was issued
-#pragma unroll
-                    for (int x = 0; x < 32; ++x) r[x] = 0;
-                }
-                if (m >= a.M) continue;
+            const int last = (ceil_div(c.n, 32) - 1 - odd) / 2;  // last block, if any
+            // columns n .. n + 32 of the output, from registers
+            auto store = [&](int n, const uint32_t(&r)[32]) {
+                if (m >= a.M) return;
 #pragma unroll
                 for (int h = 0; h < 32; h += kBoxRows) {
                     if (n + h >= c.n) break;
@@ -692,12 +723,85 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         Tout *out = reinterpret_cast<Tout *>(a.out) +
                                     (int64_t)(c.n0 + n + h) * a.M + m + lane;
 #pragma unroll
-                        for (int x = 0; x < kBoxRows; ++x)
+                        for (int x = 0; x < kBoxRows; ++x, out += a.M)
                             if (n + h + x < c.n)
-                                out[(int64_t)x * a.M] =
-                                    round_to<Tout>(__uint_as_float(r[h + x]));
+                                *out = round_to<Tout>(__uint_as_float(r[h + x]));
                     }
                 }
+            };
+            // this warp's blocks of accumulator i, each read while the one
+            // before is stored; then the next products may have it
+            auto store_all = [&] {
+                const int buf = i & 1;
+                if (!wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)) return false;
+                tc_fence_after();
+                ++i;
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kN;
+                uint32_t v[2][32];
+                if (c.n > odd * 32) {
+                    tmem_load(acc + odd * 32, v[0]);
+                } else {
+                    tc_fence_before();
+                    if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                }
+#pragma unroll
+                for (int k = 0; k < kN / 64; ++k) {
+                    const int n = k * 64 + odd * 32;
+                    if (n >= c.n) break;
+                    tmem_wait(v[k & 1]);
+                    if (k < last) {
+                        tmem_load(acc + n + 64, v[(k + 1) & 1]);
+                    } else {
+                        tc_fence_before();
+                        if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                    }
+                    if (MODE == kWeightGrad && c.blocks == 0) {
+                        // an expert without rows: no product was issued
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) v[k & 1][x] = 0;
+                    }
+                    store(n, v[k & 1]);
+                }
+                return true;
+            };
+            const int parts = reduction_parts<Tout>(c.blocks);
+            if (sizeof(Tout) == 4 && parts > 1) {
+                uint32_t sum[kN / 64][32];  // f32
+#pragma unroll
+                for (int k = 0; k < kN / 64; ++k)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) sum[k][x] = 0;
+                bool ok = true;
+                for (int p = 0; p < parts; ++p, ++i) {
+                    const int buf = i & 1;
+                    ok = wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc =
+                        tmem + ((uint32_t)(q * 32) << 16) + buf * kN + odd * 32;
+#pragma unroll
+                    for (int k = 0; k < kN / 64; ++k) {
+                        if (k * 64 + odd * 32 >= c.n) break;
+#pragma unroll
+                        for (int h = 0; h < 32; h += 16) {
+                            uint32_t v[16];
+                            tmem_load(acc + k * 64 + h, v);
+                            tmem_wait(v);
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                sum[k][h + x] = __float_as_uint(__uint_as_float(sum[k][h + x]) +
+                                                                __uint_as_float(v[x]));
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < kN / 64; ++k) store(k * 64 + odd * 32, sum[k]);
+            } else if (!store_all()) {
+                break;
             }
             __syncwarp();
         }
