@@ -472,10 +472,10 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Sc
 
 // --- the kernel ----------------------------------------------------------------
 
-// Operand maps: the M side's, and the N side's with boxes of 16, 32, 64 and 128
-// rows (weights' gradient: the first only, boxes of 64 x 64).
+// Operand maps: the M side's, and the N side's with boxes of 16, 32, .. 128 rows
+// (weights' gradient: the first only, boxes of 64 x 64).
 struct Maps {
-    CUtensorMap a, b[4];
+    CUtensorMap a, b[8];
     CUtensorMap out;   // stored boxes
 };
 
@@ -562,12 +562,11 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     const Tile c = tile_of<MODE>(a, sched, t);
                     const int half = ceil_div(c.n, kStep) * (kStep / 2);
                     const int m = c.m0 + rank * kLanes, n = c.n0 + rank * half;
-                    // the shortest box that holds this CTA's half of the columns
-                    const int size = half > 64 ? 3 : half > 32 ? 2 : half > 16 ? 1 : 0;
+                    const int size = half / 16 - 1;  // the box of just this many rows
                     const int chunks = ceil_div(half, 64);
                     const uint32_t bytes = weights              ? kABytes
                                            : MODE == kWeightGrad ? chunks * 8192
-                                                                 : 2048 << size;
+                                                                 : half * 128;
                     for (int b = 0; b < c.blocks; ++b, ++j) {
                         if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
                             ok = false;
@@ -636,7 +635,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         end();
                         ++part;
                         from = until;
-                        until = c.blocks * part / parts;
+                        until = (int)((int64_t)c.blocks * part / parts);
                         ok = begin();
                         if (!ok) break;
                     }
@@ -893,16 +892,15 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
     if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_EINVAL;
     if (rows < 0 || rows >= ((int64_t)1 << 31) || E < 1 || E > 1024) return MOE_EINVAL;
     if (N < 1 || D < 1 || N >= (1 << 24) || D >= (1 << 24)) return MOE_EINVAL;
+    if (MODE != kWeightGrad && rows == 0) return MOE_OK;  // no rows, no output
     if (!cnt || !off || !out || (rows > 0 && (!rows_a || !other))) return MOE_EINVAL;
-    if (MODE != kWeightGrad && !other) return MOE_EINVAL;
     const int64_t M = MODE == kForward ? N : D;
     const int64_t mt = (M + kM - 1) / kM;
     const int64_t most = MODE == kWeightGrad ? mt * ((N + kN - 1) / kN) * E
                                              : mt * (rows / kN + (rows < E ? rows : E));
-    if (most >= ((int64_t)1 << 31)) return MOE_EINVAL;
+    if (most >= ((int64_t)1 << 30)) return MOE_EINVAL;
     if (N % 8 || D % 8 || !aligned16(rows_a) || !aligned16(other) || !aligned16(out))
         return MOE_EALIGN;
-    if (MODE != kWeightGrad && rows == 0) return MOE_OK;
     ExpertArgs a = {};
     a.cnt = cnt;
     a.off = off;
@@ -920,8 +918,8 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         if (rows > 0 && e == cudaSuccess) e = make_map(&maps.b[0], rows_a, N, rows, 0, 64);
     } else {
         e = make_map(&maps.a, other, D, N, E, MODE == kForward ? kLanes : 64);
-        for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-            e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 << i);
+        for (int i = 0; i < 8 && e == cudaSuccess; ++i)
+            e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 * (i + 1));
     }
     const int box_rows = out_dtype == MOE_F32 ? Boxes<MODE, float>::kRows
                                               : Boxes<MODE, __nv_bfloat16>::kRows;

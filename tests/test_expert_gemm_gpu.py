@@ -240,3 +240,18 @@ def test_a_bucket_outside_the_rows_is_left_out():
     assert moe.moe_device_errors() == 32
     assert torch.equal(out[:8], want[:8])
     assert moe.moe_device_errors() == 0
+
+
+def test_the_most_experts_and_no_rows():
+    import combine_moe_plan_02_gb300 as moe
+    plan, rows = make_plan([e % 3 for e in range(1024)], 0, 0)
+    for op in ("y", "dx", "dw"):
+        a, b = operands(op, plan, rows, 40, 72, 3)
+        assert torch.equal(call(op, plan, a, b, F32), reference(op, plan, a, b).to(F32))
+    none, _ = make_plan([0] * 4)
+    x, dy, w = (torch.empty(0, 64, dtype=BF16, device="cuda"),
+                torch.empty(0, 32, dtype=BF16, device="cuda"), ints((4, 32, 64), 1))
+    assert moe.moe_expert_gemm(x, w, none).shape == (0, 32)
+    assert moe.moe_expert_gemm_dgrad(dy, w, none).shape == (0, 64)
+    dw = call("dw", none, dy, x, F32)
+    assert dw.shape == (4, 32, 64) and not dw.any()
