@@ -13,6 +13,13 @@
 // step's loads issued before the first product; its K sums stay in registers
 // in f32 and the CTA joins them in a fixed order (lanes by shuffles, then
 // warps in increasing order), so dw does not depend on timing.
+//
+// Bound by memory: 4096 tokens, K = 8, H = 7168 in bf16 move 999 MB in 148 us
+// (6.74 TB/s; 151 us without the streaming hint on bf16 stores, which costs f32
+// rows 2 us), 4096 x 4096 in f32 with 12 % padding 1198 MB in 182 us (6.59
+// TB/s).  The block scheduler hands tokens to whichever SM is free.  CTAs of
+// 256 threads at these sizes: 158 us (bf16).  With few tokens a CTA takes up to
+// 512 threads, to spread a token's row.
 
 #include "common.cuh"
 
@@ -23,7 +30,10 @@ namespace {
 
 constexpr int kEntries = 8;        // entries of a token held in registers at a time
 constexpr int kMaxThreads = 512;
-constexpr int kGapCtas = 152;      // CTAs that clear the rows without an entry
+// CTAs that clear the rows without an entry.  They come first in the grid: at
+// its end they ran alone, and 75 MB of padding in 604 MB of rows cost 197
+// instead of 182 us (608 of them: 190 us).
+constexpr int kGapCtas = 152;
 
 __device__ uint32_t g_backward_error;  // kErrCombineIndex
 
@@ -62,7 +72,7 @@ template <> struct Vec<__nv_bfloat16, 8> {
             __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * q], f[2 * q + 1]);
             u[q] = *reinterpret_cast<uint32_t *>(&b);
         }
-        st16(p, make_uint4(u[0], u[1], u[2], u[3]));
+        st16_cs(p, make_uint4(u[0], u[1], u[2], u[3]));
     }
 };
 template <> struct Vec<__nv_bfloat16, 4> {
@@ -122,16 +132,16 @@ __global__ void __launch_bounds__(kMaxThreads) combine_backward_kernel(BackwardA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int64_t row_bytes = a.H * (int)sizeof(Ty);
 
-    if (blockIdx.x >= a.S) {
-        zero_gaps(a.dy, row_bytes, a.rows, a.cnt, a.off, a.E,
-                  (int)(blockIdx.x - a.S) * warps + warp, (int)(gridDim.x - a.S) * warps);
+    if (blockIdx.x < kGapCtas) {
+        zero_gaps(a.dy, row_bytes, a.rows, a.cnt, a.off, a.E, (int)blockIdx.x * warps + warp,
+                  kGapCtas * warps);
         return;
     }
 
     __shared__ int64_t s_at[kEntries];
     __shared__ float s_w[kEntries];
     __shared__ float s_part[kMaxThreads / 32][kEntries];
-    const int64_t s = blockIdx.x;
+    const int64_t s = (int64_t)blockIdx.x - kGapCtas;
     const uint8_t *dout = a.dout + s * a.H * (int)sizeof(Td);
     const int steps = (int)(a.H / N);
 
