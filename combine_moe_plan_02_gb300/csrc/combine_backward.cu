@@ -30,10 +30,10 @@ namespace {
 
 constexpr int kEntries = 8;        // entries of a token held in registers at a time
 constexpr int kMaxThreads = 512;
-// CTAs that clear the rows without an entry.  They come first in the grid: at
-// its end they ran alone, and 75 MB of padding in 604 MB of rows cost 197
-// instead of 182 us (608 of them: 190 us).
-constexpr int kGapCtas = 152;
+// CTAs that clear the rows without an entry, one for each MB of dy up to one per
+// SM.  They come first in the grid: at its end they ran alone, and 75 MB of
+// padding in 604 MB of rows cost 197 instead of 182 us (608 of them: 190 us).
+constexpr int kMaxGapCtas = 152;
 
 __device__ uint32_t g_backward_error;  // kErrCombineIndex
 
@@ -46,6 +46,7 @@ struct BackwardArgs {
     const int64_t *off;      // [E + 1] first rows of the buckets
     int64_t S, H, rows;
     int K, E;
+    int gap_ctas;
     uint8_t *dy;             // [rows, H]
     float *dw;               // [S, K]
 };
@@ -132,16 +133,16 @@ __global__ void __launch_bounds__(kMaxThreads) combine_backward_kernel(BackwardA
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int64_t row_bytes = a.H * (int)sizeof(Ty);
 
-    if (blockIdx.x < kGapCtas) {
+    if ((int)blockIdx.x < a.gap_ctas) {
         zero_gaps(a.dy, row_bytes, a.rows, a.cnt, a.off, a.E, (int)blockIdx.x * warps + warp,
-                  kGapCtas * warps);
+                  a.gap_ctas * warps);
         return;
     }
 
     __shared__ int64_t s_at[kEntries];
     __shared__ float s_w[kEntries];
     __shared__ float s_part[kMaxThreads / 32][kEntries];
-    const int64_t s = (int64_t)blockIdx.x - kGapCtas;
+    const int64_t s = (int64_t)blockIdx.x - a.gap_ctas;
     const uint8_t *dout = a.dout + s * a.H * (int)sizeof(Td);
     const int steps = (int)(a.H / N);
 
@@ -209,7 +210,7 @@ int launch_backward(const BackwardArgs &a, cudaStream_t stream)
     int threads = 128;
     while (threads < kMaxThreads && threads < steps && a.S * threads < (int64_t)sm_count() * 1024)
         threads *= 2;
-    cudaError_t e = launch_pdl(combine_backward_kernel<Td, Ty>, dim3((unsigned)(a.S + kGapCtas)),
+    cudaError_t e = launch_pdl(combine_backward_kernel<Td, Ty>, dim3((unsigned)(a.S + a.gap_ctas)),
                                dim3(threads), 0, stream, a);
     if (e != cudaSuccess) {
         set_cuda_error(e);
@@ -252,6 +253,8 @@ MOE_EXPORT int moe_combine_backward(const void *dout, int dout_dtype, const void
     a.E = E;
     a.dy = static_cast<uint8_t *>(dy);
     a.dw = dw;
+    const int64_t mb = (y_rows * H * (y_dtype == MOE_BF16 ? 2 : 4) >> 20) + 1;
+    a.gap_ctas = (int)(mb < kMaxGapCtas ? mb : kMaxGapCtas);
     cudaStream_t st = (cudaStream_t)stream;
     if (y_dtype == MOE_BF16)
         return dout_dtype == MOE_BF16 ? launch_backward<__nv_bfloat16, __nv_bfloat16>(a, st)

@@ -319,25 +319,33 @@ __device__ __forceinline__ void zero_gaps(uint8_t *base, int64_t row_bytes, int6
 {
     const int lane = threadIdx.x & 31;
     int64_t seen = 0;
-    for (int e0 = 0; e0 <= E; e0 += 32) {
-        const int e = e0 + lane;
-        int64_t first = 0, n = 0;
-        if (e <= E) {
-            const int64_t b = __ldg(off + e);
-            first = e < E ? b + max(__ldg(cnt + e), 0) : b;
-            first = min(max(first, (int64_t)0), rows);
-            const int64_t end = e < E ? min(__ldg(off + e + 1), rows) : rows;
-            n = max(end - first, (int64_t)0);
-        }
-        for (unsigned m = __ballot_sync(0xffffffffu, n > 0); m; m &= m - 1) {
-            const int64_t f = __shfl_sync(0xffffffffu, first, __ffs(m) - 1);
-            const int64_t c = __shfl_sync(0xffffffffu, n, __ffs(m) - 1);
-            for (int64_t i = (gw - seen % W + W) % W; i < c; i += W) {
-                uint8_t *row = base + (f + i) * row_bytes;
-                for (int64_t o = lane * 16; o < row_bytes; o += 512)
-                    st16(row + o, make_uint4(0, 0, 0, 0));
+    constexpr int kAhead = 4;  // groups of 32 buckets looked up at once
+    for (int e0 = 0; e0 <= E; e0 += 32 * kAhead) {
+        int64_t first[kAhead], n[kAhead];
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) {
+            const int e = e0 + g * 32 + lane;
+            first[g] = n[g] = 0;
+            if (e <= E) {
+                const int64_t b = __ldg(off + e);
+                const int64_t end = e < E ? min(__ldg(off + e + 1), rows) : rows;
+                first[g] = e < E ? b + max(__ldg(cnt + e), 0) : b;
+                first[g] = min(max(first[g], (int64_t)0), rows);
+                n[g] = max(end - first[g], (int64_t)0);
             }
-            seen += c;
+        }
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) {
+            for (unsigned m = __ballot_sync(0xffffffffu, n[g] > 0); m; m &= m - 1) {
+                const int64_t f = __shfl_sync(0xffffffffu, first[g], __ffs(m) - 1);
+                const int64_t c = __shfl_sync(0xffffffffu, n[g], __ffs(m) - 1);
+                for (int64_t i = (gw - seen % W + W) % W; i < c; i += W) {
+                    uint8_t *row = base + (f + i) * row_bytes;
+                    for (int64_t o = lane * 16; o < row_bytes; o += 512)
+                        st16(row + o, make_uint4(0, 0, 0, 0));
+                }
+                seen += c;
+            }
         }
     }
 }
