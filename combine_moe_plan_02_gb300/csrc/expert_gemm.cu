@@ -71,15 +71,16 @@ struct ExpertArgs {
     uint8_t *out;
 };
 
-// Stored boxes: 32 outputs wide, kBoxRows columns of the accumulator high, each
+// Stored boxes: 32 outputs wide, kRows columns of the accumulator high, each
 // storing warp with room for kTurns of them.  The weights' gradient has few
-// products for each output and is often bound by these stores.  Its bf16 rows
-// are 64 bytes, so a box costs its fixed part: 256 buckets of 33 rows, 1024 x
-// 2048, take 186 us in boxes of 32 rows and 250 us in two of 16 (f32: 361 us
-// in boxes of 8, 379 us in 16).  Where rows are columns, a box holds whole
-// columns of one bucket and the rest leaves row by row: 16.
+// products for each output and is often bound by these stores, where a box
+// costs its fixed part: 256 buckets of 33 rows, 1024 x 2048, in bf16 take 186 us
+// in boxes of 32 rows and 250 us in 16; 64 ragged buckets of 512, 2048 x 7168,
+// in f32 780 us in boxes of 16, 798 us in two of 8 and 1114 us in four of 4.
+// Where rows are columns, a box holds whole columns of one bucket and the rest
+// leaves row by row: 16.
 template <int MODE, typename Tout> struct Boxes {
-    static constexpr int kRows = MODE != kWeightGrad ? 16 : sizeof(Tout) == 2 ? 32 : 8;
+    static constexpr int kRows = MODE == kWeightGrad && sizeof(Tout) == 2 ? 32 : 16;
     static constexpr int kBytes = kRows * 32 * (int)sizeof(Tout);
     static constexpr int kTurns = kBoxArea / kBytes;
 };
