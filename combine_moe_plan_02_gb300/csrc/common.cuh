@@ -318,10 +318,12 @@ __device__ __forceinline__ void zero_gaps(uint8_t *base, int64_t row_bytes, int6
                                           int W)
 {
     const int lane = threadIdx.x & 31;
-    int64_t seen = 0;
+    int64_t seen = 0;        // such rows in the groups before
+    int64_t next = gw;       // the next one that this warp clears
     constexpr int kAhead = 4;  // groups of 32 buckets looked up at once
     for (int e0 = 0; e0 <= E; e0 += 32 * kAhead) {
-        int64_t first[kAhead], n[kAhead];
+        int64_t first[kAhead];
+        int n[kAhead];
 #pragma unroll
         for (int g = 0; g < kAhead; ++g) {
             const int e = e0 + g * 32 + lane;
@@ -331,21 +333,26 @@ __device__ __forceinline__ void zero_gaps(uint8_t *base, int64_t row_bytes, int6
                 const int64_t end = e < E ? min(__ldg(off + e + 1), rows) : rows;
                 first[g] = e < E ? b + max(__ldg(cnt + e), 0) : b;
                 first[g] = min(max(first[g], (int64_t)0), rows);
-                n[g] = max(end - first[g], (int64_t)0);
+                n[g] = (int)max(end - first[g], (int64_t)0);  // rows are below 2^31
             }
         }
 #pragma unroll
         for (int g = 0; g < kAhead; ++g) {
-            for (unsigned m = __ballot_sync(0xffffffffu, n[g] > 0); m; m &= m - 1) {
-                const int64_t f = __shfl_sync(0xffffffffu, first[g], __ffs(m) - 1);
-                const int64_t c = __shfl_sync(0xffffffffu, n[g], __ffs(m) - 1);
-                for (int64_t i = (gw - seen % W + W) % W; i < c; i += W) {
-                    uint8_t *row = base + (f + i) * row_bytes;
-                    for (int64_t o = lane * 16; o < row_bytes; o += 512)
-                        st16(row + o, make_uint4(0, 0, 0, 0));
-                }
-                seen += c;
+            int64_t upto = n[g];  // rows of this lane's bucket and those before it
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
             }
+            const int64_t total = __shfl_sync(0xffffffffu, upto, 31);
+            for (; next < seen + total; next += W) {
+                const int64_t i = next - seen;
+                const int at = __popc(__ballot_sync(0xffffffffu, upto <= i));
+                const int64_t row = __shfl_sync(0xffffffffu, first[g] + n[g] - upto, at) + i;
+                for (int64_t o = lane * 16; o < row_bytes; o += 512)
+                    st16(base + row * row_bytes + o, make_uint4(0, 0, 0, 0));
+            }
+            seen += total;
         }
     }
 }
