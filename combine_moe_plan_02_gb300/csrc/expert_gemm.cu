@@ -30,9 +30,22 @@
 // wait and an arrival as much again, against 512 cycles of products a block),
 // warp 1 of the first CTA issues the matrix instructions, warp 3 clears the
 // rows of the output that belong to no bucket (weights' gradient: the staged
-// rows past a bucket's end), warps 4 to 11 store.  Two
-// accumulators of 256 columns let the stores of a tile overlap the next tile's
-// products.  Every wait is bounded.
+// rows past a bucket's end), warps 4 to 11 store.  Two accumulators of 256
+// columns let the stores of a tile overlap the next tile's products.  Every
+// wait is bounded.
+//
+// What bounds it, 64 buckets of 512 rows, 2048 x 7168, bf16 out: 552 us forward,
+// 554 us for the rows (1743, 1735 TFLOP/s; 87 % of the tensor pipe's cycles),
+// the copies from L2: six stages of 32 KB are what fits, with four it takes 618
+// us, without the tokens' copies 499 us.  For seconds on end the power limit
+// sets the pace: 619 us.  Buckets of 512 rows on average, half of them cut into
+// three parts: 595 us (670 us for seconds).  The weights' gradient: 600 us in
+// bf16 (1603 TFLOP/s), 780 us in f32, where 4.36 GB move and products, copies
+// and stores share L2 and shared memory.  One row in each of 8 buckets, 2048 x
+// 6144: 36 us, the weights at 6.3 TB/s behind 4 us of launch and tile list; 1024
+// rows in 256 buckets: 945 us (6.7 TB/s).  64 pairs' work taken over by cluster
+// launch control instead of the fixed walk measured 1 % slower, tiles of 512
+// columns 33 % (the next tile waits for both accumulators' stores).
 
 #include "common.cuh"
 
@@ -79,10 +92,19 @@ struct ExpertArgs {
 // in f32 780 us in boxes of 16, 798 us in two of 8 and 1114 us in four of 4.
 // Where rows are columns, a box holds whole columns of one bucket and the rest
 // leaves row by row: 16.
-template <int MODE, typename Tout> struct Boxes {
+//
+// JOIN = 4 puts the four quarters of the lanes into one box, for a large bf16
+// weights' gradient whose rows are not a multiple of 32 bytes: every row of a
+// box then begins and ends inside a sector, and a sector written in parts costs
+// most where the output does not stay in L2.  128 buckets of 62 rows, 1904 x
+// 6952 (3.4 GB): 729 us, and 1186 us in boxes of one warp; 512 x 2952 (387 MB):
+// 96 and 113 us; 344 x 2952 (260 MB): 75 and 68 us.  Where rows are whole
+// sectors one warp's boxes cost less: 1904 x 6976, 693 and 611 us.
+template <int MODE, typename Tout, int JOIN> struct Boxes {
     static constexpr int kRows = MODE == kWeightGrad && sizeof(Tout) == 2 ? 32 : 16;
-    static constexpr int kBytes = kRows * 32 * (int)sizeof(Tout);
-    static constexpr int kTurns = kBoxArea / kBytes;
+    static constexpr int kWidth = 32 * JOIN;
+    static constexpr int kBytes = kRows * kWidth * (int)sizeof(Tout);
+    static constexpr int kTurns = JOIN * kBoxArea / kBytes;
 };
 
 // --- tcgen05 ---------------------------------------------------------------
@@ -508,13 +530,13 @@ template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(flo
     return __float2bfloat16_rn(f);
 }
 
-template <int MODE, typename Tout>
+template <int MODE, typename Tout, int JOIN>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    using B = Boxes<MODE, Tout>;
+    using B = Boxes<MODE, Tout, JOIN>;
     uint8_t *boxes = ring + kStages * kStageBytes;
     int *lists = reinterpret_cast<int *>(boxes + kStoreWarps * kBoxArea);
     Schedule sched = {lists, lists + a.E + 1, lists + 2 * a.E + 1, 0};
@@ -692,7 +714,16 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         const int q = warp & 3;
         constexpr int kBoxRows = B::kRows;
         const int odd = warp >> 2 & 1;  // this warp's blocks of 32 columns: even or odd ones
-        Tout *box = reinterpret_cast<Tout *>(boxes + (warp - 4) * kBoxArea);
+        // the box's first storing warp and this one's place in it
+        const int member = q % JOIN;
+        Tout *box = reinterpret_cast<Tout *>(boxes + (warp - 4 - member) * kBoxArea);
+        const bool issuer = member == 0 && lane == 0;
+        auto meet = [&] {
+            if (JOIN == 1)
+                __syncwarp();
+            else
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + odd), "n"(32 * JOIN) : "memory");
+        };
         int i = 0, turn = 0;
         for (int t = pair; t < tiles; t += pairs) {
             const Tile c = tile_of<MODE>(a, sched, t);
@@ -700,22 +731,24 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             const int last = (ceil_div(c.n, 32) - 1 - odd) / 2;  // last block, if any
             // columns n .. n + 32 of the output, from registers
             auto store = [&](int n, const uint32_t(&r)[32]) {
-                if (m >= a.M) return;
+                const int m_box = m - member * 32;  // the same for all warps of a box
+                if (m_box >= a.M) return;
 #pragma unroll
                 for (int h = 0; h < 32; h += kBoxRows) {
                     if (n + h >= c.n) break;
                     if (MODE == kWeightGrad || n + h + kBoxRows <= c.n) {
-                        Tout *b = box + turn * (kBoxRows * 32);
+                        Tout *b = box + turn * (kBoxRows * B::kWidth);
                         if (++turn == B::kTurns) turn = 0;
-                        if (lane == 0) bulk_wait_read<B::kTurns - 1>();
-                        __syncwarp();
+                        if (issuer) bulk_wait_read<B::kTurns - 1>();
+                        meet();
 #pragma unroll
                         for (int x = 0; x < kBoxRows; ++x)
-                            b[x * 32 + lane] = round_to<Tout>(__uint_as_float(r[h + x]));
+                            b[x * B::kWidth + member * 32 + lane] =
+                                round_to<Tout>(__uint_as_float(r[h + x]));
                         fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            tma_store(&maps.out, b, m, c.n0 + n + h, c.e, MODE == kWeightGrad);
+                        meet();
+                        if (issuer) {
+                            tma_store(&maps.out, b, m_box, c.n0 + n + h, c.e, MODE == kWeightGrad);
                             bulk_commit();
                         }
                     } else if (m + lane < a.M) {
@@ -805,7 +838,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             }
             __syncwarp();
         }
-        if (lane == 0) bulk_wait_all();
+        if (issuer) bulk_wait_all();
         __syncwarp();
     }
     tc_fence_before();
@@ -866,15 +899,15 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t 
     return encode(map, base, false, width, rows, depth, 64, box_rows, true);
 }
 
-template <int MODE, typename Tout>
+template <int MODE, typename Tout, int JOIN>
 int launch_expert(const Maps &maps, const ExpertArgs &a, int grid, cudaStream_t stream)
 {
     static KernelCache kc;
     const size_t smem = 1024 + kStages * kStageBytes + kStoreWarps * kBoxArea +
                         (3 * (size_t)a.E + 1) * sizeof(int);
-    cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout>, smem, kThreads, kc, nullptr);
+    cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout, JOIN>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess)
-        e = launch_pdl(expert_kernel<MODE, Tout>, dim3(grid), dim3(kThreads), smem, stream, maps,
+        e = launch_pdl(expert_kernel<MODE, Tout, JOIN>, dim3(grid), dim3(kThreads), smem, stream, maps,
                        a);
     if (e != cudaSuccess) {
         set_cuda_error(e);
@@ -922,21 +955,23 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         for (int i = 0; i < 8 && e == cudaSuccess; ++i)
             e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 * (i + 1));
     }
-    const int box_rows = out_dtype == MOE_F32 ? Boxes<MODE, float>::kRows
-                                              : Boxes<MODE, __nv_bfloat16>::kRows;
+    const bool f32 = out_dtype == MOE_F32;
+    const bool join = MODE == kWeightGrad && !f32 && D % 16 && E * N * D * 2 > (320 << 20);
+    const int box_rows = f32 ? Boxes<MODE, float, 1>::kRows : Boxes<MODE, __nv_bfloat16, 1>::kRows;
+    const int box = join ? 128 : 32;
     if (e == cudaSuccess)
-        e = MODE == kWeightGrad
-                ? encode(&maps.out, out, out_dtype == MOE_F32, D, N, E, 32, box_rows, false)
-                : encode(&maps.out, out, out_dtype == MOE_F32, M, rows, 0, 32, box_rows, false);
+        e = MODE == kWeightGrad ? encode(&maps.out, out, f32, D, N, E, box, box_rows, false)
+                                : encode(&maps.out, out, f32, M, rows, 0, box, box_rows, false);
     if (e != cudaSuccess) {
         set_cuda_error(e);
         return MOE_ECUDA;
     }
     const int pairs = sm_count() / 2;
     const int grid = 2 * (int)(most < pairs ? most : pairs);
-    return out_dtype == MOE_BF16
-               ? launch_expert<MODE, __nv_bfloat16>(maps, a, grid, stream)
-               : launch_expert<MODE, float>(maps, a, grid, stream);
+    if (f32) return launch_expert<MODE, float, 1>(maps, a, grid, stream);
+    if constexpr (MODE == kWeightGrad)
+        if (join) return launch_expert<MODE, __nv_bfloat16, 4>(maps, a, grid, stream);
+    return launch_expert<MODE, __nv_bfloat16, 1>(maps, a, grid, stream);
 }
 
 } // namespace

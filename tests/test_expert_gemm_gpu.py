@@ -255,3 +255,13 @@ def test_the_most_experts_and_no_rows():
     assert moe.moe_expert_gemm_dgrad(dy, w, none).shape == (0, 64)
     dw = call("dw", none, dy, x, F32)
     assert dw.shape == (4, 32, 64) and not dw.any()
+
+
+def test_large_weights_with_rows_of_odd_sixteenths():
+    """A bf16 weights' gradient of 390 MB whose rows are not whole 32-byte
+    sectors (stored in wider boxes), with ragged and empty buckets and sizes
+    that end inside a box."""
+    plan, rows = make_plan([(7 * e) % 75 for e in range(96)], 0, 3)
+    a, b = operands("dw", plan, rows, 712, 2856, 4)
+    got = call("dw", plan, a, b, BF16)
+    assert torch.equal(got, reference("dw", plan, a, b).to(F32).to(BF16))
