@@ -425,27 +425,42 @@ __device__ __forceinline__ int bucket_tiles(const ExpertArgs &a, int fill)
 
 template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a, Schedule &s, int t)
 {
-    while (t >= s.start[s.cursor + 1]) ++s.cursor;
     Tile r;
-    r.e = s.cursor;
+    if (MODE == kWeightGrad) {
+        r.e = t / bucket_tiles<MODE>(a, 0);  // every bucket has as many
+    } else {
+        // the last bucket that begins at or before t: often near, but steps of
+        // 76 tiles pass many buckets of one tile
+        int past = s.cursor + 4;
+        while (s.cursor < past && t >= s.start[s.cursor + 1]) ++s.cursor;
+        if (t >= s.start[s.cursor + 1]) {
+            past = a.E;
+            while (past - s.cursor > 1) {
+                const int mid = (s.cursor + past) >> 1;
+                if (s.start[mid] <= t) s.cursor = mid;
+                else past = mid;
+            }
+        }
+        r.e = s.cursor;
+    }
     const int local = t - s.start[r.e], fill = s.fill[r.e];
     r.row = s.first[r.e];
     if (MODE == kWeightGrad) {
         const int mt = ceil_div(a.M, kM);
-        r.m0 = local % mt * kM;
-        r.n0 = local / mt * kN;
+        const int n = local / mt;
+        r.m0 = (local - n * mt) * kM;
+        r.n0 = n * kN;
         r.n = min(kN, a.N - r.n0);
         r.blocks = ceil_div(fill, kK);
         r.last = fill - (r.blocks - 1) * kK;
     } else {
-        const int parts = ceil_div(fill, kN);
-        const int steps = ceil_div(fill, kStep);
-        const int i = local % parts;
-        const int from = (int)((int64_t)steps * i / parts) * kStep;
-        const int to = (int)((int64_t)steps * (i + 1) / parts) * kStep;
-        r.m0 = local / parts * kM;
+        const int parts = ceil_div(fill, kN), steps = ceil_div(fill, kStep);
+        const int m = local / parts, i = local - m * parts;
+        const int each = steps / parts, longer = steps - each * parts;
+        const int from = (i * each + min(i, longer)) * kStep;
+        r.m0 = m * kM;
         r.n0 = r.row + from;
-        r.n = min(to, fill) - from;
+        r.n = min((each + (i < longer)) * kStep, fill - from);
         r.blocks = ceil_div(a.K, kK);
         r.last = a.K - (r.blocks - 1) * kK;
     }
