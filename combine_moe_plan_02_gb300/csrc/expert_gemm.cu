@@ -64,8 +64,8 @@ constexpr int kK = 64;              // reduction block: 128 bytes of bf16
 constexpr int kStep = 32;           // columns come in these steps, half of them from each CTA
 constexpr int kABytes = kLanes * kK * 2;
 constexpr int kBBytes = kN / 2 * kK * 2;
-constexpr int kStageBytes = kABytes + kBBytes;
-constexpr int kStages = 6;
+constexpr int kRingBytes = 6 * (kABytes + kBBytes);
+constexpr int kMaxStages = 10;
 constexpr int kBoxArea = 2048;      // of each storing warp
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
 
@@ -367,18 +367,19 @@ __device__ __forceinline__ void acquire_pair(uint64_t *bar, uint32_t parity)
 
 // A place in the ring and the parity of its current round.
 struct Ring {
-    int at = 0;
+    int stages, at = 0;
     uint32_t round = 0;
+    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
     __device__ __forceinline__ void next()
     {
-        if (++at == kStages) {
+        if (++at == stages) {
             at = 0;
             round ^= 1;
         }
     }
     __device__ __forceinline__ void skip(int n)
     {
-        at = (at + n) % kStages;  // the round is not kept
+        at = (at + n) % stages;  // the round is not kept
     }
 };
 
@@ -413,6 +414,7 @@ struct Schedule {
     int *start;   // [E + 1] first tile of each bucket
     int *first;   // [E] first row
     int *fill;    // [E] rows
+    int widest;   // rows of the largest bucket
     int cursor;   // bucket of the last tile asked for; tiles are asked for in order
 };
 
@@ -468,11 +470,11 @@ template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a,
 }
 
 // Lists the tiles: every thread of the CTA takes part.
-template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Schedule &s)
+template <int MODE> __device__ void build_schedule(const ExpertArgs &a, Schedule &s)
 {
-    __shared__ int s_warp[kThreads / 32];
+    __shared__ int s_warp[kThreads / 32], s_most[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int base = 0;
+    int base = 0, most = 0;
     for (int e0 = 0; e0 < a.E; e0 += kThreads) {
         const int e = e0 + tid;
         int tiles = 0;
@@ -485,6 +487,7 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Sc
             }
             s.first[e] = (int)f;
             s.fill[e] = (int)c;
+            most = max(most, (int)c);
             tiles = bucket_tiles<MODE>(a, (int)c);
         }
         int sum = tiles;
@@ -505,7 +508,10 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, const Sc
         __syncthreads();
     }
     if (tid == 0) s.start[0] = 0;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_most[warp] = most;
     __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) s.widest = max(s.widest, s_most[w]);
 }
 
 // --- the kernel ----------------------------------------------------------------
@@ -518,9 +524,9 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2], drain;
-    uint64_t tail[kStages];  // a last block, until the rows past its end are cleared
+    uint64_t tail[kMaxStages];  // a last block, until the rows past its end are cleared
     uint32_t tmem;
     volatile int stop;
 };
@@ -552,16 +558,16 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     using B = Boxes<MODE, Tout, JOIN>;
-    uint8_t *boxes = ring + kStages * kStageBytes;
+    uint8_t *boxes = ring + kRingBytes;
     int *lists = reinterpret_cast<int *>(boxes + kStoreWarps * kBoxArea);
-    Schedule sched = {lists, lists + a.E + 1, lists + 2 * a.E + 1, 0};
+    Schedule sched = {lists, lists + a.E + 1, lists + 2 * a.E + 1, 0, 0};
     __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cluster_rank();
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh.full[i], 4);   // both operands of both CTAs
             mbar_init(&sh.empty[i], 1);
             mbar_init(&sh.tail[i], 2);
@@ -582,6 +588,12 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int tiles = sched.start[a.E];
+    // Six stages of 128 + 128 rows.  Buckets of a few rows need less of a stage,
+    // and more of them keep more of the weights in flight.
+    const int rows_b =
+        MODE == kWeightGrad ? kN / 2 : min(kN / 2, ceil_div(sched.widest, kStep) * (kStep / 2));
+    const int stage_bytes = kABytes + rows_b * 128;
+    const int stages = min(kMaxStages, kRingBytes / stage_bytes);
     constexpr bool kAMn = MODE != kForward, kBMn = MODE == kWeightGrad;
 
     // In f32 a storing thread holds up to 128 sums.  The block starts with 384 x
@@ -593,7 +605,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             const bool weights = warp == 0;  // the M side's operand, or the N side's
             if (elect_one()) {
                 const uint32_t full = leader_addr(sh.full);
-                Ring r;
+                Ring r(stages);
                 int64_t j = 0;  // blocks copied
                 bool ok = true;
                 for (int t = pair; t < tiles && ok; t += pairs) {
@@ -606,11 +618,11 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                                            : MODE == kWeightGrad ? chunks * 8192
                                                                  : half * 128;
                     for (int b = 0; b < c.blocks; ++b, ++j) {
-                        if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
+                        if (j >= stages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
                             ok = false;
                             break;
                         }
-                        uint8_t *sa = ring + r.at * kStageBytes, *sb = sa + kABytes;
+                        uint8_t *sa = ring + r.at * stage_bytes, *sb = sa + kABytes;
                         uint32_t bar = full + r.at * 8;
                         if (MODE == kWeightGrad && b + 1 == c.blocks && c.last % 16) {
                             bar = smem_u32(&sh.tail[r.at]);  // warp 3 clears rows and then arrives
@@ -640,13 +652,13 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 }
                 if (!ok && rank == 0) {
                     // leave no copy in flight: both CTAs' copies arrive here
-                    for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
-                        (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
+                    for (int64_t i = j > stages ? j - stages : 0; i < j; ++i)
+                        (void)wait_slow(&sh.full[i % stages], (uint32_t)(i / stages) & 1, nullptr);
                 }
             }
             __syncwarp();
         } else if (warp == 1 && rank == 0) {
-            Ring r;
+            Ring r(stages);
             int i = -1;  // accumulators begun, less one
             bool ok = true;
             // an accumulator that the storing warps have read
@@ -681,7 +693,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = ring + r.at * kStageBytes;
+                    uint8_t *sa = ring + r.at * stage_bytes;
                     const int len = b + 1 == c.blocks ? c.last : kK;
                     const int steps = ceil_div(len, 16);
                     if (MODE == kWeightGrad && len % 16)
@@ -707,7 +719,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
                           blockIdx.x, gridDim.x);
             } else {
-                Ring r;
+                Ring r(stages);
                 uint32_t rounds = 0;  // parity of each stage's next tail
                 for (int t = pair; t < tiles; t += pairs) {
                     const Tile c = tile_of<MODE>(a, sched, t);
@@ -715,7 +727,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         r.skip(c.blocks - 1);
                         if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
                         rounds ^= 1u << r.at;
-                        clear_tail(ring + r.at * kStageBytes, c.last);
+                        clear_tail(ring + r.at * stage_bytes, c.last);
                         if (lane < 2) arrive_release_at(leader_addr(&sh.full[r.at]));
                         r.next();
                     } else {
@@ -918,7 +930,7 @@ template <int MODE, typename Tout, int JOIN>
 int launch_expert(const Maps &maps, const ExpertArgs &a, int grid, cudaStream_t stream)
 {
     static KernelCache kc;
-    const size_t smem = 1024 + kStages * kStageBytes + kStoreWarps * kBoxArea +
+    const size_t smem = 1024 + kRingBytes + kStoreWarps * kBoxArea +
                         (3 * (size_t)a.E + 1) * sizeof(int);
     cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout, JOIN>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess)
