@@ -23,6 +23,10 @@
 // memory, so a pair reads 64 KB per block of 64 along the reduction where two
 // single CTAs of 128 x 256 read 96 KB.
 //
+// Where a call of few rows has fewer tiles than half of the pairs, two or four
+// pairs of a cluster share a tile's reduction; the first adds the others' sums,
+// which they write into its shared memory, in a fixed order.  Otherwise:
+//
 // A pair is persistent (one per two SMs) and walks the tiles of all buckets,
 // which it lists itself from cnt and off: the sizes stay on the device.  Warps
 // 0 and 2 copy the operands' blocks of 64 along the reduction with TMA into a
@@ -39,11 +43,11 @@
 // the copies from L2: six stages of 32 KB are what fits, with four it takes 618
 // us, without the tokens' copies 499 us.  For seconds on end the power limit
 // sets the pace: 619 us.  Buckets of 512 rows on average, half of them cut into
-// three parts: 595 us (670 us for seconds).  The weights' gradient: 600 us in
+// three parts: 590 us (670 us for seconds).  The weights' gradient: 600 us in
 // bf16 (1603 TFLOP/s), 780 us in f32, where 4.36 GB move and products, copies
 // and stores share L2 and shared memory.  One row in each of 8 buckets, 2048 x
-// 6144: 36 us, the weights at 6.3 TB/s behind 4 us of launch and tile list; 1024
-// rows in 256 buckets: 945 us (6.7 TB/s).  64 pairs' work taken over by cluster
+// 6144: 35 us, the weights at 6.5 TB/s behind 4 us of launch and tile list; 1024
+// rows in 256 buckets: 885 us (7.3 TB/s).  64 pairs' work taken over by cluster
 // launch control instead of the fixed walk measured 1 % slower, tiles of 512
 // columns 33 % (the next tile waits for both accumulators' stores).
 
@@ -67,6 +71,8 @@ constexpr int kBBytes = kN / 2 * kK * 2;
 constexpr int kRingBytes = 6 * (kABytes + kBBytes);
 constexpr int kMaxStages = 10;
 constexpr int kBoxArea = 2048;      // of each storing warp
+constexpr int kSplitRows = 64;      // rows of a call whose reductions may be split
+constexpr int kSplitBytes = kSplitRows * kLanes * 4;  // one pair's sums, in each CTA
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
 
 __device__ uint32_t g_expert_error;  // kErrExpertTimeout | kErrExpertBucket
@@ -81,6 +87,7 @@ struct ExpertArgs {
     int M;                // contiguous output dimension
     int N;                // rows of a weight (weights' gradient)
     int K;                // reduction length (the other two)
+    int split;            // pairs that share a tile's reduction
     uint8_t *out;
 };
 
@@ -134,14 +141,14 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         : "memory");
 }
 
-// Arrives on `bar` of both CTAs when the matrix instructions issued so far are
-// done.
-__device__ __forceinline__ void mma_commit(uint64_t *bar)
+// Arrives on `bar` of both CTAs of the pair (`lead` is the first one's rank) when
+// the matrix instructions issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t lead)
 {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
         "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
+        "h"((uint16_t)(3u << lead))
         : "memory");
 }
 
@@ -240,11 +247,11 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
-// The address of a shared variable in the first CTA of the pair.
-__device__ __forceinline__ uint32_t leader_addr(const void *p)
+// The address of a shared variable in the CTA of that rank.
+__device__ __forceinline__ uint32_t addr_in(const void *p, uint32_t rank)
 {
     uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
 
@@ -402,6 +409,7 @@ struct Tile {
     int e, m0;
     int n0;       // first column: a row of the packed rows, or a row of dw[e]
     int n;        // columns that are stored
+    int from;     // first reduction block
     int blocks;   // reduction blocks
     int last;     // reduction length of the last block (1..64)
     int row;      // first row of the bucket (weights' gradient)
@@ -453,6 +461,7 @@ template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a,
         r.m0 = (local - n * mt) * kM;
         r.n0 = n * kN;
         r.n = min(kN, a.N - r.n0);
+        r.from = 0;
         r.blocks = ceil_div(fill, kK);
         r.last = fill - (r.blocks - 1) * kK;
     } else {
@@ -463,10 +472,20 @@ template <int MODE> __device__ __forceinline__ Tile tile_of(const ExpertArgs &a,
         r.m0 = m * kM;
         r.n0 = r.row + from;
         r.n = min((each + (i < longer)) * kStep, fill - from);
+        r.from = 0;
         r.blocks = ceil_div(a.K, kK);
         r.last = a.K - (r.blocks - 1) * kK;
     }
     return r;
+}
+
+// Leaves one pair's part of a tile's reduction.
+__device__ __forceinline__ void take_part(Tile &c, int part, int parts)
+{
+    const int to = c.blocks * (part + 1) / parts;
+    c.from = c.blocks * part / parts;
+    if (to < c.blocks) c.last = kK;
+    c.blocks = to - c.from;
 }
 
 // Lists the tiles: every thread of the CTA takes part.
@@ -551,8 +570,8 @@ template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(flo
     return __float2bfloat16_rn(f);
 }
 
-template <int MODE, typename Tout, int JOIN>
-__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+template <int MODE, typename Tout, int JOIN, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
 expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -564,8 +583,10 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
-    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    // the CTA's place in the pair, the pair's first CTA and place in the cluster
+    const uint32_t cta = cluster_rank(), rank = cta & 1, lead = cta & ~1u;
+    const int part = SPLIT ? (int)(cta >> 1) : 0, split = SPLIT ? a.split : 1;
+    const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh.full[i], 4);   // both operands of both CTAs
@@ -587,7 +608,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     cluster_sync();                  // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int tiles = sched.start[a.E];
+    // (a split grid has a cluster for each tile that disjoint buckets can have)
+    const int tiles = SPLIT ? min(sched.start[a.E], pairs) : sched.start[a.E];
     // Six stages of 128 + 128 rows.  Buckets of a few rows need less of a stage,
     // and more of them keep more of the weights in flight.
     const int rows_b =
@@ -598,18 +620,19 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 
     // In f32 a storing thread holds up to 128 sums.  The block starts with 384 x
     // 168 = 64512 registers; 128 x 48 + 256 x 224 = 63488.
-    constexpr bool kSplit = sizeof(Tout) == 4;
+    constexpr bool kRegs = sizeof(Tout) == 4;
     if (warp < 4) {
-        if (kSplit) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        if (kRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 0 || warp == 2) {
             const bool weights = warp == 0;  // the M side's operand, or the N side's
             if (elect_one()) {
-                const uint32_t full = leader_addr(sh.full);
+                const uint32_t full = addr_in(sh.full, lead);
                 Ring r(stages);
                 int64_t j = 0;  // blocks copied
                 bool ok = true;
                 for (int t = pair; t < tiles && ok; t += pairs) {
-                    const Tile c = tile_of<MODE>(a, sched, t);
+                    Tile c = tile_of<MODE>(a, sched, t);
+                    if (SPLIT) take_part(c, part, split);
                     const int half = ceil_div(c.n, kStep) * (kStep / 2);
                     const int m = c.m0 + rank * kLanes, n = c.n0 + rank * half;
                     const int size = half / 16 - 1;  // the box of just this many rows
@@ -630,7 +653,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         } else {
                             arrive_expect_at(bar, bytes);
                         }
-                        const int k = b * kK;
+                        const int k = (c.from + b) * kK;
                         if (weights) {
                             if (MODE == kForward) {
                                 tma_3d(sa, &maps.a, bar, k, m, c.e);
@@ -670,22 +693,23 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 return true;
             };
             auto end = [&] {
-                if (elect_one()) mma_commit(&sh.acc_full[i & 1]);
+                if (elect_one()) mma_commit(&sh.acc_full[i & 1], lead);
                 __syncwarp();
             };
             for (int t = pair; t < tiles && ok; t += pairs) {
-                const Tile c = tile_of<MODE>(a, sched, t);
+                Tile c = tile_of<MODE>(a, sched, t);
+                if (SPLIT) take_part(c, part, split);
                 if (!begin()) break;
                 const int cols = ceil_div(c.n, kStep) * kStep;
                 const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
                 const int parts = reduction_parts<Tout>(c.blocks);
-                int part = 1, from = 0, until = c.blocks / parts;  // blocks of part 1
+                int p = 1, from = 0, until = c.blocks / parts;  // blocks of part 1
                 for (int b = 0; b < c.blocks; ++b) {
                     if (sizeof(Tout) == 4 && b == until) {
                         end();
-                        ++part;
+                        ++p;
                         from = until;
-                        until = (int)((int64_t)c.blocks * part / parts);
+                        until = (int)((int64_t)c.blocks * p / parts);
                         ok = begin();
                         if (!ok) break;
                     }
@@ -705,14 +729,14 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         for (int s = 0; s < steps; ++s)
                             mma_bf16(tmem + (i & 1) * kN, da + s * (kAMn ? 128 : 2),
                                      db + s * (kBMn ? 128 : 2), idesc, b > from || s > 0);
-                        mma_commit(&sh.empty[r.at]);
+                        mma_commit(&sh.empty[r.at], lead);
                     }
                     __syncwarp();
                     r.next();
                 }
                 if (ok) end();
             }
-            if (elect_one()) mma_commit(&sh.drain);  // nothing is issued after this
+            if (elect_one()) mma_commit(&sh.drain, lead);  // nothing is issued after this
             __syncwarp();
         } else if (warp == 3) {
             if (MODE != kWeightGrad) {
@@ -728,7 +752,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
                         rounds ^= 1u << r.at;
                         clear_tail(ring + r.at * stage_bytes, c.last);
-                        if (lane < 2) arrive_release_at(leader_addr(&sh.full[r.at]));
+                        if (lane < 2) arrive_release_at(addr_in(&sh.full[r.at], lead));
                         r.next();
                     } else {
                         r.skip(c.blocks);
@@ -736,8 +760,13 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 }
             }
         }
+        __syncwarp();
+        if (SPLIT) {
+            cluster_sync();
+            cluster_sync();
+        }
     } else {
-        if (kSplit) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        if (kRegs) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int q = warp & 3;
         constexpr int kBoxRows = B::kRows;
         const int odd = warp >> 2 & 1;  // this warp's blocks of 32 columns: even or odd ones
@@ -752,8 +781,9 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + odd), "n"(32 * JOIN) : "memory");
         };
         int i = 0, turn = 0;
-        for (int t = pair; t < tiles; t += pairs) {
-            const Tile c = tile_of<MODE>(a, sched, t);
+        for (int t = pair; SPLIT || t < tiles; t += pairs) {
+            Tile c = {};
+            if (!SPLIT || t < tiles) c = tile_of<MODE>(a, sched, t);
             const int m = c.m0 + rank * kLanes + q * 32;
             const int last = (ceil_div(c.n, 32) - 1 - odd) / 2;  // last block, if any
             // columns n .. n + 32 of the output, from registers
@@ -789,6 +819,54 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     }
                 }
             };
+            if constexpr (SPLIT) {
+                // One tile a cluster, of at most 64 columns: a block a warp.  Each
+                // pair sums its part of the reduction; the first one adds the
+                // others' in their order.
+                take_part(c, part, split);
+                const int n = odd * 32;
+                uint32_t sum[32] = {};  // f32
+                bool ok = true;
+                for (int p = c.n ? reduction_parts<Tout>(c.blocks) : 0; p > 0 && ok; --p, ++i) {
+                    const int buf = i & 1;
+                    ok = wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t v[32];
+                    tmem_load(tmem + ((uint32_t)(q * 32) << 16) + buf * kN + n, v);
+                    tmem_wait(v);
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        sum[x] = __float_as_uint(__uint_as_float(sum[x]) + __uint_as_float(v[x]));
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(addr_in(&sh.acc_empty[buf], lead));
+                }
+                // the ring of every pair is idle now and takes the others' sums
+                cluster_sync();
+                const uint32_t place = (uint32_t)(n * kLanes + q * 32 + lane) * 4;
+                if (part > 0 && ok && n < c.n) {
+                    const uint32_t to = addr_in(ring, rank) + (part - 1) * kSplitBytes + place;
+#pragma unroll
+                    for (int x = 0; x < 32; ++x)
+                        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + x * kLanes * 4),
+                                     "r"(sum[x])
+                                     : "memory");
+                }
+                cluster_sync();
+                if (part == 0 && ok && n < c.n) {
+                    for (int o = 0; o + 1 < split; ++o) {
+                        const uint8_t *from = ring + o * kSplitBytes + place;
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            sum[x] = __float_as_uint(
+                                __uint_as_float(sum[x]) +
+                                *reinterpret_cast<const float *>(from + x * kLanes * 4));
+                    }
+                    store(n, sum);
+                }
+                break;
+            }
             // this warp's blocks of accumulator i, each read while the one
             // before is stored; then the next products may have it
             auto store_all = [&] {
@@ -802,7 +880,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     tmem_load(acc + odd * 32, v[0]);
                 } else {
                     tc_fence_before();
-                    if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                    if (lane == 0) arrive_at(addr_in(&sh.acc_empty[buf], lead));
                 }
 #pragma unroll
                 for (int k = 0; k < kN / 64; ++k) {
@@ -813,7 +891,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         tmem_load(acc + n + 64, v[(k + 1) & 1]);
                     } else {
                         tc_fence_before();
-                        if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                        if (lane == 0) arrive_at(addr_in(&sh.acc_empty[buf], lead));
                     }
                     if (MODE == kWeightGrad && c.blocks == 0) {
                         // an expert without rows: no product was issued
@@ -825,7 +903,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 return true;
             };
             const int parts = reduction_parts<Tout>(c.blocks);
-            if (sizeof(Tout) == 4 && parts > 1) {
+            if constexpr (SPLIT) {
+            } else if (sizeof(Tout) == 4 && parts > 1) {
                 uint32_t sum[kN / 64][32];  // f32
 #pragma unroll
                 for (int k = 0; k < kN / 64; ++k)
@@ -855,7 +934,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) arrive_at(leader_addr(&sh.acc_empty[buf]));
+                    if (lane == 0) arrive_at(addr_in(&sh.acc_empty[buf], lead));
                 }
                 if (!ok) break;
 #pragma unroll
@@ -926,16 +1005,31 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t 
     return encode(map, base, false, width, rows, depth, 64, box_rows, true);
 }
 
-template <int MODE, typename Tout, int JOIN>
-int launch_expert(const Maps &maps, const ExpertArgs &a, int grid, cudaStream_t stream)
+// Launches `clusters` clusters of as many pairs as share a tile.
+template <int MODE, typename Tout, int JOIN, bool SPLIT = false>
+int launch_expert(const Maps &maps, const ExpertArgs &a, int clusters, cudaStream_t stream)
 {
     static KernelCache kc;
+    auto kernel = expert_kernel<MODE, Tout, JOIN, SPLIT>;
     const size_t smem = 1024 + kRingBytes + kStoreWarps * kBoxArea +
                         (3 * (size_t)a.E + 1) * sizeof(int);
-    cudaError_t e = prepare_kernel(expert_kernel<MODE, Tout, JOIN>, smem, kThreads, kc, nullptr);
-    if (e == cudaSuccess)
-        e = launch_pdl(expert_kernel<MODE, Tout, JOIN>, dim3(grid), dim3(kThreads), smem, stream, maps,
-                       a);
+    cudaError_t e = prepare_kernel(kernel, smem, kThreads, kc, nullptr);
+    if (e == cudaSuccess) {
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = MOE_USE_PDL;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2 * a.split;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * a.split * clusters);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, kernel, maps, a);
+    }
     if (e != cudaSuccess) {
         set_cuda_error(e);
         return MOE_ECUDA;
@@ -967,6 +1061,7 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
     a.off = off;
     a.rows = rows;
     a.E = E;
+    a.split = 1;
     a.M = (int)M;
     a.N = (int)N;
     a.K = (int)(MODE == kForward ? D : N);
@@ -993,12 +1088,27 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         set_cuda_error(e);
         return MOE_ECUDA;
     }
+    if constexpr (MODE != kWeightGrad) {
+        // A few rows of a few small experts fill a fraction of the pairs, each
+        // streaming its tile's weights at what its own copies in flight allow.
+        // The pairs of a cluster then share a tile's reduction: 15 clusters of four
+        // pairs run at once, or 36 of two.  One row in each of 6 buckets, 472 x
+        // 4000: 17.7 -> 10.5 us (four pairs); two in each of 8, 1024 x 4096: 18.2
+        // -> 13.7 us (two); with 16 and 8 blocks of reduction nothing is lost (1312
+        // long: 9.3 -> 8.9 us).
+        const int blocks = ceil_div(a.K, kK);
+        if (rows <= kSplitRows && most <= 36 && blocks >= 8) {
+            a.split = most <= 15 && blocks >= 16 ? 4 : 2;
+            return f32 ? launch_expert<MODE, float, 1, true>(maps, a, (int)most, stream)
+                       : launch_expert<MODE, __nv_bfloat16, 1, true>(maps, a, (int)most, stream);
+        }
+    }
     const int pairs = sm_count() / 2;
-    const int grid = 2 * (int)(most < pairs ? most : pairs);
-    if (f32) return launch_expert<MODE, float, 1>(maps, a, grid, stream);
+    const int clusters = (int)(most < pairs ? most : pairs);
+    if (f32) return launch_expert<MODE, float, 1>(maps, a, clusters, stream);
     if constexpr (MODE == kWeightGrad)
-        if (join) return launch_expert<MODE, __nv_bfloat16, 4>(maps, a, grid, stream);
-    return launch_expert<MODE, __nv_bfloat16, 1>(maps, a, grid, stream);
+        if (join) return launch_expert<MODE, __nv_bfloat16, 4>(maps, a, clusters, stream);
+    return launch_expert<MODE, __nv_bfloat16, 1>(maps, a, clusters, stream);
 }
 
 } // namespace

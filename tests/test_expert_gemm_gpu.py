@@ -265,3 +265,25 @@ def test_large_weights_with_rows_of_odd_sixteenths():
     a, b = operands("dw", plan, rows, 712, 2856, 4)
     got = call("dw", plan, a, b, BF16)
     assert torch.equal(got, reference("dw", plan, a, b).to(F32).to(BF16))
+
+
+@pytest.mark.parametrize("op", ["y", "dx"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("counts,out,length,cap,tail", [
+    ([1], 8, 1024, 0, 0),                       # the fewest rows, the shortest reduction
+    ([1, 0, 2], 600, 1032, 0, 0),               # nine tiles, four pairs each
+    ([64], 256, 4104, 0, 0),                    # the most rows
+    ([33, 31], 1280, 2048, 0, 0),               # ten tiles, blocks of 33 and 31 rows
+    ([3, 0, 1, 4], 1000, 520, 0, 0),            # 32 tiles, two pairs each
+    ([2, 5], 264, 3000, 6, 3),                  # padded, rows after the last bucket
+    ([0, 0, 0], 64, 1024, 0, 7),                # no tile at all
+])
+def test_few_rows_share_a_reduction(op, dtype, counts, out, length, cap, tail):
+    plan, rows = make_plan(counts, cap, tail)
+    N, D = (out, length) if op == "y" else (length, out)
+    a, b = operands(op, plan, rows, N, D, 7)
+    got = call(op, plan, a, b, dtype)
+    want = reference(op, plan, a, b)
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(got, want.to(F32).to(dtype))
+    assert torch.equal(got, call(op, plan, a, b, dtype))
