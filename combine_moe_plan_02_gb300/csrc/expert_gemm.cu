@@ -780,6 +780,20 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             else
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + odd), "n"(32 * JOIN) : "memory");
         };
+        // whether all of them go on: one that gave up must not leave the others
+        // at their next meeting
+        auto agree = [&](bool ok) {
+            if (JOIN == 1) return ok;
+            uint32_t all;
+            asm volatile("{\n\t.reg .pred p, q;\n\t"
+                         "setp.ne.u32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, %2, %3, p;\n\t"
+                         "selp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all)
+                         : "r"((uint32_t)ok), "r"(1 + odd), "n"(32 * JOIN)
+                         : "memory");
+            return all != 0;
+        };
         int i = 0, turn = 0;
         for (int t = pair; SPLIT || t < tiles; t += pairs) {
             Tile c = {};
@@ -871,7 +885,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             // before is stored; then the next products may have it
             auto store_all = [&] {
                 const int buf = i & 1;
-                if (!wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)) return false;
+                if (!agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop)))
+                    return false;
                 tc_fence_after();
                 ++i;
                 const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kN;
@@ -903,8 +918,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 return true;
             };
             const int parts = reduction_parts<Tout>(c.blocks);
-            if constexpr (SPLIT) {
-            } else if (sizeof(Tout) == 4 && parts > 1) {
+            if (sizeof(Tout) == 4 && parts > 1) {
                 uint32_t sum[kN / 64][32];  // f32
 #pragma unroll
                 for (int k = 0; k < kN / 64; ++k)

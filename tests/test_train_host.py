@@ -77,11 +77,12 @@ def test_grad_norm_validation(L):
 
 def test_binding_checks():
     import combine_moe_plan_02_gb300 as moe
-    bf, f32 = torch.bfloat16, torch.float32
+    bf = torch.bfloat16
     plan = moe.Plan(torch.zeros(4, dtype=torch.int32), torch.zeros(5, dtype=torch.int64),
                     torch.zeros(6, dtype=torch.int32), torch.zeros(3, 2, dtype=torch.int64),
                     torch.zeros(1, dtype=torch.int32))
-    x, w, dy = torch.zeros(6, 16, dtype=bf), torch.zeros(4, 8, 16, dtype=bf), torch.zeros(6, 8, dtype=bf)
+    x, w = torch.zeros(6, 16, dtype=bf), torch.zeros(4, 8, 16, dtype=bf)
+    dy = torch.zeros(6, 8, dtype=bf)
     with pytest.raises(TypeError, match="bfloat16"):
         moe.moe_expert_gemm(x.float(), w, plan)
     with pytest.raises(TypeError, match="bfloat16"):
