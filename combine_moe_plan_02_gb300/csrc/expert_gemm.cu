@@ -584,7 +584,8 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     // the CTA's place in the pair, the pair's first CTA and place in the cluster
-    const uint32_t cta = cluster_rank(), rank = cta & 1, lead = cta & ~1u;
+    const uint32_t cta = cluster_rank();
+    const uint32_t rank = SPLIT ? cta & 1 : cta, lead = SPLIT ? cta & ~1u : 0;
     const int part = SPLIT ? (int)(cta >> 1) : 0, split = SPLIT ? a.split : 1;
     const int pair = blockIdx.x / (2 * split), pairs = gridDim.x / (2 * split);
     if (tid == 0) {
@@ -653,7 +654,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         } else {
                             arrive_expect_at(bar, bytes);
                         }
-                        const int k = (c.from + b) * kK;
+                        const int k = ((SPLIT ? c.from : 0) + b) * kK;
                         if (weights) {
                             if (MODE == kForward) {
                                 tma_3d(sa, &maps.a, bar, k, m, c.e);
@@ -796,8 +797,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         };
         int i = 0, turn = 0;
         for (int t = pair; SPLIT || t < tiles; t += pairs) {
-            Tile c = {};
-            if (!SPLIT || t < tiles) c = tile_of<MODE>(a, sched, t);
+            Tile c = SPLIT && t >= tiles ? Tile{} : tile_of<MODE>(a, sched, t);
             const int m = c.m0 + rank * kLanes + q * 32;
             const int last = (ceil_div(c.n, 32) - 1 - odd) / 2;  // last block, if any
             // columns n .. n + 32 of the output, from registers
