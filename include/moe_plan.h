@@ -45,12 +45,15 @@
  *     CUDA call failed; moe_last_cuda_error() returns its error code.
  *     Data-dependent problems are never clamped: an expert id outside
  *     [0, E) is counted in *n_invalid and its entries are marked -1.
- *   - S = 0 is valid: moe_plan still writes zero counts/offsets; the other
- *     calls enqueue nothing.
- *   - No kernel waits for other CTAs or needs the whole GPU (no cooperative
- *     launch; MoonEP page above), so the calls share the GPU with work on
- *     other streams.  Beside a compute-bound kernel (an expert GEMM), a
- *     stream of high priority lets their CTAs take SMs first as they free up.
+ *   - S = 0 is valid: moe_plan still writes zero counts/offsets and
+ *     moe_combine_backward clears dy; the other calls over tokens enqueue
+ *     nothing.
+ *   - No kernel waits for CTAs outside its own cluster (only the experts'
+ *     products have clusters: two CTAs on neighbouring SMs, up to eight for a
+ *     few rows) or needs the whole GPU (no cooperative launch; MoonEP page
+ *     above), so the calls share the GPU with work on other streams.  Beside a
+ *     compute-bound kernel (an expert GEMM), a stream of high priority lets
+ *     their CTAs take SMs first as they free up.
  */
 #ifndef MOE_PLAN_H
 #define MOE_PLAN_H
