@@ -15,8 +15,9 @@
 // token costs 32 columns instead of a padded tile of rows.  Rows of other
 // buckets that a copied box holds land in columns that are never stored;
 // columns are independent, so nothing they hold (NaN included) matters.  The
-// weights' gradient reduces over the tokens: there the rows past the bucket's
-// end are cleared in shared memory before the matrix instruction reads them.
+// weights' gradient reduces over the tokens: a bucket's last block is copied
+// through a map that ends where the bucket ends, and the copy fills the rest of
+// the block with zeros.
 //
 // Two CTAs on neighbouring SMs work on one tile of 256 x 256 (cta_group::2):
 // each holds its 128 lanes of the M side and half of the N side in shared
@@ -33,8 +34,7 @@
 // ring of stages (one warp each: issuing a copy takes 60 to 100 cycles and a
 // wait and an arrival as much again, against 512 cycles of products a block),
 // warp 1 of the first CTA issues the matrix instructions, warp 3 clears the
-// rows of the output that belong to no bucket (weights' gradient: the staged
-// rows past a bucket's end), warps 4 to 11 store.  Two accumulators of 256
+// rows of the output that belong to no bucket, warps 4 to 11 store.  Two accumulators of 256
 // columns let the stores of a tile overlap the next tile's products.  Every
 // wait is bounded.
 //
@@ -262,22 +262,13 @@ __device__ __forceinline__ void cluster_sync()
                      : "memory");
 }
 
-// Arrivals at a barrier of either CTA.  Those that only hand over tensor
-// memory or a copy's byte count order nothing (the copy and the tcgen05 fences
-// do).  The one behind cleared rows is ordered after the clearing CTA's
-// fence.proxy.async; the rows lie in that CTA's own shared memory and are read
-// there by its half of the matrix instruction.  A release at cluster scope
-// costs 0.4 us of every block (1745 against 885 us for 64 buckets of 512 rows,
-// 2048 x 7168) and 0.8 us of every cleared one (768 against 636 us).
+// Arrivals at a barrier of either CTA.  They hand over tensor memory or a copy's
+// byte count and order nothing themselves: the copy and the tcgen05 fences do.
+// A release at cluster scope costs 0.4 us of every block (1745 against 885 us
+// for 64 buckets of 512 rows, 2048 x 7168).
 __device__ __forceinline__ void arrive_at(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ void arrive_release_at(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar)
                  : "memory");
 }
 
@@ -361,17 +352,6 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile in
     return false;
 }
 
-// Orders what follows after the pair's writes before a phase that has passed.
-__device__ __forceinline__ void acquire_pair(uint64_t *bar, uint32_t parity)
-{
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(
-            smem_u32(bar)),
-        "r"(parity)
-        : "memory");
-}
-
 // A place in the ring and the parity of its current round.
 struct Ring {
     int stages, at = 0;
@@ -383,10 +363,6 @@ struct Ring {
             at = 0;
             round ^= 1;
         }
-    }
-    __device__ __forceinline__ void skip(int n)
-    {
-        at = (at + n) % stages;  // the round is not kept
     }
 };
 
@@ -535,8 +511,20 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, Schedule
 
 // --- the kernel ----------------------------------------------------------------
 
-// Operand maps: the M side's, and the N side's with boxes of 16, 32, .. 128 rows
-// (weights' gradient: the first only, boxes of 64 x 64).
+// Operand maps: the M side's, and the N side's with boxes of 16, 32, .. 128 rows.
+// Weights' gradient: boxes of 64 x 64, the first of b for the N side, and the
+// tail maps of the M and the N side.
+//
+// A tail map sees the rows [rows, W] as (z, y, x) with 64 places of y, where
+// (z, y) is the row z + y.  A box of all y that begins at y = -(64 - len),
+// z = row reads zeros for its first 64 - len rows, for y < 0 lies outside, and
+// then the rows row .. row + len: never one past the bucket.  Where in the
+// block the rows stand does not matter, as both operands have them in the same
+// places; those steps of 16 that hold none are not multiplied.  A tail is then a
+// block like any other: no thread clears rows that the other CTA's matrix
+// instruction reads, which would have to be released at cluster scope (0.8 us a
+// tail).  64 ragged buckets of 512, 2048 x 7168: 789 us in f32, 635 in bf16.
+constexpr int kTailM = 1, kTailN = 2;
 struct Maps {
     CUtensorMap a, b[8];
     CUtensorMap out;   // stored boxes
@@ -545,23 +533,9 @@ struct Maps {
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2], drain;
-    uint64_t tail[kMaxStages];  // a last block, until the rows past its end are cleared
     uint32_t tmem;
     volatile int stop;
 };
-
-// Clears the rows past a bucket's end in a staged block (weights' gradient),
-// up to the last row that is multiplied: 128 bytes of each of the four boxes of
-// 64, eight lanes a box.
-__device__ __forceinline__ void clear_tail(uint8_t *stage, int len)
-{
-    const int lane = threadIdx.x & 31;
-    uint8_t *at = stage + (lane >> 3) * 8192 + (lane & 7) * 16;
-    for (int row = len; row & 15; ++row)
-        *reinterpret_cast<uint4 *>(at + row * 128) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-    __syncwarp();
-}
 
 template <typename T> __device__ __forceinline__ T round_to(float f);
 template <> __device__ __forceinline__ float round_to<float>(float f) { return f; }
@@ -592,7 +566,6 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh.full[i], 4);   // both operands of both CTAs
             mbar_init(&sh.empty[i], 1);
-            mbar_init(&sh.tail[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.acc_full[i], 1);
@@ -647,24 +620,28 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                             break;
                         }
                         uint8_t *sa = ring + r.at * stage_bytes, *sb = sa + kABytes;
-                        uint32_t bar = full + r.at * 8;
-                        if (MODE == kWeightGrad && b + 1 == c.blocks && c.last % 16) {
-                            bar = smem_u32(&sh.tail[r.at]);  // warp 3 clears rows and then arrives
-                            mbar_arrive_expect_tx(&sh.tail[r.at], bytes);
-                        } else {
-                            arrive_expect_at(bar, bytes);
-                        }
+                        const uint32_t bar = full + r.at * 8;
+                        arrive_expect_at(bar, bytes);
                         const int k = ((SPLIT ? c.from : 0) + b) * kK;
+                        const bool tail = b + 1 == c.blocks && c.last < kK;
                         if (weights) {
                             if (MODE == kForward) {
                                 tma_3d(sa, &maps.a, bar, k, m, c.e);
                             } else if (MODE == kRowGrad) {
                                 tma_3d(sa, &maps.a, bar, m, k, c.e);
                                 tma_3d(sa + 8192, &maps.a, bar, m + 64, k, c.e);
+                            } else if (tail) {
+                                tma_3d(sa, &maps.b[kTailM], bar, m, c.last - kK, c.row + k);
+                                tma_3d(sa + 8192, &maps.b[kTailM], bar, m + 64, c.last - kK,
+                                       c.row + k);
                             } else {
                                 tma_2d(sa, &maps.a, bar, m, c.row + k);
                                 tma_2d(sa + 8192, &maps.a, bar, m + 64, c.row + k);
                             }
+                        } else if (MODE == kWeightGrad && tail) {
+                            for (int i = 0; i < chunks; ++i)
+                                tma_3d(sb + i * 8192, &maps.b[kTailN], bar, n + i * 64,
+                                       c.last - kK, c.row + k);
                         } else if (MODE == kWeightGrad) {
                             for (int i = 0; i < chunks; ++i)
                                 tma_2d(sb + i * 8192, &maps.b[0], bar, n + i * 64, c.row + k);
@@ -721,12 +698,14 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     uint8_t *sa = ring + r.at * stage_bytes;
                     const int len = b + 1 == c.blocks ? c.last : kK;
                     const int steps = ceil_div(len, 16);
-                    if (MODE == kWeightGrad && len % 16)
-                        acquire_pair(&sh.full[r.at], r.round);  // what either CTA cleared
+                    // the weights' gradient has a tail's rows at the end of its block
+                    const int first = MODE == kWeightGrad ? kK / 16 - steps : 0;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t da = operand_desc(smem_u32(sa), kAMn);
-                        const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
+                        const uint64_t da =
+                            operand_desc(smem_u32(sa), kAMn) + first * (kAMn ? 128 : 2);
+                        const uint64_t db =
+                            operand_desc(smem_u32(sa + kABytes), kBMn) + first * (kBMn ? 128 : 2);
                         for (int s = 0; s < steps; ++s)
                             mma_bf16(tmem + (i & 1) * kN, da + s * (kAMn ? 128 : 2),
                                      db + s * (kBMn ? 128 : 2), idesc, b > from || s > 0);
@@ -739,27 +718,9 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
             }
             if (elect_one()) mma_commit(&sh.drain, lead);  // nothing is issued after this
             __syncwarp();
-        } else if (warp == 3) {
-            if (MODE != kWeightGrad) {
-                zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
-                          blockIdx.x, gridDim.x);
-            } else {
-                Ring r(stages);
-                uint32_t rounds = 0;  // parity of each stage's next tail
-                for (int t = pair; t < tiles; t += pairs) {
-                    const Tile c = tile_of<MODE>(a, sched, t);
-                    if (c.blocks && c.last % 16) {
-                        r.skip(c.blocks - 1);
-                        if (!wait(&sh.tail[r.at], rounds >> r.at & 1, &sh.stop)) break;
-                        rounds ^= 1u << r.at;
-                        clear_tail(ring + r.at * stage_bytes, c.last);
-                        if (lane < 2) arrive_release_at(addr_in(&sh.full[r.at], lead));
-                        r.next();
-                    } else {
-                        r.skip(c.blocks);
-                    }
-                }
-            }
+        } else if (warp == 3 && MODE != kWeightGrad) {
+            zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
+                      blockIdx.x, gridDim.x);
         }
         __syncwarp();
         if (SPLIT) {
@@ -991,15 +952,17 @@ EncodeFn encode_fn()
     return fn;
 }
 
-// A map over [depth, rows, width] (2-D when depth is 0).
+// A map over [depth, rows, width] (2-D when depth is 0), the slices one after
+// another, or one row apart.
 cudaError_t encode(CUtensorMap *map, const void *base, bool f32, int64_t width, int64_t rows,
-                   int64_t depth, int box_width, int box_rows, bool swizzle)
+                   int64_t depth, int box_width, int box_rows, bool swizzle, bool sliding = false)
 {
     EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     const int size = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)depth};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * size, (cuuint64_t)width * rows * size};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * size,
+                                   (cuuint64_t)width * (sliding ? 1 : rows) * size};
     const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r =
@@ -1017,6 +980,12 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t 
                      int64_t depth, int box_rows)
 {
     return encode(map, base, false, width, rows, depth, 64, box_rows, true);
+}
+
+// A tail map of `rows` rows (see Maps).
+cudaError_t make_tail_map(CUtensorMap *map, const void *base, int64_t width, int64_t rows)
+{
+    return encode(map, base, false, width, kK, rows, 64, kK, true, true);
 }
 
 // Launches `clusters` clusters of as many pairs as share a tile.
@@ -1086,6 +1055,8 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         // without rows there is nothing to copy, and no address to describe
         if (rows > 0) e = make_map(&maps.a, other, D, rows, 0, 64);
         if (rows > 0 && e == cudaSuccess) e = make_map(&maps.b[0], rows_a, N, rows, 0, 64);
+        if (rows > 0 && e == cudaSuccess) e = make_tail_map(&maps.b[kTailM], other, D, rows);
+        if (rows > 0 && e == cudaSuccess) e = make_tail_map(&maps.b[kTailN], rows_a, N, rows);
     } else {
         e = make_map(&maps.a, other, D, N, E, MODE == kForward ? kLanes : 64);
         for (int i = 0; i < 8 && e == cudaSuccess; ++i)

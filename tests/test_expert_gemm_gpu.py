@@ -287,3 +287,20 @@ def test_few_rows_share_a_reduction(op, dtype, counts, out, length, cap, tail):
     assert want.abs().max() < 2 ** 24
     assert torch.equal(got, want.to(F32).to(dtype))
     assert torch.equal(got, call(op, plan, a, b, dtype))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,D", [(264, 392), (8, 8), (40, 264)])
+def test_the_weights_gradient_ends_where_a_bucket_ends(dtype, N, D):
+    """Buckets of 1 to 130 rows, so every length of a last block, the next one
+    all NaN: a row read past an end, by either CTA of a pair, would show."""
+    counts = [c for n in range(1, 131) for c in (n, 1 + n % 3)]
+    plan, rows = make_plan(counts, 0, 5)
+    a, b = operands("dw", plan, rows, N, D, 11)
+    off = plan.off.tolist()
+    for e in range(1, len(counts), 2):
+        a[off[e]:off[e + 1]], b[off[e]:off[e + 1]] = float("nan"), float("nan")
+    want = reference("dw", plan, a, b)[::2].to(F32).to(dtype)
+    for _ in range(5):
+        got = call("dw", plan, a, b, dtype)
+        assert torch.equal(got[::2], want) and torch.isnan(got[1::2]).all()
