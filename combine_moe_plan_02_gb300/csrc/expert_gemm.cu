@@ -867,6 +867,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         tmem_load(acc + n + 64, v[(k + 1) & 1]);
                     } else {
                         tc_fence_before();
+                        __syncwarp();  // every lane's columns are in registers
                         if (lane == 0) arrive_at(addr_in(&sh.acc_empty[buf], lead));
                     }
                     if (MODE == kWeightGrad && c.blocks == 0) {
