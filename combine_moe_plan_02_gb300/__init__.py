@@ -74,7 +74,7 @@ def _ptr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream, like: torch.Tensor) -> int:
+def _stream(stream, like: Optional[torch.Tensor]) -> int:
     """The stream to enqueue on: the given one, else the current stream of
     the device that holds `like`."""
     if stream is None:
@@ -82,6 +82,17 @@ def _stream(stream, like: torch.Tensor) -> int:
             return _raw_stream(like.get_device())
         return torch.cuda.current_stream(like.device).cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream, device: torch.device):
+    """The context in which what a call allocates or fills for itself belongs
+    to the stream that the call runs on.  torch hands a freed block on in the
+    order of the stream it was allocated on, so a temporary of another stream
+    may still be in use when it is handed out, or be handed on while the call
+    uses it."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream, None), device=device)
+    return torch.cuda.stream(stream)   # None: no change
 
 
 class Plan(NamedTuple):

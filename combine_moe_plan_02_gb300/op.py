@@ -44,7 +44,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (GroupPlan, moe_combine_backward, moe_combine_dedup, moe_combine_fold,
+from . import (GroupPlan, _on, moe_combine_backward, moe_combine_dedup, moe_combine_fold,
                moe_dispatch, moe_dispatch_backward, moe_dispatch_dedup, moe_dispatch_quant_fp8, moe_group_plan, moe_plan,
                moe_plan_capacity, moe_plan_dispatch)
 
@@ -156,10 +156,13 @@ class MoeOp:
                          stream=None):
         """Gradient of combine's sum: (dy in y's type, dw f32 [S, K]); dw is
         None for an unweighted op."""
-        weighted = self.weighted or routing.group is not None
-        w = routing.topk_w if weighted else torch.ones_like(routing.topk_w)
-        dy, dw = moe_combine_backward(dout, y, w, routing.plan, stream=stream)
-        return dy, dw if weighted else None
+        if self.weighted or routing.group is not None:
+            return moe_combine_backward(dout, y, routing.topk_w, routing.plan, stream=stream)
+        with _on(stream, y.device):
+            w = torch.ones_like(routing.topk_w)
+            unused = torch.empty_like(w)
+        dy, _ = moe_combine_backward(dout, y, w, routing.plan, dw=unused, stream=stream)
+        return dy, None
 
     def dispatch_backward(self, dpacked: torch.Tensor, routing: Routing, *,
                           out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:

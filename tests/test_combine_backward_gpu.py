@@ -156,3 +156,42 @@ def test_op_round_trip(kw):
         ref = (rows * dout.to(F64)[:, None]).sum(-1)
         mass = (rows * dout.to(F64)[:, None]).abs().sum(-1)
         assert ((dw.to(F64) - ref).abs() <= H * 2.0 ** -24 * mass).all()
+
+
+def busy():
+    """Work that keeps the current stream at it for some tens of ms."""
+    a = torch.ones(8192, 8192, dtype=BF16, device="cuda")
+    for _ in range(40):
+        a = (a @ a).clamp_(max=1)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_unweighted_op_beside_a_busy_stream(raw):
+    """The gradient of an unweighted op on a stream of its own, while the
+    current stream is behind and reuses the memory of what was freed: before
+    the call with NaN in it, after the call filled at once."""
+    import combine_moe_plan_02_gb300 as moe
+    S, H, E, K = 3000, 512, 8, 3
+    op = moe.MoeOp(E, weighted=False, fold=False)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    x = torch.randn(S, H, generator=g, device="cuda").to(BF16)
+    w = torch.full((S, K), 0.25, device="cuda")
+    _, _, routing = op.dispatch(x, w, route(S, E, K, 3))
+    dout = torch.randn(S, H, generator=g, device="cuda").to(BF16)
+    y = torch.randn(routing.rows, H, generator=g, device="cuda").to(BF16)
+    m = routing.plan.tok_map
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        trash = [torch.full((S, K), float("nan"), device="cuda") for _ in range(8)]
+        busy()
+        torch.cuda.synchronize()
+        del trash
+        busy()                                   # the current stream is behind from here on
+        dy, dw = op.combine_backward(dout, y, routing,
+                                     stream=side.cuda_stream if raw else side)
+        mine = [torch.full((S, K), 7.0, device="cuda") for _ in range(8)]
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert dw is None and torch.equal(dy[m], dout[:, None].expand(S, K, H))
+        assert all((t == 7).all() for t in mine)
+    assert moe.moe_device_errors() == 0
