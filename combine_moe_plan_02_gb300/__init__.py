@@ -23,6 +23,7 @@ from __future__ import annotations
 
 import ctypes
 from array import array
+from contextlib import nullcontext
 from operator import attrgetter
 from typing import NamedTuple, Optional, Sequence, Union
 
@@ -90,9 +91,25 @@ def _on(stream, device: torch.device):
     order of the stream it was allocated on, so a temporary of another stream
     may still be in use when it is handed out, or be handed on while the call
     uses it."""
-    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+    if stream is None:
+        return _AS_IT_IS
+    if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream, None), device=device)
-    return torch.cuda.stream(stream)   # None: no change
+    return torch.cuda.stream(stream)
+
+
+_AS_IT_IS = nullcontext()
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """A new output of a call on `stream`: the stream's own memory, which is not
+    handed on before what the current stream does with it until then is done."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream, device):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
 
 
 class Plan(NamedTuple):
@@ -518,15 +535,12 @@ def _grad_call(fn: str, grads: Sequence[torch.Tensor], max_norm, out, norm, work
     ptrs = _addresses("grads", grads, device)
     outs = ptrs if out is None else _addresses("out", out, device)
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=like.device)
+        norm = _empty(1, torch.float32, like.device, stream)
     elif norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be float32 [1]")
     L = lib()
-    ws = _workspace(int(L.moe_grad_norm_workspace_size()), like.device, workspace)
-    if ws is not workspace and stream is not None:
-        # made on the current stream, used on another
-        ws.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                         torch.cuda.ExternalStream(int(stream), device=like.device))
+    with _on(stream, like.device):
+        ws = _workspace(int(L.moe_grad_norm_workspace_size()), like.device, workspace)
     numel = array("q", sizes)
     codes = array("i", [MOE_F32 if n32 == n else MOE_BF16]) * n if n32 in (0, n) else \
         array("i", [MOE_F32 if d is torch.float32 else MOE_BF16 for d in dtypes])

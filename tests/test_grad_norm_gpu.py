@@ -138,3 +138,30 @@ def test_side_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         check_out(gs, out, 1.0)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_calls_that_overlap_on_two_streams(raw):
+    """A call on the current stream and one on another, with no wait between:
+    neither may use the other's partial sums, and neither norm's memory may be
+    one that earlier work of the current stream still writes."""
+    import combine_moe_plan_02_gb300 as moe
+    big, small = grads([(60_000_000, F32)], seed=1), grads([(300_001, F32), (7, BF16)], seed=2)
+    out = [[torch.empty_like(g) for g in gs] for gs in (big, small)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for n in (1, 16384):                       # freed while the fills below are pending
+            for t in [torch.empty(n, device="cuda") for _ in range(4)]:
+                moe.moe_clip_grad_norm(big, 1.0, out=out[0])
+                t.fill_(float("nan"))
+        del t
+        a = moe.moe_clip_grad_norm(big, 1.0, out=out[0])
+        b = moe.moe_clip_grad_norm(small, 1.0, out=out[1],
+                                   stream=side.cuda_stream if raw else side)
+        c = moe.moe_grad_norm(small, stream=side)
+        torch.cuda.synchronize()
+        assert abs(float(a) - norm64(big)) <= 2 * NORM * norm64(big)  # at most 128 additions
+        for t in (b, c):
+            assert abs(float(t) - norm64(small)) <= NORM * norm64(small)
+        check_out(small, out[1], 1.0)
