@@ -102,13 +102,17 @@ _AS_IT_IS = nullcontext()
 
 
 def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
-    """A new output of a call on `stream`: the stream's own memory, which is not
-    handed on before what the current stream does with it until then is done."""
+    """A new output or workspace of a call on `stream`: the stream's own memory,
+    which is not handed on before what the current stream does with it until
+    then is done."""
     if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
+    if here.cuda_stream == _stream(stream, None):
         return torch.empty(shape, dtype=dtype, device=device)
     with _on(stream, device):
         t = torch.empty(shape, dtype=dtype, device=device)
-    t.record_stream(torch.cuda.current_stream(device))
+    t.record_stream(here)
     return t
 
 
@@ -145,11 +149,11 @@ def moe_group_plan_workspace_size(S: int, K: int, E: int, group_size: int) -> in
     return int(lib().moe_group_plan_workspace_size(S, K, E, group_size))
 
 
-def _workspace(nbytes: int, device, ws: Optional[torch.Tensor]):
+def _workspace(nbytes: int, device, ws: Optional[torch.Tensor], stream):
     if nbytes == 0:
         return ws
     if ws is None or ws.numel() * ws.element_size() < nbytes:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        ws = _empty(nbytes, torch.uint8, device, stream)
     return ws
 
 
@@ -161,14 +165,14 @@ def moe_plan(topk_idx: torch.Tensor, E: int, *, out: Optional[Plan] = None,
     S, K = topk_idx.shape
     dev = topk_idx.device
     if out is None:
-        out = Plan(torch.empty(E, dtype=torch.int32, device=dev),
-                   torch.empty(E + 1, dtype=torch.int64, device=dev),
-                   torch.empty(max(S * K, 1), dtype=torch.int32, device=dev),
-                   torch.empty(S, K, dtype=torch.int64, device=dev),
-                   torch.empty(1, dtype=torch.int32, device=dev))
+        out = Plan(_empty(E, torch.int32, dev, stream),
+                   _empty(E + 1, torch.int64, dev, stream),
+                   _empty(max(S * K, 1), torch.int32, dev, stream),
+                   _empty((S, K), torch.int64, dev, stream),
+                   _empty(1, torch.int32, dev, stream))
     L = lib()
     nws = int(L.moe_plan_workspace_size(S, K, E))
-    ws = _workspace(nws, dev, workspace)
+    ws = _workspace(nws, dev, workspace, stream)
     _abi.check("moe_plan", L.moe_plan(
         _ptr(topk_idx), S, K, E, _ptr(out.cnt), _ptr(out.off), _ptr(out.packed_src),
         _ptr(out.tok_map), _ptr(out.n_invalid), _ptr(ws), nws, _stream(stream, topk_idx)))
@@ -195,15 +199,15 @@ def moe_plan_capacity(topk_idx: torch.Tensor, E: int, capacity: int, *,
     S, K = topk_idx.shape
     dev = topk_idx.device
     if out is None:
-        out = CapacityPlan(torch.empty(E, dtype=torch.int32, device=dev),
-                           torch.empty(E + 1, dtype=torch.int64, device=dev),
-                           torch.empty(E * capacity, dtype=torch.int32, device=dev),
-                           torch.empty(S, K, dtype=torch.int64, device=dev),
-                           torch.empty(1, dtype=torch.int32, device=dev),
-                           torch.empty(1, dtype=torch.int32, device=dev), capacity)
+        out = CapacityPlan(_empty(E, torch.int32, dev, stream),
+                           _empty(E + 1, torch.int64, dev, stream),
+                           _empty(E * capacity, torch.int32, dev, stream),
+                           _empty((S, K), torch.int64, dev, stream),
+                           _empty(1, torch.int32, dev, stream),
+                           _empty(1, torch.int32, dev, stream), capacity)
     L = lib()
     nws = int(L.moe_plan_workspace_size(S, K, E))
-    ws = _workspace(nws, dev, workspace)
+    ws = _workspace(nws, dev, workspace, stream)
     _abi.check("moe_plan_capacity", L.moe_plan_capacity(
         _ptr(topk_idx), S, K, E, capacity, _ptr(out.cnt), _ptr(out.off), _ptr(out.packed_src),
         _ptr(out.tok_map), _ptr(out.n_invalid), _ptr(out.n_dropped), _ptr(ws), nws,
@@ -220,15 +224,15 @@ def moe_group_plan(topk_idx: torch.Tensor, tok_map: torch.Tensor, E: int, group_
     dev = topk_idx.device
     if out is None:
         rmax = max(S * min(K, G), 1)
-        out = GroupPlan(torch.empty(G, dtype=torch.int32, device=dev),
-                        torch.empty(G + 1, dtype=torch.int64, device=dev),
-                        torch.empty(S, K, dtype=torch.int64, device=dev),
-                        torch.empty(rmax, dtype=torch.int32, device=dev),
-                        torch.empty(rmax, K, dtype=torch.int64, device=dev),
+        out = GroupPlan(_empty(G, torch.int32, dev, stream),
+                        _empty(G + 1, torch.int64, dev, stream),
+                        _empty((S, K), torch.int64, dev, stream),
+                        _empty(rmax, torch.int32, dev, stream),
+                        _empty((rmax, K), torch.int64, dev, stream),
                         group_size)
     L = lib()
     nws = int(L.moe_group_plan_workspace_size(S, K, E, group_size))
-    ws = _workspace(nws, dev, workspace)
+    ws = _workspace(nws, dev, workspace, stream)
     _abi.check("moe_group_plan", L.moe_group_plan(
         _ptr(topk_idx), _ptr(tok_map), S, K, E, group_size, _ptr(out.gcnt), _ptr(out.goff),
         _ptr(out.gtok_map), _ptr(out.grp_src), _ptr(out.grp_tok_map), _ptr(ws), nws,
@@ -244,12 +248,12 @@ def moe_dispatch(x: torch.Tensor, tok_map: torch.Tensor, *, packed_x: Optional[t
     S, H = x.shape
     K = tok_map.shape[1]
     if packed_x is None:
-        packed_x = torch.empty(S * K, H, dtype=x.dtype, device=x.device)
+        packed_x = _empty((S * K, H), x.dtype, x.device, stream)
     n_scales = 0
     if x_scales is not None:
         n_scales = x_scales.shape[1]
         if packed_scales is None:
-            packed_scales = torch.empty(S * K, n_scales, dtype=torch.float32, device=x.device)
+            packed_scales = _empty((S * K, n_scales), torch.float32, x.device, stream)
     if packed_scales is not None and packed_scales.shape[0] < packed_x.shape[0]:
         raise ValueError("packed_scales needs as many rows as packed_x")
     _abi.check("moe_dispatch", lib().moe_dispatch(
@@ -282,26 +286,25 @@ def moe_plan_dispatch(topk_idx: torch.Tensor, x: torch.Tensor, E: int, *,
     H = x.shape[1]
     dev = topk_idx.device
     if out is None:
-        out = Plan(torch.empty(E, dtype=torch.int32, device=dev),
-                   torch.empty(E + 1, dtype=torch.int64, device=dev),
-                   torch.empty(max(S * K, 1), dtype=torch.int32, device=dev),
-                   torch.empty(S, K, dtype=torch.int64, device=dev),
-                   torch.empty(1, dtype=torch.int32, device=dev))
+        out = Plan(_empty(E, torch.int32, dev, stream),
+                   _empty(E + 1, torch.int64, dev, stream),
+                   _empty(max(S * K, 1), torch.int32, dev, stream),
+                   _empty((S, K), torch.int64, dev, stream),
+                   _empty(1, torch.int32, dev, stream))
     if packed_x is None:
-        packed_x = torch.empty(max(S * K, 1), H, dtype=x.dtype, device=dev)
+        packed_x = _empty((max(S * K, 1), H), x.dtype, dev, stream)
     n_scales = 0
     if x_scales is not None:
         n_scales = x_scales.shape[1]
         if packed_scales is None:
-            packed_scales = torch.empty(packed_x.shape[0], n_scales, dtype=torch.float32,
-                                        device=dev)
+            packed_scales = _empty((packed_x.shape[0], n_scales), torch.float32, dev, stream)
     if packed_scales is not None and packed_scales.shape[0] < packed_x.shape[0]:
         raise ValueError("packed_scales needs as many rows as packed_x")
     L = lib()
     nws = 0
     if S * K > _fused_max(L):
         nws = int(L.moe_plan_workspace_size(S, K, E))
-    ws = _workspace(nws, dev, workspace)
+    ws = _workspace(nws, dev, workspace, stream)
     _abi.check("moe_plan_dispatch", L.moe_plan_dispatch(
         _ptr(topk_idx), _ptr(x), S, H, _dt(x), K, E, _ptr(x_scales), n_scales, _ptr(out.cnt),
         _ptr(out.off), _ptr(out.packed_src), _ptr(out.tok_map), _ptr(out.n_invalid),
@@ -320,9 +323,9 @@ def moe_dispatch_quant_fp8(x: torch.Tensor, tok_map: torch.Tensor, *, block: int
     S, H = x.shape
     K = tok_map.shape[1]
     if packed_q is None:
-        packed_q = torch.empty(S * K, H, dtype=torch.float8_e4m3fn, device=x.device)
+        packed_q = _empty((S * K, H), torch.float8_e4m3fn, x.device, stream)
     if packed_scales is None:
-        packed_scales = torch.empty(S * K, H // block, dtype=torch.float32, device=x.device)
+        packed_scales = _empty((S * K, H // block), torch.float32, x.device, stream)
     rows = min(packed_q.shape[0], packed_scales.shape[0])
     _abi.check("moe_dispatch_quant_fp8", lib().moe_dispatch_quant_fp8(
         _ptr(x), S, H, K, _ptr(tok_map), block, _ptr(packed_q), _ptr(packed_scales), rows,
@@ -337,9 +340,9 @@ def moe_dispatch_dedup(x: torch.Tensor, gp: GroupPlan, *, packed_x: Optional[tor
     S, H = x.shape
     K = gp.gtok_map.shape[1]
     if grp_x is None:
-        grp_x = torch.empty(gp.max_rows, H, dtype=x.dtype, device=x.device)
+        grp_x = _empty((gp.max_rows, H), x.dtype, x.device, stream)
     if packed_x is None:
-        packed_x = torch.empty(S * K, H, dtype=x.dtype, device=x.device)
+        packed_x = _empty((S * K, H), x.dtype, x.device, stream)
     _abi.check("moe_dispatch_dedup", lib().moe_dispatch_dedup(
         _ptr(x), S, H, _dt(x), K, gp.G, _ptr(gp.goff), _ptr(gp.grp_src), _ptr(gp.grp_tok_map),
         _ptr(gp.gtok_map), gp.max_rows, _ptr(grp_x), _ptr(packed_x), packed_x.shape[0],
@@ -354,7 +357,7 @@ def moe_combine(y: torch.Tensor, topk_w: torch.Tensor, tok_map: torch.Tensor, *,
     S, K = tok_map.shape
     H = y.shape[1]
     if out is None:
-        out = torch.empty(S, H, dtype=out_dtype, device=y.device)
+        out = _empty((S, H), out_dtype, y.device, stream)
     _abi.check("moe_combine", lib().moe_combine(
         _ptr(y), y.shape[0], _dt(y), _ptr(topk_w), _ptr(tok_map), S, H, K, _ptr(out), _dt(out),
         _stream(stream, y)))
@@ -369,9 +372,9 @@ def moe_combine_dedup(y: torch.Tensor, topk_w: torch.Tensor, gp: GroupPlan, *,
     S, K = gp.gtok_map.shape
     H = y.shape[1]
     if gtok is None:
-        gtok = torch.empty(gp.max_rows, H, dtype=torch.float32, device=y.device)
+        gtok = _empty((gp.max_rows, H), torch.float32, y.device, stream)
     if out is None:
-        out = torch.empty(S, H, dtype=out_dtype, device=y.device)
+        out = _empty((S, H), out_dtype, y.device, stream)
     _abi.check("moe_combine_dedup", lib().moe_combine_dedup(
         _ptr(y), y.shape[0], _dt(y), _ptr(topk_w), _ptr(gp.goff), gp.G, _ptr(gp.grp_src),
         _ptr(gp.grp_tok_map), _ptr(gp.gtok_map), S, H, K, gp.max_rows, _ptr(gtok), _ptr(out),
@@ -390,9 +393,9 @@ def moe_combine_fold(y: torch.Tensor, topk_w: Optional[torch.Tensor], token_map:
     S, K = token_map.shape
     H = y.shape[1]
     if out is None:
-        out = torch.empty(S, H, dtype=out_dtype, device=y.device)
+        out = _empty((S, H), out_dtype, y.device, stream)
     if fold and out_weights is None:
-        out_weights = torch.empty(S, K, dtype=torch.float32, device=y.device)
+        out_weights = _empty((S, K), torch.float32, y.device, stream)
     if not fold:
         out_weights = None
     _abi.check("moe_combine_fold", lib().moe_combine_fold(
@@ -423,11 +426,11 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tens
     if topk_w.dtype != torch.float32 or topk_w.shape != shape:
         raise TypeError("topk_w must be float32 with the shape of tok_map")
     if dy is None:
-        dy = torch.empty_like(y)
+        dy = _empty(y.shape, y.dtype, y.device, stream)
     elif dy.dtype != y.dtype or dy.shape != y.shape:
         raise ValueError("dy must have y's type and shape")
     if dw is None:
-        dw = torch.empty_like(topk_w)
+        dw = _empty(shape, torch.float32, y.device, stream)
     elif dw.dtype != torch.float32 or dw.shape != shape:
         raise ValueError("dw must be float32 [S, K]")
     _abi.check("moe_combine_backward", lib().moe_combine_backward(
@@ -446,11 +449,11 @@ def _expert_args(rows: torch.Tensor, name: str, w: torch.Tensor, width: int, pla
         raise ValueError("the plan and w must have the same number of experts")
 
 
-def _expert_out(out, shape, dtype, device):
+def _expert_out(out, shape, dtype, device, stream):
     if out is None:
         if dtype not in _TORCH_DT.values():
             raise TypeError(f"unsupported output dtype {dtype}")
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _empty(shape, dtype, device, stream)
     if tuple(out.shape) != tuple(shape):
         raise ValueError(f"out must be {list(shape)}")
     if out.dtype not in _TORCH_DT.values():
@@ -465,7 +468,7 @@ def moe_expert_gemm(x: torch.Tensor, w: torch.Tensor, plan: Union[Plan, Capacity
     in no bucket.  x bf16 [rows, D], w bf16 [E, N, D]; y [rows, N]."""
     _expert_args(x, "x", w, 2, plan)
     E, N, D = w.shape
-    out = _expert_out(out, (x.shape[0], N), out_dtype, x.device)
+    out = _expert_out(out, (x.shape[0], N), out_dtype, x.device, stream)
     _abi.check("moe_expert_gemm", lib().moe_expert_gemm(
         _ptr(x), x.shape[0], _ptr(w), N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),
         _dt(out), _stream(stream, x)))
@@ -479,7 +482,7 @@ def moe_expert_gemm_dgrad(dy: torch.Tensor, w: torch.Tensor, plan: Union[Plan, C
     rows in no bucket.  dy bf16 [rows, N]; dx [rows, D]."""
     _expert_args(dy, "dy", w, 1, plan)
     E, N, D = w.shape
-    out = _expert_out(out, (dy.shape[0], D), out_dtype, dy.device)
+    out = _expert_out(out, (dy.shape[0], D), out_dtype, dy.device, stream)
     _abi.check("moe_expert_gemm_dgrad", lib().moe_expert_gemm_dgrad(
         _ptr(dy), dy.shape[0], _ptr(w), N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),
         _dt(out), _stream(stream, dy)))
@@ -497,7 +500,7 @@ def moe_expert_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, plan: Union[Plan, C
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
         raise ValueError("dy must be [rows, N] and x [rows, D]")
     E, N, D = plan.cnt.numel(), dy.shape[1], x.shape[1]
-    out = _expert_out(out, (E, N, D), out_dtype, x.device)
+    out = _expert_out(out, (E, N, D), out_dtype, x.device, stream)
     _abi.check("moe_expert_gemm_wgrad", lib().moe_expert_gemm_wgrad(
         _ptr(dy), _ptr(x), x.shape[0], N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),
         _dt(out), _stream(stream, x)))
@@ -539,8 +542,7 @@ def _grad_call(fn: str, grads: Sequence[torch.Tensor], max_norm, out, norm, work
     elif norm.dtype != torch.float32 or norm.numel() != 1:
         raise ValueError("norm must be float32 [1]")
     L = lib()
-    with _on(stream, like.device):
-        ws = _workspace(int(L.moe_grad_norm_workspace_size()), like.device, workspace)
+    ws = _workspace(int(L.moe_grad_norm_workspace_size()), like.device, workspace, stream)
     numel = array("q", sizes)
     codes = array("i", [MOE_F32 if n32 == n else MOE_BF16]) * n if n32 in (0, n) else \
         array("i", [MOE_F32 if d is torch.float32 else MOE_BF16 for d in dtypes])

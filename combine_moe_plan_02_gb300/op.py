@@ -44,7 +44,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import (GroupPlan, _on, moe_combine_backward, moe_combine_dedup, moe_combine_fold,
+from . import (GroupPlan, _empty, _on, moe_combine_backward, moe_combine_dedup, moe_combine_fold,
                moe_dispatch, moe_dispatch_backward, moe_dispatch_dedup, moe_dispatch_quant_fp8, moe_group_plan, moe_plan,
                moe_plan_capacity, moe_plan_dispatch)
 
@@ -116,17 +116,17 @@ class MoeOp:
             rows = packed.shape[0]
         if self.group_size:
             group = moe_group_plan(topk_idx, plan.tok_map, E, self.group_size, stream=stream)
-            packed = torch.empty(rows, H, dtype=x.dtype, device=dev)
+            packed = _empty((rows, H), x.dtype, dev, stream)
             moe_dispatch_dedup(x, group, packed_x=packed, stream=stream)
         elif self.quant_block:
-            packed = torch.empty(rows, H, dtype=torch.float8_e4m3fn, device=dev)
-            scales = torch.empty(rows, H // self.quant_block, dtype=torch.float32, device=dev)
+            packed = _empty((rows, H), torch.float8_e4m3fn, dev, stream)
+            scales = _empty((rows, H // self.quant_block), torch.float32, dev, stream)
             moe_dispatch_quant_fp8(x, plan.tok_map, block=self.quant_block, packed_q=packed,
                                    packed_scales=scales, stream=stream)
         elif self.capacity:
-            packed = torch.empty(rows, H, dtype=x.dtype, device=dev)
+            packed = _empty((rows, H), x.dtype, dev, stream)
             if x_scales is not None:
-                scales = torch.empty(rows, x_scales.shape[1], dtype=torch.float32, device=dev)
+                scales = _empty((rows, x_scales.shape[1]), torch.float32, dev, stream)
             moe_dispatch(x, plan.tok_map, packed_x=packed, x_scales=x_scales,
                          packed_scales=scales, stream=stream)
         out = packed if scales is None else (packed, scales)
