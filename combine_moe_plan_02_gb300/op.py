@@ -91,7 +91,8 @@ class MoeOp:
         process (the valid rows, or E * capacity padded rows in capacity
         mode, whose per-bucket fill is routing.plan.cnt)."""
         if topk_idx.dtype == torch.int64:
-            topk_idx = topk_idx.to(torch.int32)   # expert ids below 1024
+            with _on(stream, topk_idx.device):
+                topk_idx = topk_idx.to(torch.int32)   # expert ids below 1024
         if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2:
             raise TypeError("topk_idx must be an integer [S, K] tensor")
         if topk_w.dtype != torch.float32 or tuple(topk_w.shape) != tuple(topk_idx.shape):

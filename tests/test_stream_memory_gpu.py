@@ -111,3 +111,16 @@ def test_op(data, kw):
                 op.combine_backward(d["x"], y, routing, stream=stream),
                 op.dispatch_backward(y, routing, stream=stream))
     compare(f)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(group_size=8), dict(capacity=2600)])
+def test_op_with_64_bit_ids(data, kw):
+    import combine_moe_plan_02_gb300 as moe
+    d = data
+    op = moe.MoeOp(d["E"], **kw)
+    idx = d["idx"].long()
+
+    def f(stream):
+        _, total, routing = op.dispatch(d["x"], d["w"], idx, stream=stream)
+        return total, routing.plan.cnt, routing.plan.tok_map
+    compare(f)
