@@ -404,11 +404,28 @@ def moe_combine_fold(y: torch.Tensor, topk_w: Optional[torch.Tensor], token_map:
     return out, out_weights
 
 
+def _check_plan(plan, E: int, tok_map: bool = False):
+    """The kernels read cnt, off and tok_map as these types, and so many of
+    them."""
+    cnt, off = plan.cnt, plan.off
+    if cnt.dtype != torch.int32 or off.dtype != torch.int64:
+        raise TypeError("the plan's cnt must be int32 and its off int64")
+    if cnt.numel() != E or off.numel() != E + 1:
+        raise ValueError("the plan must have cnt [E] and off [E + 1] of as many experts")
+    if tok_map and (plan.tok_map.dtype != torch.int64 or plan.tok_map.dim() != 2):
+        raise TypeError("the plan's tok_map must be int64 [S, K]")
+
+
 def moe_dispatch_backward(dpacked: torch.Tensor, plan: Union[Plan, CapacityPlan], *,
                           out_dtype: torch.dtype = torch.bfloat16,
                           out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Gradient of moe_dispatch: dx[s] = sum over valid k of
     dpacked[tok_map[s,k]], in f32, increasing k."""
+    _check_plan(plan, plan.cnt.numel(), True)
+    if dpacked.dim() != 2:
+        raise ValueError("dpacked must be [rows, H]")
+    if out is not None and out.shape != (plan.tok_map.shape[0], dpacked.shape[1]):
+        raise ValueError("out must be [S, H]")
     return moe_combine_fold(dpacked, None, plan.tok_map, weighted=False, fold=False,
                             out_dtype=out_dtype, out=out, stream=stream)[0]
 
@@ -419,6 +436,7 @@ def moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, topk_w: torch.Tens
     """Gradient of moe_combine: dy[tok_map[s,k]] = topk_w[s,k] * dout[s], zero
     on rows that no entry fills, and dw[s,k] = <dout[s], y[tok_map[s,k]]>,
     zero without a row.  Returns (dy in y's type, dw f32 [S, K])."""
+    _check_plan(plan, plan.cnt.numel(), True)
     S, K = shape = plan.tok_map.shape
     if y.dim() != 2 or dout.shape != (S, y.shape[1]):
         raise ValueError("dout must be [S, H] and y [rows, H]")
@@ -445,8 +463,7 @@ def _expert_args(rows: torch.Tensor, name: str, w: torch.Tensor, width: int, pla
         raise TypeError(f"{name} and w must be bfloat16")
     if w.dim() != 3 or rows.dim() != 2 or rows.shape[1] != w.shape[width]:
         raise ValueError(f"w must be [E, N, D] and {name} [rows, {'N' if width == 1 else 'D'}]")
-    if plan.cnt.numel() != w.shape[0]:
-        raise ValueError("the plan and w must have the same number of experts")
+    _check_plan(plan, w.shape[0])
 
 
 def _expert_out(out, shape, dtype, device, stream):
@@ -500,6 +517,7 @@ def moe_expert_gemm_wgrad(dy: torch.Tensor, x: torch.Tensor, plan: Union[Plan, C
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0]:
         raise ValueError("dy must be [rows, N] and x [rows, D]")
     E, N, D = plan.cnt.numel(), dy.shape[1], x.shape[1]
+    _check_plan(plan, E)
     out = _expert_out(out, (E, N, D), out_dtype, x.device, stream)
     _abi.check("moe_expert_gemm_wgrad", lib().moe_expert_gemm_wgrad(
         _ptr(dy), _ptr(x), x.shape[0], N, D, E, _ptr(plan.cnt), _ptr(plan.off), _ptr(out),

@@ -118,3 +118,33 @@ def test_binding_checks():
     with pytest.raises(ValueError, match="types and sizes"):
         moe.moe_clip_grad_norm([torch.zeros(4)], 1.0, out=[torch.zeros(5)],
                                workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+def test_plans_of_other_types_or_lengths():
+    """The kernels read cnt as int32 [E] and off as int64 [E + 1]: anything
+    else would be read as other numbers or past its end."""
+    import combine_moe_plan_02_gb300 as moe
+    bf = torch.bfloat16
+    good = moe.Plan(torch.zeros(4, dtype=torch.int32), torch.zeros(5, dtype=torch.int64),
+                    torch.zeros(6, dtype=torch.int32), torch.zeros(3, 2, dtype=torch.int64),
+                    torch.zeros(1, dtype=torch.int32))
+    x, w, dy = torch.zeros(6, 16, dtype=bf), torch.zeros(4, 8, 16, dtype=bf), torch.zeros(6, 8, dtype=bf)
+    dout, y, tw = torch.zeros(3, 16), torch.zeros(6, 16), torch.zeros(3, 2)
+    calls = [lambda p: moe.moe_expert_gemm(x, w, p), lambda p: moe.moe_expert_gemm_dgrad(dy, w, p),
+             lambda p: moe.moe_expert_gemm_wgrad(dy, x, p),
+             lambda p: moe.moe_combine_backward(dout, y, tw, p),
+             lambda p: moe.moe_dispatch_backward(y, p)]
+    for call in calls:
+        with pytest.raises(TypeError, match="cnt must be int32"):
+            call(good._replace(cnt=good.cnt.long()))
+        with pytest.raises(TypeError, match="off int64"):
+            call(good._replace(off=good.off.int()))
+        with pytest.raises(ValueError, match="experts"):
+            call(good._replace(off=good.off[:4]))
+        with pytest.raises(ValueError, match="CUDA"):
+            call(good)
+    for call in calls[3:]:
+        with pytest.raises(TypeError, match="tok_map"):
+            call(good._replace(tok_map=good.tok_map.int()))
+    with pytest.raises(ValueError, match="out must"):
+        moe.moe_dispatch_backward(y, good, out=torch.zeros(3, 8, dtype=bf))
