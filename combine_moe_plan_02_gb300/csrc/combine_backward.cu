@@ -236,6 +236,7 @@ MOE_EXPORT int moe_combine_backward(const void *dout, int dout_dtype, const void
         return MOE_EINVAL;
     if (S < 0 || H < 1 || K < 1 || K > 32 || E < 1 || E > 1024) return MOE_EINVAL;
     if (S >= ((int64_t)1 << 31) / K || H >= ((int64_t)1 << 31)) return MOE_EINVAL;
+    if (S == 0 && y_rows == 0) return MOE_OK;  // no token and no row to clear
     if (y_rows < 1 || y_rows >= ((int64_t)1 << 31) || !dy || !cnt || !off) return MOE_EINVAL;
     if (S > 0 && (!dout || !y || !topk_w || !tok_map || !dw)) return MOE_EINVAL;
     if (H % 8 || !aligned16(dout) || !aligned16(y) || !aligned16(dy)) return MOE_EALIGN;

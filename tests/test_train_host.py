@@ -148,3 +148,12 @@ def test_plans_of_other_types_or_lengths():
             call(good._replace(tok_map=good.tok_map.int()))
     with pytest.raises(ValueError, match="out must"):
         moe.moe_dispatch_backward(y, good, out=torch.zeros(3, 8, dtype=bf))
+
+
+def test_combine_backward_of_nothing(L):
+    """No tokens and no rows: nothing to do, as in the calls before it."""
+    f = lambda **k: L.moe_combine_backward(
+        None, 0, None, k.get("rows", 0), k.get("ydt", 0), None, None, FAKE, FAKE, 0, k.get("H", 64),
+        2, 8, None, None, None)
+    assert f() == OK
+    assert f(rows=1) == EINVAL and f(H=0) == EINVAL and f(ydt=2) == EINVAL

@@ -81,3 +81,19 @@ def test_a_batch_without_tokens(layer):
     dx, dw, dup, ddown = layer.backward(dout[:0], w[:0].contiguous(), w_up, w_down, saved)
     assert out.shape == (0, 64) and dx.shape == (0, 64) and dw.shape == (0, 2)
     assert not dup.any() and not ddown.any()
+
+
+def test_a_batch_without_tokens_call_by_call():
+    """moe_plan and moe_dispatch make no row at all for no tokens."""
+    import combine_moe_plan_02_gb300 as moe
+    x, idx, w, w_up, _, _ = inputs(4, 64, 72, 8, 2, lost=False)
+    plan = moe.moe_plan(idx[:0].contiguous(), 8)
+    packed, _ = moe.moe_dispatch(x[:0], plan.tok_map)
+    y = moe.moe_expert_gemm(packed, w_up, plan)
+    out = moe.moe_combine(y, w[:0].contiguous(), plan.tok_map)
+    dy, dw = moe.moe_combine_backward(out, y, w[:0].contiguous(), plan)
+    dwe = moe.moe_expert_gemm_wgrad(dy, packed, plan)
+    dx = moe.moe_dispatch_backward(moe.moe_expert_gemm_dgrad(dy, w_up, plan), plan)
+    assert out.shape == (0, 72) and dy.shape == (0, 72) and dw.shape == (0, 2)
+    assert dx.shape == (0, 64) and not dwe.any()
+    assert moe.moe_device_errors() == 0
