@@ -1,7 +1,7 @@
 // Global L2 norm of many gradients, and the gradients scaled to a limit.
 //
 //   norm = sqrt(sum over all tensors of g^2)
-//   c    = min(1, max_norm / (norm + 1e-6))
+//   c    = min(1, max_norm / (norm + 1e-6)), 1 without a limit (infinity)
 //   out  = c * g, rounded once to the tensor's type
 //
 // The norm has to be known before the first product, so the data is passed
@@ -198,7 +198,7 @@ scale_kernel(const __grid_constant__ Table<N> t, const float *partial, int n_par
     if (norm_out && blockIdx.x == 0 && tid == 0) *norm_out = norm;
     if (max_norm < 0.0f) return;
     float c = max_norm / (norm + kEps);
-    if (c > 1.0f) c = 1.0f;  // a NaN stays
+    if (c > 1.0f || isinf(max_norm)) c = 1.0f;  // a NaN stays under a finite limit
     if (c == 1.0f && t.in_place) return;  // the values are already there
     for (int64_t b = blockIdx.x; b < t.chunks; b += gridDim.x) {
         const Chunk k = chunk_of(t, t.chunks - 1 - b);

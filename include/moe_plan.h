@@ -478,9 +478,9 @@ int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N
  * Global L2 norm over many gradients, and clipping to a limit:
  *   norm[0] = sqrt(sum over all tensors of g^2)
  *   out[i]  = min(1, max_norm / (norm + 1e-6)) * grads[i], rounded once
- * Squares are summed in f32, in a fixed order.  An infinite norm scales by 0
- * (an infinity becomes NaN); a NaN anywhere makes every output NaN; the host
- * sees neither without reading norm.
+ * Squares are summed in f32, in a fixed order.  Under a finite max_norm an
+ * infinite norm scales by 0 (an infinity becomes NaN) and a NaN anywhere makes
+ * every output NaN; the host sees neither without reading norm.
  *
  * grads, out  HOST arrays of n DEVICE pointers (copied before the call
  *             returns); out[i] may be grads[i], and may not overlap any other
@@ -490,7 +490,7 @@ int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N
  * norm        f32 [1] device, written
  * workspace   moe_grad_norm_workspace_size() bytes, 256-byte aligned, dead
  *             after the call
- * max_norm    >= 0 (infinity: nothing is scaled).  n <= MOE_GRAD_TENSORS_MAX.
+ * max_norm    >= 0 (infinity: nothing is scaled, whatever the norm).  n <= MOE_GRAD_TENSORS_MAX.
  * ---------------------------------------------------------------------- */
 #define MOE_GRAD_TENSORS_MAX 65536
 

@@ -165,3 +165,20 @@ def test_calls_that_overlap_on_two_streams(raw):
         for t in (b, c):
             assert abs(float(t) - norm64(small)) <= NORM * norm64(small)
         check_out(small, out[1], 1.0)
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_an_infinite_limit_scales_nothing(value, dtype):
+    import combine_moe_plan_02_gb300 as moe
+    gs = grads([(1000, dtype), (30, F32)])
+    gs[0][7] = value
+    out = [torch.full_like(g, 3.0) for g in gs]
+    norm = moe.moe_clip_grad_norm(gs, float("inf"), out=out)
+    assert not torch.isfinite(norm).any()
+    assert all(torch.equal(torch.nan_to_num(g, nan=9.0), torch.nan_to_num(o, nan=9.0))
+               for g, o in zip(gs, out))
+    kept = [g.clone() for g in gs]
+    moe.moe_clip_grad_norm(gs, float("inf"))
+    assert all(torch.equal(torch.nan_to_num(g, nan=9.0), torch.nan_to_num(o, nan=9.0))
+               for g, o in zip(gs, kept))
