@@ -582,7 +582,9 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
     cluster_sync();                  // both CTAs' barriers are ready
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    // (a split grid has a cluster for each tile that disjoint buckets can have)
+    // A split grid has a cluster for each tile that disjoint buckets can have;
+    // what overlapping ones have beyond is left out and reported.
+    if (SPLIT && tid == 0 && sched.start[a.E] > pairs) atomicOr(&g_expert_error, kErrExpertBucket);
     const int tiles = SPLIT ? min(sched.start[a.E], pairs) : sched.start[a.E];
     // Six stages of 128 + 128 rows.  Buckets of a few rows need less of a stage,
     // and more of them keep more of the weights in flight.

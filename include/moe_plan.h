@@ -105,7 +105,8 @@ int moe_last_cuda_error(void);
  *   bit 4  expert products: a bounded wait ran out of time (the kernel stopped
  *          early; its output is incomplete)
  *   bit 5  expert products: a bucket of the plan lies outside the rows (that
- *          bucket was left out)
+ *          bucket was left out), or buckets overlap in a call of up to 64 rows
+ *          and some were left out
  * flags: HOST pointer to one uint32.  Synchronous: waits for the device. */
 int moe_device_errors(uint32_t *flags);
 
@@ -457,7 +458,8 @@ int moe_combine_backward(const void *dout, int dout_dtype, const void *y, int64_
  * bf16 operands, f32 sums, rounded once to the output's type (MOE_BF16 or
  * MOE_F32).  Output rows in no bucket are zero; dw[e] of an empty bucket is
  * zero.  Rows in no bucket and experts without rows are never used, whatever
- * they hold.  A bucket outside [0, rows) is left out and flagged (bit 5).
+ * they hold.  A bucket outside [0, rows) is left out and flagged (bit 5); buckets
+ * must not overlap.
  *
  * x [rows, D], dy [rows, N] bf16; w bf16 [E, N, D]; y [rows, N], dx [rows, D],
  * dw [E, N, D] of the given output type.  cnt and off are read on the device:
