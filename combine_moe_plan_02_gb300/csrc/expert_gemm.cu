@@ -371,12 +371,20 @@ struct Ring {
 // leaves a relative error of 1e-6 in the 2-norm and grows with their number.
 // For f32 outputs at most 12 blocks (768 products) are summed there; the
 // storing warps add the parts in registers, rounding to nearest.  The bf16
-// outputs are rounded 1000 times more coarsely and take one accumulator.
-constexpr int kPartBlocks = 12;
+// outputs are rounded 1000 times more coarsely: up to 32768 products take one
+// accumulator, which loses 2.4e-4 of a sum at most where the rounding is up to
+// 3.9e-3.  2^23 positive products come out 1 to 5 % low that way, so calls whose
+// reductions may be longer run a LONG kernel with parts of 128 blocks.  Such a
+// part takes 35 us, and its sums wait in local memory for the next.  The code
+// for it costs the others 1 to 5 % (64 ragged buckets of 512, 2048 x 7168, rows'
+// gradient 603 and 619 us, weights' gradient 631 and 647 us), hence a kernel of
+// its own.
+constexpr int64_t kLongest = 32768;
 
-template <typename Tout> __device__ __forceinline__ int reduction_parts(int blocks)
+template <typename Tout, bool LONG> __device__ __forceinline__ int reduction_parts(int blocks)
 {
-    return sizeof(Tout) == 4 ? max(1, (blocks + kPartBlocks - 1) / kPartBlocks) : 1;
+    constexpr int kPartBlocks = sizeof(Tout) == 4 ? 12 : 128;
+    return sizeof(Tout) == 4 || LONG ? max(1, (blocks + kPartBlocks - 1) / kPartBlocks) : 1;
 }
 
 // --- tiles -------------------------------------------------------------------
@@ -544,7 +552,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(flo
     return __float2bfloat16_rn(f);
 }
 
-template <int MODE, typename Tout, int JOIN, bool SPLIT>
+template <int MODE, typename Tout, int JOIN, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
 expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
 {
@@ -682,10 +690,10 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 if (!begin()) break;
                 const int cols = ceil_div(c.n, kStep) * kStep;
                 const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
-                const int parts = reduction_parts<Tout>(c.blocks);
+                const int parts = reduction_parts<Tout, LONG>(c.blocks);
                 int p = 1, from = 0, until = c.blocks / parts;  // blocks of part 1
                 for (int b = 0; b < c.blocks; ++b) {
-                    if (sizeof(Tout) == 4 && b == until) {
+                    if ((sizeof(Tout) == 4 || LONG) && b == until) {
                         end();
                         ++p;
                         from = until;
@@ -804,7 +812,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 const int n = odd * 32;
                 uint32_t sum[32] = {};  // f32
                 bool ok = true;
-                for (int p = c.n ? reduction_parts<Tout>(c.blocks) : 0; p > 0 && ok; --p, ++i) {
+                for (int p = c.n ? reduction_parts<Tout, LONG>(c.blocks) : 0; p > 0 && ok; --p, ++i) {
                     const int buf = i & 1;
                     ok = wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
                     if (!ok) break;
@@ -881,7 +889,7 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 }
                 return true;
             };
-            const int parts = reduction_parts<Tout>(c.blocks);
+            const int parts = reduction_parts<Tout, LONG>(c.blocks);
             if (sizeof(Tout) == 4 && parts > 1) {
                 uint32_t sum[kN / 64][32];  // f32
 #pragma unroll
@@ -917,6 +925,38 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                 if (!ok) break;
 #pragma unroll
                 for (int k = 0; k < kN / 64; ++k) store(k * 64 + odd * 32, sum[k]);
+            } else if (LONG && parts > 1) {
+                float sum[kN / 64][32];
+                bool ok = true;
+                for (int p = 0; p < parts; ++p, ++i) {
+                    const int buf = i & 1;
+                    ok = agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc =
+                        tmem + ((uint32_t)(q * 32) << 16) + buf * kN + odd * 32;
+#pragma unroll 1
+                    for (int k = 0; k < kN / 64 && k * 64 + odd * 32 < c.n; ++k) {
+                        uint32_t v[32];
+                        tmem_load(acc + k * 64, v);
+                        tmem_wait(v);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            sum[k][x] = p ? sum[k][x] + __uint_as_float(v[x])
+                                          : __uint_as_float(v[x]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(addr_in(&sh.acc_empty[buf], lead));
+                }
+                if (!ok) break;
+#pragma unroll 1
+                for (int k = 0; k < kN / 64 && k * 64 + odd * 32 < c.n; ++k) {
+                    uint32_t v[32];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(sum[k][x]);
+                    store(k * 64 + odd * 32, v);
+                }
             } else if (!store_all()) {
                 break;
             }
@@ -992,11 +1032,11 @@ cudaError_t make_tail_map(CUtensorMap *map, const void *base, int64_t width, int
 }
 
 // Launches `clusters` clusters of as many pairs as share a tile.
-template <int MODE, typename Tout, int JOIN, bool SPLIT = false>
+template <int MODE, typename Tout, int JOIN, bool SPLIT = false, bool LONG = false>
 int launch_expert(const Maps &maps, const ExpertArgs &a, int clusters, cudaStream_t stream)
 {
     static KernelCache kc;
-    auto kernel = expert_kernel<MODE, Tout, JOIN, SPLIT>;
+    auto kernel = expert_kernel<MODE, Tout, JOIN, SPLIT, LONG>;
     const size_t smem = 1024 + kRingBytes + kStoreWarps * kBoxArea +
                         (3 * (size_t)a.E + 1) * sizeof(int);
     cudaError_t e = prepare_kernel(kernel, smem, kThreads, kc, nullptr);
@@ -1066,6 +1106,8 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
             e = make_map(&maps.b[i], rows_a, a.K, rows, 0, 16 * (i + 1));
     }
     const bool f32 = out_dtype == MOE_F32;
+    // a bucket may have all rows
+    const bool longer = !f32 && (MODE == kWeightGrad ? rows : a.K) > kLongest;
     const bool join = MODE == kWeightGrad && !f32 && D % 16 && E * N * D * 2 > (320 << 20);
     const int box_rows = f32 ? Boxes<MODE, float, 1>::kRows : Boxes<MODE, __nv_bfloat16, 1>::kRows;
     const int box = join ? 128 : 32;
@@ -1085,7 +1127,7 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
         // -> 13.7 us (two); with 16 and 8 blocks of reduction nothing is lost (1312
         // long: 9.3 -> 8.9 us).
         const int blocks = ceil_div(a.K, kK);
-        if (rows <= kSplitRows && most <= 36 && blocks >= 8) {
+        if (rows <= kSplitRows && most <= 36 && blocks >= 8 && !longer) {
             a.split = most <= 15 && blocks >= 16 ? 4 : 2;
             return f32 ? launch_expert<MODE, float, 1, true>(maps, a, (int)most, stream)
                        : launch_expert<MODE, __nv_bfloat16, 1, true>(maps, a, (int)most, stream);
@@ -1094,9 +1136,13 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
     const int pairs = sm_count() / 2;
     const int clusters = (int)(most < pairs ? most : pairs);
     if (f32) return launch_expert<MODE, float, 1>(maps, a, clusters, stream);
+    auto launch = longer ? launch_expert<MODE, __nv_bfloat16, 1, false, true>
+                         : launch_expert<MODE, __nv_bfloat16, 1>;
     if constexpr (MODE == kWeightGrad)
-        if (join) return launch_expert<MODE, __nv_bfloat16, 4>(maps, a, clusters, stream);
-    return launch_expert<MODE, __nv_bfloat16, 1>(maps, a, clusters, stream);
+        if (join)
+            launch = longer ? launch_expert<MODE, __nv_bfloat16, 4, false, true>
+                            : launch_expert<MODE, __nv_bfloat16, 4>;
+    return launch(maps, a, clusters, stream);
 }
 
 } // namespace

@@ -456,7 +456,11 @@ int moe_combine_backward(const void *dout, int dout_dtype, const void *y, int64_
  *   moe_expert_gemm_dgrad  dx[r, d]    = sum_n dy[r, n] * w[e, n, d]
  *   moe_expert_gemm_wgrad  dw[e, n, d] = sum_{r in bucket e} dy[r, n] * x[r, d]
  * bf16 operands, f32 sums, rounded once to the output's type (MOE_BF16 or
- * MOE_F32).  Output rows in no bucket are zero; dw[e] of an empty bucket is
+ * MOE_F32).  The tensor core sums in f32 but drops a sum's low bits at each step
+ * of 16 products; parts of at most 768 products (f32 outputs), or of 8192 where a
+ * reduction may be longer than 32768 (bf16 outputs), are summed there and added
+ * rounding to nearest, so at any length a positive sum is off by less than
+ * 6e-6 (f32) or 2.5e-4 (bf16) of itself and 6e-8 a part, before its rounding.  Output rows in no bucket are zero; dw[e] of an empty bucket is
  * zero.  Rows in no bucket and experts without rows are never used, whatever
  * they hold.  A bucket outside [0, rows) is left out and flagged (bit 5); buckets
  * must not overlap.

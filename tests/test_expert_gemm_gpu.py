@@ -318,3 +318,93 @@ def test_overlapping_buckets_of_a_few_rows():
     torch.cuda.synchronize()
     assert moe.moe_device_errors() == 32
     assert moe.moe_device_errors() == 0
+
+
+# Long reductions.  At every step of 16 products the accumulator loses at most
+# 2^-23 of what it holds; 8192 products (bf16 outputs) or 768 (f32) are summed
+# there, and the parts of a sum are added in f32, each off by at most 2^-24.  For
+# sums of positive terms that is relative to the sum, and a rounded output lies
+# between the rounded ends of that interval.
+
+def positive(shape, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.rand(shape, generator=g, device="cuda") + 0.5).to(BF16)
+
+
+def check_long(got, want, length, dtype):
+    per = 768 if dtype == F32 else 8192
+    bound = per / 16 * 2.0 ** -23 + (length / per + 1) * 2.0 ** -24
+    low, high = ((want * f).to(F32).to(dtype) for f in (1 - bound, 1 + bound))
+    assert ((low <= got) & (got <= high)).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("op,counts,out", [("y", [2], 8), ("y", [70, 3], 40), ("dx", [1], 16),
+                                           ("dx", [80], 8)])
+def test_long_products(op, counts, out, dtype):
+    """2^23 products for each output: more than one accumulator may sum, with
+    the pairs of a cluster sharing the reduction and without."""
+    length = 1 << 23
+    plan, rows = make_plan(counts)
+    N, D = (out, length) if op == "y" else (length, out)
+    a, b = operands(op, plan, rows, N, D, 3, positive)
+    got = call(op, plan, a, b, dtype)
+    check_long(got, reference(op, plan, a, b), length, dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("N,D", [(8, 8), (136, 264)])
+def test_long_buckets(dtype, N, D):
+    """The weights' gradient over millions of rows, beside short buckets."""
+    length = (1 << 24) + 5 if N == 8 else (1 << 22) + 5
+    plan, rows = make_plan([3, length, 0, 9000])
+    a, b = operands("dw", plan, rows, N, D, 3, positive)
+    got = call("dw", plan, a, b, dtype)
+    check_long(got, reference("dw", plan, a, b), length, dtype)
+
+
+def test_large_weights_with_long_buckets():
+    """As test_large_weights_with_rows_of_odd_sixteenths, with reductions of more
+    than one accumulator in some buckets."""
+    plan, rows = make_plan([(7 * e) % 75 for e in range(94)] + [45000, 9001], 0, 3)
+    a, b = operands("dw", plan, rows, 712, 2856, 4)
+    got = call("dw", plan, a, b, BF16)
+    want = reference("dw", plan, a, b)
+    assert want.abs().max() < 2 ** 24
+    assert torch.equal(got, want.to(F32).to(BF16))
+
+
+@pytest.mark.parametrize("op", ["y", "dx", "dw"])
+def test_f32_sums_of_thousands_of_products(op):
+    """The 2-norm of an f32 output's error.  A step loses half of 2^-23 of the
+    running sum on average at most, which in a part of 48 steps is a walk to
+    the part's sum: 48 * 2^-24 * sqrt(1/4 + 1/12) of it (the mean and the
+    spread of the walk), and the parts' additions 2^-25 each.  8192 products in
+    one accumulator lose ten times as much."""
+    length = 8192
+    plan, rows = make_plan([length, length] if op == "dw" else [90, 300])
+    N, D = {"y": (256, length), "dx": (length, 256), "dw": (256, 320)}[op]
+    a, b = operands(op, plan, rows, N, D, 3, normal)
+    got, want = call(op, plan, a, b, F32).to(F64), reference(op, plan, a, b)
+    bound = 48 * 2.0 ** -24 * 3 ** -0.5 + (length / 768 + 1) * 2.0 ** -25
+    assert (got - want).norm() <= bound * want.norm()
+
+
+def test_a_bucket_that_takes_seconds():
+    """The weights' gradient of 1.1 billion rows: its waits are for parts of
+    the sum, each of which is done in time, not for the whole of it."""
+    import combine_moe_plan_02_gb300 as moe
+    rows = 1_100_000_003                                  # dy and x: 17.6 GB each
+    plan, _ = make_plan([rows])
+    a = torch.zeros(rows, 8, dtype=BF16, device="cuda")
+    b = torch.zeros(rows, 8, dtype=BF16, device="cuda")
+    at = torch.tensor([0, 1, 12345, rows // 2, rows - 70, rows - 1], device="cuda")
+    a[at], b[at] = ints((6, 8), 1), ints((6, 8), 2)
+    events = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    events[0].record()
+    dw = moe.moe_expert_gemm_wgrad(a, b, plan, out_dtype=BF16)
+    events[1].record()
+    torch.cuda.synchronize()
+    print(f"{events[0].elapsed_time(events[1]):.0f} ms")
+    assert moe.moe_device_errors() == 0
+    assert torch.equal(dw[0], (a[at].to(F64).T @ b[at].to(F64)).to(F32).to(BF16))
