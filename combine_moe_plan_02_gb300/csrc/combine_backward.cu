@@ -7,9 +7,9 @@
 // and dy is zero on the rows that no entry reaches: the ends of padded
 // buckets and what lies past the last one.
 //
-// A CTA owns one token: its dout row is read once and serves both products of
-// all K entries, so the call moves S*H of dout, V*H of y and R*H of dy and
-// nothing twice.  A thread takes 16 bytes of y per entry and step, all of a
+// A CTA owns one token: its dout row is read once for each eight entries and
+// serves both products of them, so up to K = 8 the call moves S*H of dout, V*H
+// of y and R*H of dy and nothing twice.  A thread takes 16 bytes of y per entry and step, all of a
 // step's loads issued before the first product; its K sums stay in registers
 // in f32 and the CTA joins them in a fixed order (lanes by shuffles, then
 // warps in increasing order), so dw does not depend on timing.
@@ -236,6 +236,7 @@ MOE_EXPORT int moe_combine_backward(const void *dout, int dout_dtype, const void
         return MOE_EINVAL;
     if (S < 0 || H < 1 || K < 1 || K > 32 || E < 1 || E > 1024) return MOE_EINVAL;
     if (S >= ((int64_t)1 << 31) / K || H >= ((int64_t)1 << 31)) return MOE_EINVAL;
+    if (S + kMaxGapCtas >= ((int64_t)1 << 31)) return MOE_EINVAL;  // CTAs of a grid
     if (S == 0 && y_rows == 0) return MOE_OK;  // no token and no row to clear
     if (y_rows < 1 || y_rows >= ((int64_t)1 << 31) || !dy || !cnt || !off) return MOE_EINVAL;
     if (S > 0 && (!dout || !y || !topk_w || !tok_map || !dw)) return MOE_EINVAL;

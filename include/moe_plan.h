@@ -441,7 +441,7 @@ int moe_combine_fold(const void *y, int64_t y_rows, int in_dtype, const float *t
  *          [-1, y_rows) drops its terms and is flagged (bit 2)
  * dw       f32 [S, K].  The sum's order is fixed: results are reproducible.
  * S = 0 clears the unfilled rows of dy.  1 <= y_rows < 2^31 (0 too where S is),
- * S*K < 2^31.
+ * S*K < 2^31, S < 2^31 - 152.
  * Alignment: dout, y, dy 16-byte aligned; H a multiple of 8.
  * ---------------------------------------------------------------------- */
 int moe_combine_backward(const void *dout, int dout_dtype, const void *y, int64_t y_rows,

@@ -157,3 +157,11 @@ def test_combine_backward_of_nothing(L):
         2, 8, None, None, None)
     assert f() == OK
     assert f(rows=1) == EINVAL and f(H=0) == EINVAL and f(ydt=2) == EINVAL
+
+
+def test_combine_backward_of_more_tokens_than_a_grid_has(L):
+    """One CTA a token beside those that clear rows: refused, not left to the
+    launch."""
+    f = lambda S: L.moe_combine_backward(FAKE, 0, FAKE, 8, 0, FAKE, FAKE, FAKE, FAKE, S, 64, 1, 8,
+                                         FAKE, FAKE, None)
+    assert f((1 << 31) - 1) == EINVAL and f((1 << 31) - 152) == EINVAL
