@@ -34,9 +34,12 @@ combined_wts[s,i] is the sum of topk_w[s,i] over the token's valid copies
 row and the group rows are summed unweighted; the fold there takes a second
 pass over the group rows.
 
-Training: combine_backward and dispatch_backward are the gradients of the two
-calls, from the same handle, in every mode (the quantising dispatch passes
-gradients straight through).
+Training: dispatch_backward is the gradient of dispatch's rows and
+combine_backward that of combine's first result, from the same handle, in every
+mode (the quantising dispatch passes gradients straight through).  combined_wts
+is not differentiated: where a loss depends on it, its term of topk_w's gradient
+(each token's number of valid copies times the gradient of combined_wts) is the
+caller's to add.
 """
 from __future__ import annotations
 
@@ -155,8 +158,8 @@ class MoeOp:
 
     def combine_backward(self, dout: torch.Tensor, y: torch.Tensor, routing: Routing, *,
                          stream=None):
-        """Gradient of combine's sum: (dy in y's type, dw f32 [S, K]); dw is
-        None for an unweighted op."""
+        """Gradient of combine's first result: (dy in y's type, dw f32 [S, K]);
+        dw is None for an unweighted op.  combined_wts has no part in it."""
         if self.weighted or routing.group is not None:
             return moe_combine_backward(dout, y, routing.topk_w, routing.plan, stream=stream)
         with _on(stream, y.device):
