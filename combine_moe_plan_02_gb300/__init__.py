@@ -3,7 +3,8 @@
 Python binding of the C ABI in include/moe_plan.h: each function checks and
 marshals torch tensors (device pointers, sizes, the current stream) into one
 C call; all work runs in the library's CUDA kernels.  Output tensors are
-allocated with torch when not passed in.
+allocated with torch when not passed in, as memory of the stream that the call
+runs on.
 
     plan  = moe_plan(topk_idx, E)                  # counts, offsets, maps
     px, _ = moe_dispatch(x, plan.tok_map)          # packed_x[off[e] + slot]

@@ -38,13 +38,13 @@
 // columns let the stores of a tile overlap the next tile's products.  Every
 // wait is bounded.
 //
-// What bounds it, 64 buckets of 512 rows, 2048 x 7168, bf16 out: 552 us forward,
-// 554 us for the rows (1743, 1735 TFLOP/s; 87 % of the tensor pipe's cycles),
+// What bounds it, 64 buckets of 512 rows, 2048 x 7168, bf16 out: 549 us forward,
+// 550 us for the rows (1753, 1749 TFLOP/s; 87 % of the tensor pipe's cycles),
 // the copies from L2: six stages of 32 KB are what fits, with four it takes 618
 // us, without the tokens' copies 499 us.  For seconds on end the power limit
-// sets the pace: 619 us.  Buckets of 512 rows on average, half of them cut into
-// three parts: 590 us (670 us for seconds).  The weights' gradient: 600 us in
-// bf16 (1603 TFLOP/s), 780 us in f32, where 4.36 GB move and products, copies
+// sets the pace: 620 to 640 us.  Buckets of 512 rows on average, half of them
+// cut into three parts: 590 us (670 to 690 us for seconds).  The weights'
+// gradient: 606 us in bf16 (1588 TFLOP/s), 767 us in f32, where 4.36 GB move and products, copies
 // and stores share L2 and shared memory.  One row in each of 8 buckets, 2048 x
 // 6144: 35 us, the weights at 6.5 TB/s behind 4 us of launch and tile list; 1024
 // rows in 256 buckets: 885 us (7.3 TB/s).  64 pairs' work taken over by cluster
@@ -531,7 +531,8 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, Schedule
 // places; those steps of 16 that hold none are not multiplied.  A tail is then a
 // block like any other: no thread clears rows that the other CTA's matrix
 // instruction reads, which would have to be released at cluster scope (0.8 us a
-// tail).  64 ragged buckets of 512, 2048 x 7168: 789 us in f32, 635 in bf16.
+// tail).  64 ragged buckets of 512, 2048 x 7168: 779 us in f32, 620 in bf16; 512
+// rows each, without a tail: 767 and 606.
 constexpr int kTailM = 1, kTailN = 2;
 struct Maps {
     CUtensorMap a, b[8];
