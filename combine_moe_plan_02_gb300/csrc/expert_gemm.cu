@@ -15,9 +15,8 @@
 // token costs 32 columns instead of a padded tile of rows.  Rows of other
 // buckets that a copied box holds land in columns that are never stored;
 // columns are independent, so nothing they hold (NaN included) matters.  The
-// weights' gradient reduces over the tokens: a bucket's last block is copied
-// through a map that ends where the bucket ends, and the copy fills the rest of
-// the block with zeros.
+// weights' gradient reduces over the tokens: of a bucket's last block just the
+// bucket's rows are copied, and zeros after them up to a multiple of 16 rows.
 //
 // Two CTAs on neighbouring SMs work on one tile of 256 x 256 (cta_group::2):
 // each holds its 128 lanes of the M side and half of the N side in shared
@@ -301,6 +300,48 @@ __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, uint32
         : "memory");
 }
 
+// Rows y .. y + len of 64 columns, in boxes of rows inside their tensor, one for
+// each digit of len to base 4 (`maps`: of 48, 32, 16, 12, 8, 4, 3, 2, 1 rows), and
+// zeros up to a multiple of 16 rows at least: a box of 16, or where that would
+// pass the block's 64 rows one or two that end with it (`zeros`: of 16, 8, .. 1
+// rows).  So a last block arrives like any other: no thread clears rows that the
+// other CTA's matrix instruction reads, which would have to be released at
+// cluster scope (0.8 us a block).  The swizzle goes by the address in shared
+// memory, so a box may begin at any row.  64 buckets of 512 rows on average, 2048 x
+// 7168: 793 us in f32, 628 in bf16; of 512 each, without such blocks, 765 and 603;
+// with one box for each bit of len 806 and 662, of the rows of zeros too.
+__device__ __forceinline__ void tma_tail(uint8_t *dst, const CUtensorMap *maps,
+                                         const CUtensorMap *zeros, uint32_t bar, int x, int y,
+                                         int len)
+{
+#pragma unroll
+    for (int s = 4; s >= 0; s -= 2, maps += 3) {
+        const int digit = len >> s & 3;
+        if (digit) {
+            tma_2d(dst, maps + 3 - digit, bar, x, y);
+            dst += (digit << s) * 128;
+            y += digit << s;
+        }
+    }
+    int h = 16;
+    while (h > kK - len) {
+        h >>= 1;
+        ++zeros;
+    }
+    tma_2d(dst, zeros, bar, 0, 0);
+    if (len + h < kK && len > kK - 16)
+        tma_2d(dst + (kK - len - h) * 128, zeros, bar, 0, 0);
+}
+
+// What it copies, in rows.
+__device__ __forceinline__ int tail_rows(int len)
+{
+    const int pad = kK - len;
+    if (pad >= 16) return len + 16;
+    const int h = 1 << (31 - __clz(pad));
+    return len + (pad == h ? h : 2 * h);
+}
+
 // A box from this CTA's shared memory to global memory; what lies outside the
 // tensor is not written.
 __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int x, int y,
@@ -520,24 +561,17 @@ template <int MODE> __device__ void build_schedule(const ExpertArgs &a, Schedule
 // --- the kernel ----------------------------------------------------------------
 
 // Operand maps: the M side's, and the N side's with boxes of 16, 32, .. 128 rows.
-// Weights' gradient: boxes of 64 x 64, the first of b for the N side, and the
-// tail maps of the M and the N side.
-//
-// A tail map sees the rows [rows, W] as (z, y, x) with 64 places of y, where
-// (z, y) is the row z + y.  A box of all y that begins at y = -(64 - len),
-// z = row reads zeros for its first 64 - len rows, for y < 0 lies outside, and
-// then the rows row .. row + len: never one past the bucket.  Where in the
-// block the rows stand does not matter, as both operands have them in the same
-// places; those steps of 16 that hold none are not multiplied.  A tail is then a
-// block like any other: no thread clears rows that the other CTA's matrix
-// instruction reads, which would have to be released at cluster scope (0.8 us a
-// tail).  64 ragged buckets of 512, 2048 x 7168: 779 us in f32, 620 in bf16; 512
-// rows each, without a tail: 767 and 606.
-constexpr int kTailM = 1, kTailN = 2;
-struct Maps {
-    CUtensorMap a, b[8];
+// Weights' gradient: boxes of 64 x 64, the first of b for the N side; then boxes
+// of 48 to 1 rows of the M and of the N side and of 16, 8, .. 1 rows of zeros, for
+// the last block of a bucket.
+constexpr int kTailM = 1, kTailN = 10, kZeros = 19;
+template <int MODE> struct Maps {
+    CUtensorMap a, b[MODE == kWeightGrad ? 24 : 8];
     CUtensorMap out;   // stored boxes
 };
+
+// What the padding of a bucket's last block is copied from.
+__device__ __align__(128) uint16_t g_zero_rows[16 * 64];
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
@@ -555,7 +589,7 @@ template <> __device__ __forceinline__ __nv_bfloat16 round_to<__nv_bfloat16>(flo
 
 template <int MODE, typename Tout, int JOIN, bool SPLIT, bool LONG>
 __global__ void __launch_bounds__(kThreads, 1)
-expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
+expert_kernel(const __grid_constant__ Maps<MODE> maps, ExpertArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -632,9 +666,10 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                         }
                         uint8_t *sa = ring + r.at * stage_bytes, *sb = sa + kABytes;
                         const uint32_t bar = full + r.at * 8;
-                        arrive_expect_at(bar, bytes);
+                        const bool tail =
+                            MODE == kWeightGrad && b + 1 == c.blocks && c.last % 16;
+                        arrive_expect_at(bar, tail ? bytes / kK * tail_rows(c.last) : bytes);
                         const int k = ((SPLIT ? c.from : 0) + b) * kK;
-                        const bool tail = b + 1 == c.blocks && c.last < kK;
                         if (weights) {
                             if (MODE == kForward) {
                                 tma_3d(sa, &maps.a, bar, k, m, c.e);
@@ -642,17 +677,17 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                                 tma_3d(sa, &maps.a, bar, m, k, c.e);
                                 tma_3d(sa + 8192, &maps.a, bar, m + 64, k, c.e);
                             } else if (tail) {
-                                tma_3d(sa, &maps.b[kTailM], bar, m, c.last - kK, c.row + k);
-                                tma_3d(sa + 8192, &maps.b[kTailM], bar, m + 64, c.last - kK,
-                                       c.row + k);
+                                for (int i = 0; i < 2; ++i)
+                                    tma_tail(sa + i * 8192, maps.b + kTailM, maps.b + kZeros, bar,
+                                             m + i * 64, c.row + k, c.last);
                             } else {
                                 tma_2d(sa, &maps.a, bar, m, c.row + k);
                                 tma_2d(sa + 8192, &maps.a, bar, m + 64, c.row + k);
                             }
-                        } else if (MODE == kWeightGrad && tail) {
+                        } else if (tail) {
                             for (int i = 0; i < chunks; ++i)
-                                tma_3d(sb + i * 8192, &maps.b[kTailN], bar, n + i * 64,
-                                       c.last - kK, c.row + k);
+                                tma_tail(sb + i * 8192, maps.b + kTailN, maps.b + kZeros, bar,
+                                         n + i * 64, c.row + k, c.last);
                         } else if (MODE == kWeightGrad) {
                             for (int i = 0; i < chunks; ++i)
                                 tma_2d(sb + i * 8192, &maps.b[0], bar, n + i * 64, c.row + k);
@@ -709,14 +744,10 @@ expert_kernel(const __grid_constant__ Maps maps, ExpertArgs a)
                     uint8_t *sa = ring + r.at * stage_bytes;
                     const int len = b + 1 == c.blocks ? c.last : kK;
                     const int steps = ceil_div(len, 16);
-                    // the weights' gradient has a tail's rows at the end of its block
-                    const int first = MODE == kWeightGrad ? kK / 16 - steps : 0;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint64_t da =
-                            operand_desc(smem_u32(sa), kAMn) + first * (kAMn ? 128 : 2);
-                        const uint64_t db =
-                            operand_desc(smem_u32(sa + kABytes), kBMn) + first * (kBMn ? 128 : 2);
+                        const uint64_t da = operand_desc(smem_u32(sa), kAMn);
+                        const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
                         for (int s = 0; s < steps; ++s)
                             mma_bf16(tmem + (i & 1) * kN, da + s * (kAMn ? 128 : 2),
                                      db + s * (kBMn ? 128 : 2), idesc, b > from || s > 0);
@@ -996,17 +1027,15 @@ EncodeFn encode_fn()
     return fn;
 }
 
-// A map over [depth, rows, width] (2-D when depth is 0), the slices one after
-// another, or one row apart.
+// A map over [depth, rows, width] (2-D when depth is 0).
 cudaError_t encode(CUtensorMap *map, const void *base, bool f32, int64_t width, int64_t rows,
-                   int64_t depth, int box_width, int box_rows, bool swizzle, bool sliding = false)
+                   int64_t depth, int box_width, int box_rows, bool swizzle)
 {
     EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     const int size = f32 ? 4 : 2;
     const cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)rows, (cuuint64_t)depth};
-    const cuuint64_t strides[2] = {(cuuint64_t)width * size,
-                                   (cuuint64_t)width * (sliding ? 1 : rows) * size};
+    const cuuint64_t strides[2] = {(cuuint64_t)width * size, (cuuint64_t)width * rows * size};
     const cuuint32_t box[3] = {(cuuint32_t)box_width, (cuuint32_t)box_rows, 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r =
@@ -1026,15 +1055,36 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int64_t width, int64_t 
     return encode(map, base, false, width, rows, depth, 64, box_rows, true);
 }
 
-// A tail map of `rows` rows (see Maps).
-cudaError_t make_tail_map(CUtensorMap *map, const void *base, int64_t width, int64_t rows)
+// The maps of tma_tail over rows.
+cudaError_t make_tail_maps(CUtensorMap *map, const void *base, int64_t width, int64_t rows)
 {
-    return encode(map, base, false, width, kK, rows, 64, kK, true, true);
+    cudaError_t e = cudaSuccess;
+    for (int s = 4; s >= 0; s -= 2)
+        for (int digit = 3; digit && e == cudaSuccess; --digit)
+            e = make_map(map++, base, width, rows, 0, digit << s);
+    return e;
+}
+
+// g_zero_rows on the current device.
+cudaError_t zero_rows(const void **p)
+{
+    static void *cached[kMaxCachedDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    void *at = dev >= 0 && dev < kMaxCachedDevices ? cached[dev] : nullptr;
+    if (!at) {
+        e = cudaGetSymbolAddress(&at, g_zero_rows);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < kMaxCachedDevices) cached[dev] = at;
+    }
+    *p = at;
+    return cudaSuccess;
 }
 
 // Launches `clusters` clusters of as many pairs as share a tile.
 template <int MODE, typename Tout, int JOIN, bool SPLIT = false, bool LONG = false>
-int launch_expert(const Maps &maps, const ExpertArgs &a, int clusters, cudaStream_t stream)
+int launch_expert(const Maps<MODE> &maps, const ExpertArgs &a, int clusters, cudaStream_t stream)
 {
     static KernelCache kc;
     auto kernel = expert_kernel<MODE, Tout, JOIN, SPLIT, LONG>;
@@ -1093,14 +1143,20 @@ int run_expert(const void *rows_a, const void *other, int64_t rows, int64_t N, i
     a.N = (int)N;
     a.K = (int)(MODE == kForward ? D : N);
     a.out = static_cast<uint8_t *>(out);
-    Maps maps = {};
+    Maps<MODE> maps = {};
     cudaError_t e = cudaSuccess;
-    if (MODE == kWeightGrad) {
+    if constexpr (MODE == kWeightGrad) {
         // without rows there is nothing to copy, and no address to describe
-        if (rows > 0) e = make_map(&maps.a, other, D, rows, 0, 64);
-        if (rows > 0 && e == cudaSuccess) e = make_map(&maps.b[0], rows_a, N, rows, 0, 64);
-        if (rows > 0 && e == cudaSuccess) e = make_tail_map(&maps.b[kTailM], other, D, rows);
-        if (rows > 0 && e == cudaSuccess) e = make_tail_map(&maps.b[kTailN], rows_a, N, rows);
+        if (rows > 0) {
+            const void *zeros = nullptr;
+            e = zero_rows(&zeros);
+            if (e == cudaSuccess) e = make_map(&maps.a, other, D, rows, 0, 64);
+            if (e == cudaSuccess) e = make_map(&maps.b[0], rows_a, N, rows, 0, 64);
+            if (e == cudaSuccess) e = make_tail_maps(&maps.b[kTailM], other, D, rows);
+            if (e == cudaSuccess) e = make_tail_maps(&maps.b[kTailN], rows_a, N, rows);
+            for (int i = 0; i < 5 && e == cudaSuccess; ++i)
+                e = make_map(&maps.b[kZeros + i], zeros, 64, 16, 0, 16 >> i);
+        }
     } else {
         e = make_map(&maps.a, other, D, N, E, MODE == kForward ? kLanes : 64);
         for (int i = 0; i < 8 && e == cudaSuccess; ++i)

@@ -408,3 +408,23 @@ def test_a_bucket_that_takes_seconds():
     print(f"{events[0].elapsed_time(events[1]):.0f} ms")
     assert moe.moe_device_errors() == 0
     assert torch.equal(dw[0], (a[at].to(F64).T @ b[at].to(F64)).to(F32).to(BF16))
+
+
+def test_random_shapes():
+    """Shapes and buckets of no pattern, each over memory that is mapped anew, so
+    that operands begin and end where mapped memory may."""
+    import random
+    r = random.Random(41)
+    for n in range(60):
+        counts = [0 if r.random() < 0.2 else r.randint(0, r.choice([3, 20, 80, 300]))
+                  for _ in range(r.choice([1, 2, 5, 16, 64]))]
+        N, D = 8 * r.randint(1, 80), 8 * r.randint(1, 120)
+        plan, rows = make_plan(counts, max(counts) + 1 if n % 4 == 0 else 0, r.choice([0, 0, 5]))
+        if rows == 0:
+            continue
+        for op in ("y", "dx", "dw"):
+            torch.cuda.empty_cache()
+            dtype = r.choice([F32, BF16])
+            a, b = operands(op, plan, rows, N, D, n)
+            want = reference(op, plan, a, b).to(F32).to(dtype)
+            assert torch.equal(call(op, plan, a, b, dtype), want), (op, counts, N, D)
