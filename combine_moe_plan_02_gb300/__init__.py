@@ -39,7 +39,9 @@ __all__ = [
     "moe_combine_dedup", "moe_plan_workspace_size", "moe_group_plan_workspace_size",
     "moe_combine_backward", "moe_dispatch_backward", "moe_expert_gemm", "moe_expert_gemm_dgrad",
     "moe_expert_gemm_wgrad", "moe_grad_norm", "moe_clip_grad_norm",
-    "moe_device_errors", "moe_plan_capacity", "Plan", "GroupPlan", "CapacityPlan", "MoeError",
+    "moe_quant_mxfp4", "moe_dispatch_quant_mxfp4", "moe_swiglu_quant_mxfp4", "moe_dequant_mxfp4",
+    "moe_expert_gemm_mxfp4",
+    "moe_device_errors", "moe_plan_capacity", "Plan", "GroupPlan", "CapacityPlan", "MxFp4", "MoeError",
     "MoeOp", "Routing", "lib",
 ]
 
@@ -591,6 +593,137 @@ def moe_clip_grad_norm(grads: Sequence[torch.Tensor], max_norm: float, *,
     into `out` (tensors of the same types and sizes).  Returns the norm before
     it, float32 [1] on the device."""
     return _grad_call("moe_clip_grad_norm", grads, max_norm, out, norm, workspace, stream)
+
+
+class MxFp4(NamedTuple):
+    """A [rows, D] or [E, rows, D] tensor in MXFP4: E2M1 codes, two a byte, and
+    one E8M0 scale byte for 32 elements of a row, four to a row's word."""
+    codes: torch.Tensor        # uint8 [.., rows, D / 2]
+    scales: torch.Tensor       # uint8 [.., ceil(D / 128), rows, 4]
+
+    @property
+    def shape(self):
+        """The shape of the values."""
+        return torch.Size((*self.codes.shape[:-1], 2 * self.codes.shape[-1]))
+
+
+def _check_mx(name: str, q: MxFp4, dims: Sequence[int] = (2, 3)):
+    """Raises unless codes and scales are what the kernels read."""
+    codes, scales = q
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise TypeError(f"{name} must have uint8 codes and scales")
+    shape = codes.shape
+    if len(shape) not in dims or shape[-1] % 16:
+        raise ValueError(f"{name} must hold rows of a multiple of 32 elements")
+    if tuple(scales.shape) != (*shape[:-2], -(-shape[-1] // 64), shape[-2], 4):
+        raise ValueError(f"{name}'s scales must be [.., ceil(D / 128), rows, 4]")
+    if codes.device != scales.device:
+        raise ValueError(f"{name}'s codes and scales must live on one device")
+
+
+def _mx_out(name: str, out: Optional[MxFp4], lead, rows: int, D: int, device, stream) -> MxFp4:
+    if out is None:
+        return MxFp4(_empty((*lead, rows, D // 2), torch.uint8, device, stream),
+                     _empty((*lead, -(-D // 128), rows, 4), torch.uint8, device, stream))
+    _check_mx(name, out)
+    if tuple(out.shape) != (*lead, rows, D):
+        raise ValueError(f"{name} must be {[*lead, rows, D]}")
+    return out
+
+
+def _values(x: torch.Tensor, name: str, D: int):
+    if x.dtype not in _TORCH_DT.values():
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    if D < 32 or D % 32:
+        raise ValueError("MXFP4 rows must be a multiple of 32 elements")
+
+
+def moe_quant_mxfp4(x: torch.Tensor, *, out: Optional[MxFp4] = None, stream=None) -> MxFp4:
+    """Rows [rows, D] or weights [E, rows, D] (bf16 or f32) to MXFP4."""
+    if x.dim() not in (2, 3):
+        raise ValueError("x must be [rows, D] or [E, rows, D]")
+    *lead, rows, D = x.shape
+    _values(x, "x", D)
+    out = _mx_out("out", out, lead, rows, D, x.device, stream)
+    _abi.check("moe_quant_mxfp4", lib().moe_quant_mxfp4(
+        _ptr(x), _dt(x), lead[0] if lead else 1, rows, D, _ptr(out.codes), _ptr(out.scales),
+        _stream(stream, x)))
+    return out
+
+
+def moe_dispatch_quant_mxfp4(x: torch.Tensor, tok_map: torch.Tensor, *,
+                             out: Optional[MxFp4] = None, stream=None) -> MxFp4:
+    """Rows [S, D] (bf16 or f32) to MXFP4 in the K packed rows of each token.
+    Without `out` there are S * K packed rows, rounded up to a multiple of 4 as
+    moe_expert_gemm_mxfp4 asks."""
+    if x.dim() != 2 or tok_map.dim() != 2 or tok_map.shape[0] != x.shape[0]:
+        raise ValueError("x must be [S, D] and tok_map [S, K]")
+    if tok_map.dtype != torch.int64:
+        raise TypeError("tok_map must be int64")
+    S, D = x.shape
+    _values(x, "x", D)
+    K = tok_map.shape[1]
+    if out is None:
+        out = _mx_out("out", None, (), max(-(-S * K // 4) * 4, 4), D, x.device, stream)
+    else:
+        _check_mx("out", out, (2,))
+        if out.shape[1] != D:
+            raise ValueError("out must hold rows of D elements")
+    _abi.check("moe_dispatch_quant_mxfp4", lib().moe_dispatch_quant_mxfp4(
+        _ptr(x), _dt(x), S, D, K, _ptr(tok_map), _ptr(out.codes), _ptr(out.scales), out.shape[0],
+        _stream(stream, x)))
+    return out
+
+
+def moe_swiglu_quant_mxfp4(u: torch.Tensor, *, out: Optional[MxFp4] = None,
+                           stream=None) -> MxFp4:
+    """silu(gate) * up of rows u [rows, 2 F] (gates before ups, bf16 or f32),
+    in f32, to MXFP4 [rows, F]."""
+    if u.dim() != 2 or u.shape[1] % 2:
+        raise ValueError("u must be [rows, 2 F]")
+    rows, F = u.shape[0], u.shape[1] // 2
+    _values(u, "u", F)
+    out = _mx_out("out", out, (), rows, F, u.device, stream)
+    _abi.check("moe_swiglu_quant_mxfp4", lib().moe_swiglu_quant_mxfp4(
+        _ptr(u), _dt(u), rows, F, _ptr(out.codes), _ptr(out.scales), _stream(stream, u)))
+    return out
+
+
+def moe_dequant_mxfp4(q: MxFp4, *, out_dtype: torch.dtype = torch.bfloat16,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values that MXFP4 rows or weights stand for."""
+    _check_mx("q", q)
+    shape = q.shape
+    if out is None:
+        if out_dtype not in _TORCH_DT.values():
+            raise TypeError(f"unsupported output dtype {out_dtype}")
+        out = _empty(shape, out_dtype, q.codes.device, stream)
+    elif out.shape != shape or out.dtype not in _TORCH_DT.values():
+        raise ValueError("out must be bfloat16 or float32 with the shape of the values")
+    _abi.check("moe_dequant_mxfp4", lib().moe_dequant_mxfp4(
+        _ptr(q.codes), _ptr(q.scales), shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1],
+        _ptr(out), _dt(out), _stream(stream, q.codes)))
+    return out
+
+
+def moe_expert_gemm_mxfp4(x: MxFp4, w: MxFp4, plan: Union[Plan, CapacityPlan], *,
+                          out_dtype: torch.dtype = torch.bfloat16,
+                          out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y[r] = w[e] x[r] for the rows of each bucket e of the plan, zero on rows
+    in no bucket.  x [rows, D] (rows of the buffer a multiple of 4), w
+    [E, N, D], both in MXFP4; y [rows, N]."""
+    _check_mx("x", x, (2,))
+    _check_mx("w", w, (3,))
+    rows, D = x.shape
+    E, N, _ = w.shape
+    if w.shape[2] != D:
+        raise ValueError("w must be [E, N, D] and x [rows, D]")
+    _check_plan(plan, E)
+    out = _expert_out(out, (rows, N), out_dtype, x.codes.device, stream)
+    _abi.check("moe_expert_gemm_mxfp4", lib().moe_expert_gemm_mxfp4(
+        _ptr(x.codes), _ptr(x.scales), rows, _ptr(w.codes), _ptr(w.scales), N, D, E,
+        _ptr(plan.cnt), _ptr(plan.off), _ptr(out), _dt(out), _stream(stream, x.codes)))
+    return out
 
 
 def moe_device_errors() -> int:

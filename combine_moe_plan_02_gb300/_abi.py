@@ -49,6 +49,11 @@ SIGNATURES = {
     "moe_grad_norm_workspace_size": (SZ, []),
     "moe_grad_norm": (I32, [P, P, P, I32, P, P, SZ, P]),
     "moe_clip_grad_norm": (I32, [P, P, P, P, I32, ctypes.c_float, P, P, SZ, P]),
+    "moe_quant_mxfp4": (I32, [P, I32, I64, I64, I64, P, P, P]),
+    "moe_dispatch_quant_mxfp4": (I32, [P, I32, I64, I64, I32, P, P, P, I64, P]),
+    "moe_swiglu_quant_mxfp4": (I32, [P, I32, I64, I64, P, P, P]),
+    "moe_dequant_mxfp4": (I32, [P, P, I64, I64, I64, P, I32, P]),
+    "moe_expert_gemm_mxfp4": (I32, [P, P, I64, P, P, I64, I64, I32, P, P, P, I32, P]),
     "moe_device_errors": (I32, [P]),
     "moe_selftest_wait_timeout": (I32, [I64, P]),
     "moe_selftest_convert": (I32, [ctypes.c_uint32, I64, P, P, P]),

@@ -50,9 +50,8 @@
 // launch control instead of the fixed walk measured 1 % slower, tiles of 512
 // columns 33 % (the next tile waits for both accumulators' stores).
 
-#include "common.cuh"
+#include "pair.cuh"
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 
 namespace moe {
@@ -72,7 +71,6 @@ constexpr int kMaxStages = 10;
 constexpr int kBoxArea = 2048;      // of each storing warp
 constexpr int kSplitRows = 64;      // rows of a call whose reductions may be split
 constexpr int kSplitBytes = kSplitRows * kLanes * 4;  // one pair's sums, in each CTA
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per mbarrier wait
 
 __device__ uint32_t g_expert_error;  // kErrExpertTimeout | kErrExpertBucket
 
@@ -115,20 +113,6 @@ template <int MODE, typename Tout, int JOIN> struct Boxes {
 
 // --- tcgen05 ---------------------------------------------------------------
 
-__device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t cols)
-{
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(slot)),
-                 "r"(cols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-}
-
-__device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-}
-
 __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          bool add)
 {
@@ -138,76 +122,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
         "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
         : "memory");
-}
-
-// Arrives on `bar` of both CTAs of the pair (`lead` is the first one's rank) when
-// the matrix instructions issued so far are done.
-__device__ __forceinline__ void mma_commit(uint64_t *bar, uint32_t lead)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)(3u << lead))
-        : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before()
-{
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after()
-{
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
-// 32 columns of this warp's 32 lanes: thread = lane, register = column.  The
-// values may be used after tmem_wait, which the compiler sees to write them.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
-        : "r"(addr));
-}
-
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-                 "%10, %11, %12, %13, %14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                   "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                   "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(addr));
-}
-
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[32])
-{
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
 }
 
 // Shared-memory operand descriptor, 128-byte swizzle.  Rows along the
@@ -226,78 +140,6 @@ __device__ __forceinline__ uint32_t instr_desc(int n, bool a_mn, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kM >> 4) << 24);
-}
-
-// --- the pair ----------------------------------------------------------------
-
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// The address of a shared variable in the CTA of that rank.
-__device__ __forceinline__ uint32_t addr_in(const void *p, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-                 "barrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
-}
-
-// Arrivals at a barrier of either CTA.  They hand over tensor memory or a copy's
-// byte count and order nothing themselves: the copy and the tcgen05 fences do.
-// A release at cluster scope costs 0.4 us of every block (1745 against 885 us
-// for 64 buckets of 512 rows, 2048 x 7168).
-__device__ __forceinline__ void arrive_at(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-                 : "memory");
-}
-
-__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(
-                     bar),
-                 "r"(bytes)
-                 : "memory");
-}
-
-// TMA copies into this CTA; `bar` may be either CTA's barrier.
-__device__ __forceinline__ void tma_2d(void *dst, const CUtensorMap *map, uint32_t bar, int x,
-                                       int y)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, uint32_t bar, int x,
-                                       int y, int z)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile"
-        ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
-        : "memory");
 }
 
 // Rows y .. y + len of 64 columns, in boxes of rows inside their tensor, one for
@@ -359,53 +201,6 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *sr
             "r"(smem_u32(src)), "r"(x), "r"(y)
             : "memory");
 }
-
-// --- bounded waits -----------------------------------------------------------
-
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Waits for phase `parity`; false once the limit ran out here or, with
-// `stop`, in another warp of the CTA.
-__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
-{
-    // reading the timer costs about as much as a block of products: probe
-    // first
-    uint64_t t0 = 0;
-    for (;;) {
-        for (int i = 0; i < 256; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t t = now_ns();
-        if (t0 == 0) t0 = t;
-        if ((stop && *stop) || t - t0 > kWaitLimitNs) return false;
-    }
-}
-
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *stop)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    if (wait_slow(bar, parity, stop)) return true;
-    *stop = 1;
-    return false;
-}
-
-// A place in the ring and the parity of its current round.
-struct Ring {
-    int stages, at = 0;
-    uint32_t round = 0;
-    __device__ __forceinline__ explicit Ring(int n) : stages(n) {}
-    __device__ __forceinline__ void next()
-    {
-        if (++at == stages) {
-            at = 0;
-            round ^= 1;
-        }
-    }
-};
 
 // Parts of a tile's reduction that have an accumulator each.  The tensor core
 // cuts a sum's low bits off at every step of 16, which after 1048 products
@@ -1007,25 +802,6 @@ expert_kernel(const __grid_constant__ Maps<MODE> maps, ExpertArgs a)
 }
 
 // --- host ----------------------------------------------------------------------
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn()
-{
-    static EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult got = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &got) != cudaSuccess ||
-            got != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
 
 // A map over [depth, rows, width] (2-D when depth is 0).
 cudaError_t encode(CUtensorMap *map, const void *base, bool f32, int64_t width, int64_t rows,

@@ -1,0 +1,350 @@
+// MXFP4 rows and weights: quantisation, also on the way into the experts'
+// buckets and behind a gated activation, and back to values.
+//
+// The OCP Microscaling format v1.0 with E2M1 elements: 32 elements of a row
+// share a scale 2^(s - 127), s one byte (E8M0, 255 is NaN).  With a the largest
+// magnitude of a block, s = floor(log2 a) - 2 + 127, clamped at 0 (so that the
+// largest element lands in 4 .. 8, where E2M1 ends at 6), and each code is
+// v / 2^(s - 127) rounded to nearest even, saturating at 6.  The division is by a power
+// of two and exact wherever the quotient rounds to anything but zero, so the
+// codes are a pure function of the values.  A block with an infinite or NaN
+// element gets s = 255 and codes of zero: all of it reads back as NaN.
+//
+// Layout of a [rows, D] tensor: codes [rows, D / 2], element 2i in the low half
+// of byte i; scales [ceil(D / 128)][rows][4], the four blocks of 128 elements in
+// one word and the words of neighbouring rows side by side, as the experts'
+// product copies them (csrc/expert_gemm_mxfp4.cu).  Blocks past D are zero.
+//
+// A warp takes 512 elements of a row: 16 a lane, two lanes a block, 8 bytes of
+// codes a lane, and every eighth lane a word of scales.  A row that goes to K
+// buckets is read and rounded once and stored K times.
+
+#include "common.cuh"
+
+#include <cuda_bf16.h>
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kLane = 16;             // elements of a lane
+constexpr int kUnit = 32 * kLane;     // of a warp
+constexpr int kWaves = 8;             // resident waves of the largest grid
+
+__device__ uint32_t g_mxfp4_error;  // kErrDispatchIndex
+
+struct QuantArgs {
+    const uint8_t *x;       // [S, D], gated [S, 2 D]
+    const int64_t *map;     // [S, K] destination rows, or null: row s to row s
+    int64_t S, D;
+    int64_t rows;           // destination rows
+    int64_t group;          // rows that share a scale array
+    int K;
+    uint8_t *codes;         // [rows, D / 2]
+    uint32_t *scales;       // [rows / group][ceil(D / 128)][group]
+};
+
+template <typename T> struct Sixteen;
+template <> struct Sixteen<float> {
+    static constexpr int kBytes = 64;
+    __device__ __forceinline__ static void load(const uint8_t *p, float (&f)[kLane])
+    {
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = ld_stream16(p + 16 * q);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f[4 * q] = __uint_as_float(v[q].x);
+            f[4 * q + 1] = __uint_as_float(v[q].y);
+            f[4 * q + 2] = __uint_as_float(v[q].z);
+            f[4 * q + 3] = __uint_as_float(v[q].w);
+        }
+    }
+    __device__ __forceinline__ static void store(uint8_t *p, const float (&f)[kLane])
+    {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            st16_cs(p + 16 * q,
+                    make_uint4(__float_as_uint(f[4 * q]), __float_as_uint(f[4 * q + 1]),
+                               __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3])));
+    }
+};
+template <> struct Sixteen<__nv_bfloat16> {
+    static constexpr int kBytes = 32;
+    __device__ __forceinline__ static void load(const uint8_t *p, float (&f)[kLane])
+    {
+        const uint4 v[2] = {ld_stream16(p), ld_stream16(p + 16)};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f[8 * q + 2 * i] = __uint_as_float(u[i] << 16);
+                f[8 * q + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            }
+        }
+    }
+    __device__ __forceinline__ static void store(uint8_t *p, const float (&f)[kLane])
+    {
+        uint32_t u[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        st16_cs(p, make_uint4(u[0], u[1], u[2], u[3]));
+        st16_cs(p + 16, make_uint4(u[4], u[5], u[6], u[7]));
+    }
+};
+
+// Four pairs of values as eight codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t e2m1x8(const float *f)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
+    return r;
+}
+
+template <typename T, bool GATED>
+__global__ void __launch_bounds__(kThreads) quant_kernel(QuantArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t W = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t chunks = (a.D + kUnit - 1) / kUnit, words = (a.D + 127) / 128;
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < a.S * chunks;
+         u += W) {
+        const int64_t s = u / chunks, c = u - s * chunks;
+        const int64_t at = c * kUnit + lane * kLane;  // first element of this lane
+        const bool in = at < a.D;                     // D is a multiple of two lanes
+        const int64_t mine = a.map && lane < a.K ? __ldg(a.map + s * a.K + lane) : s;
+        float f[kLane];
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) f[i] = 0.0f;
+        if (in) {
+            const uint8_t *p = a.x + (s * a.D * (GATED ? 2 : 1) + at) * (int64_t)sizeof(T);
+            Sixteen<T>::load(p, f);
+            if (GATED) {
+                // f32 with the fast exponential and division: a few units in the
+                // last place of 24 bits (2^-17 where exp(-gate) is 2^100), where
+                // the codes that follow keep two bits
+                float up[kLane];
+                Sixteen<T>::load(p + a.D * (int64_t)sizeof(T), up);
+#pragma unroll
+                for (int i = 0; i < kLane; ++i)
+                    f[i] = __fdividef(f[i], 1.0f + __expf(-f[i])) * up[i];
+            }
+        }
+        uint32_t top = 0;  // of the magnitudes' patterns; a NaN's is above them all
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        const int e = (int)(top >> 23);
+        const uint32_t byte = e == 255 ? 255u : (uint32_t)max(e - 2, 0);
+        const float inv = __uint_as_float((254u - min(byte, 253u)) << 23);  // 2^(127 - byte)
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) f[i] *= inv;
+        uint2 code = make_uint2(e2m1x8(f), e2m1x8(f + 8));
+        if (byte == 255) code = make_uint2(0, 0);
+        uint32_t word = byte;
+        word |= __shfl_down_sync(0xffffffffu, word, 2) << 8;
+        word = (word & 0xffffu) | __shfl_down_sync(0xffffffffu, word, 4) << 16;
+        const int64_t w = c * 4 + (lane >> 3);
+        const bool holds = (lane & 7) == 0 && w < words;
+        const int n = a.map ? a.K : 1;
+        for (int k = 0; k < n; ++k) {
+            const int64_t r = __shfl_sync(0xffffffffu, mine, k);
+            if (r < 0 || r >= a.rows) {
+                if (r != -1 && lane == 0) atomicOr(&g_mxfp4_error, kErrDispatchIndex);
+                continue;
+            }
+            if (in) st8(a.codes + r * (a.D / 2) + at / 2, code);
+            if (holds) {
+                const int64_t g = a.map ? 0 : r / a.group;
+                a.scales[(g * words + w) * a.group + (r - g * a.group)] = word;
+            }
+        }
+    }
+}
+
+struct DequantArgs {
+    const uint8_t *codes;
+    const uint32_t *scales;
+    int64_t rows, D, group;
+    uint8_t *out;  // [rows, D]
+};
+
+template <typename T> __global__ void __launch_bounds__(kThreads) dequant_kernel(DequantArgs a)
+{
+    const int lane = threadIdx.x & 31;
+    const int64_t W = (int64_t)gridDim.x * (kThreads / 32);
+    const int64_t chunks = (a.D + kUnit - 1) / kUnit, words = (a.D + 127) / 128;
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+         u < a.rows * chunks; u += W) {
+        const int64_t r = u / chunks, c = u - r * chunks;
+        const int64_t at = c * kUnit + lane * kLane;
+        if (at >= a.D) continue;
+        const int64_t g = r / a.group;
+        const uint2 code = ld_stream8(a.codes + r * (a.D / 2) + at / 2);
+        const uint32_t word = __ldg(a.scales + (g * words + c * 4 + (lane >> 3)) * a.group +
+                                    (r - g * a.group));
+        const uint32_t byte = word >> ((lane >> 1 & 3) * 8) & 255u;
+        const float scale = __uint_as_float(byte == 255 ? 0x7fffffffu
+                                            : byte     ? byte << 23
+                                                       : 0x00400000u);
+        const uint32_t q[2] = {code.x, code.y};
+        float f[kLane];
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) {
+            // the code's exponent and mantissa as those of an f32: 2^-126 of its
+            // value, subnormal where it is
+            const uint32_t nibble = q[i >> 3] >> (4 * (i & 7));
+            f[i] = __uint_as_float((nibble & 7u) << 22 | (nibble & 8u) << 28) * 0x1p126f * scale;
+        }
+        Sixteen<T>::store(a.out + (r * a.D + at) * (int64_t)sizeof(T), f);
+    }
+}
+
+template <auto KERNEL, typename Args>
+int launch_units(const Args &a, int64_t units, cudaStream_t stream)
+{
+    static KernelCache kc;
+    int per_sm = 0;
+    cudaError_t e = prepare_kernel(KERNEL, 0, kThreads, kc, &per_sm);
+    if (e == cudaSuccess) {
+        const int64_t warps = kThreads / 32, most = (int64_t)sm_count() * per_sm * kWaves;
+        const int64_t grid = (units + warps - 1) / warps;
+        e = launch_pdl(KERNEL, dim3((unsigned)(grid < most ? grid : most)), dim3(kThreads), 0,
+                       stream, a);
+    }
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    return check_launch();
+}
+
+int64_t units_of(int64_t rows, int64_t D) { return rows * ((D + kUnit - 1) / kUnit); }
+
+constexpr int64_t kMaxWidth = 1 << 24;
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// What all of these calls ask of a tensor of `groups` [rows, D].
+int check_tensor(int64_t groups, int64_t rows, int64_t D)
+{
+    if (groups < 0 || rows < 0 || D < 1 || D >= kMaxWidth) return MOE_EINVAL;
+    if (groups > 0 && rows >= ((int64_t)1 << 31) / groups) return MOE_EINVAL;
+    return MOE_OK;
+}
+
+template <bool GATED> int run_quant(QuantArgs a, int dtype, cudaStream_t stream)
+{
+    const int64_t units = units_of(a.S, a.D);
+    if (dtype == MOE_F32) return launch_units<quant_kernel<float, GATED>>(a, units, stream);
+    return launch_units<quant_kernel<__nv_bfloat16, GATED>>(a, units, stream);
+}
+
+} // namespace
+} // namespace moe
+
+using namespace moe;
+
+MOE_EXPORT int moe_quant_mxfp4(const void *x, int dtype, int64_t groups, int64_t rows, int64_t D,
+                               uint8_t *codes, uint8_t *scales, moe_stream_t stream)
+{
+    MOE_TRACE("moe_quant_mxfp4");
+    if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_EINVAL;
+    if (check_tensor(groups, rows, D) != MOE_OK) return MOE_EINVAL;
+    if (groups == 0 || rows == 0) return MOE_OK;
+    if (!x || !codes || !scales) return MOE_EINVAL;
+    if (D % 32 || !aligned16(x) || !aligned16(codes) || !aligned4(scales)) return MOE_EALIGN;
+    QuantArgs a = {};
+    a.x = static_cast<const uint8_t *>(x);
+    a.S = a.rows = groups * rows;
+    a.D = D;
+    a.group = rows;
+    a.codes = codes;
+    a.scales = reinterpret_cast<uint32_t *>(scales);
+    return run_quant<false>(a, dtype, (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_dispatch_quant_mxfp4(const void *x, int dtype, int64_t S, int64_t D, int K,
+                                        const int64_t *tok_map, uint8_t *codes, uint8_t *scales,
+                                        int64_t packed_rows, moe_stream_t stream)
+{
+    MOE_TRACE("moe_dispatch_quant_mxfp4");
+    if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_EINVAL;
+    if (S < 0 || K < 1 || K > 32 || S >= ((int64_t)1 << 31) / K) return MOE_EINVAL;
+    if (check_tensor(1, packed_rows, D) != MOE_OK) return MOE_EINVAL;
+    if (S == 0) return MOE_OK;
+    if (packed_rows < 1 || !x || !tok_map || !codes || !scales) return MOE_EINVAL;
+    if (D % 32 || !aligned16(x) || !aligned16(codes) || !aligned4(scales)) return MOE_EALIGN;
+    QuantArgs a = {};
+    a.x = static_cast<const uint8_t *>(x);
+    a.map = tok_map;
+    a.S = S;
+    a.D = D;
+    a.rows = a.group = packed_rows;
+    a.K = K;
+    a.codes = codes;
+    a.scales = reinterpret_cast<uint32_t *>(scales);
+    return run_quant<false>(a, dtype, (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_swiglu_quant_mxfp4(const void *u, int dtype, int64_t rows, int64_t F,
+                                      uint8_t *codes, uint8_t *scales, moe_stream_t stream)
+{
+    MOE_TRACE("moe_swiglu_quant_mxfp4");
+    if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_EINVAL;
+    if (check_tensor(1, rows, F) != MOE_OK) return MOE_EINVAL;
+    if (rows == 0) return MOE_OK;
+    if (!u || !codes || !scales) return MOE_EINVAL;
+    if (F % 32 || !aligned16(u) || !aligned16(codes) || !aligned4(scales)) return MOE_EALIGN;
+    QuantArgs a = {};
+    a.x = static_cast<const uint8_t *>(u);
+    a.S = a.rows = a.group = rows;
+    a.D = F;
+    a.codes = codes;
+    a.scales = reinterpret_cast<uint32_t *>(scales);
+    return run_quant<true>(a, dtype, (cudaStream_t)stream);
+}
+
+MOE_EXPORT int moe_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t groups,
+                                 int64_t rows, int64_t D, void *out, int out_dtype,
+                                 moe_stream_t stream)
+{
+    MOE_TRACE("moe_dequant_mxfp4");
+    if (out_dtype != MOE_BF16 && out_dtype != MOE_F32) return MOE_EINVAL;
+    if (check_tensor(groups, rows, D) != MOE_OK) return MOE_EINVAL;
+    if (groups == 0 || rows == 0) return MOE_OK;
+    if (!codes || !scales || !out) return MOE_EINVAL;
+    if (D % 32 || !aligned16(codes) || !aligned4(scales) || !aligned16(out)) return MOE_EALIGN;
+    DequantArgs a = {codes, reinterpret_cast<const uint32_t *>(scales), groups * rows, D, rows,
+                     static_cast<uint8_t *>(out)};
+    const int64_t units = units_of(a.rows, D);
+    return out_dtype == MOE_F32
+               ? launch_units<dequant_kernel<float>>(a, units, (cudaStream_t)stream)
+               : launch_units<dequant_kernel<__nv_bfloat16>>(a, units, (cudaStream_t)stream);
+}
+
+namespace moe {
+// Reads and clears this file's device error bits.
+cudaError_t read_mxfp4_errors(uint32_t *flags)
+{
+    uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_mxfp4_error, sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_mxfp4_error, &zero, sizeof(uint32_t));
+    return e;
+}
+} // namespace moe

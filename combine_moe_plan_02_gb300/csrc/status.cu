@@ -50,16 +50,18 @@ MOE_EXPORT int moe_last_cuda_error(void) { return moe::t_last_cuda_error; }
 MOE_EXPORT int moe_device_errors(uint32_t *flags)
 {
     if (!flags) return MOE_EINVAL;
-    uint32_t a = 0, b = 0, c = 0, d = 0, x = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, x = 0, m = 0, g = 0;
     cudaError_t e = moe::read_dispatch_errors(&a);
     if (e == cudaSuccess) e = moe::read_combine_errors(&b);
     if (e == cudaSuccess) e = moe::read_plan_dispatch_errors(&c);
     if (e == cudaSuccess) e = moe::read_backward_errors(&d);
     if (e == cudaSuccess) e = moe::read_expert_errors(&x);
+    if (e == cudaSuccess) e = moe::read_mxfp4_errors(&m);
+    if (e == cudaSuccess) e = moe::read_mxgemm_errors(&g);
     if (e != cudaSuccess) {
         moe::set_cuda_error(e);
         return MOE_ECUDA;
     }
-    *flags = a | b | c | d | x;
+    *flags = a | b | c | d | x | m | g;
     return MOE_OK;
 }

@@ -481,6 +481,67 @@ int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N
                           moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * MXFP4 rows and weights: the OCP Microscaling format v1.0 with E2M1 elements
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), 32 of a row sharing a scale
+ * 2^(s - 127), s one byte (E8M0).  For a block with largest magnitude a:
+ *   s       = max(floor(log2 a) - 2 + 127, 0); 0 for an all-zero block
+ *   code    = E2M1(v / 2^(s - 127)), nearest even, saturating at +-6
+ * A block with an infinite or NaN element has s = 255 and codes of zero, and
+ * reads back as NaN.
+ *
+ * A [rows, D] tensor, D a multiple of 32, is held as
+ *   codes  uint8 [rows, D / 2]           element 2i in the low half of byte i
+ *   scales uint8 [ceil(D / 128), rows, 4] blocks 4g .. 4g + 3 of row r in
+ *                                        scales[g, r]; zero past D
+ * and `groups` such tensors (an expert each) one after another in both.
+ *
+ *   moe_quant_mxfp4           x [groups, rows, D] to codes and scales
+ *   moe_dispatch_quant_mxfp4  x [S, D], row s to the packed rows tok_map[s, k]
+ *       >= 0 (int64 [S, K] from moe_plan or moe_plan_capacity); an entry outside
+ *       [-1, packed_rows) is skipped and flagged (bit 1); other rows are left
+ *       untouched
+ *   moe_swiglu_quant_mxfp4    u [rows, 2 F], gates before ups:
+ *       h[r, f] = u[r, f] / (1 + exp(-u[r, f])) * u[r, F + f] in f32, quantised
+ *   moe_dequant_mxfp4         the values, [groups, rows, D] of out_dtype (exact
+ *       where the value is in the type's range)
+ *
+ * x, u of dtype MOE_BF16 or MOE_F32.  groups * rows < 2^31, D < 2^24.
+ * Alignment: rows and codes 16-byte aligned, scales 4-byte aligned (16-byte, and
+ * the rows of a tensor a multiple of 4, for moe_expert_gemm_mxfp4); D and F
+ * multiples of 32.
+ * ---------------------------------------------------------------------- */
+int moe_quant_mxfp4(const void *x, int dtype, int64_t groups, int64_t rows, int64_t D,
+                    uint8_t *codes, uint8_t *scales, moe_stream_t stream);
+int moe_dispatch_quant_mxfp4(const void *x, int dtype, int64_t S, int64_t D, int K,
+                             const int64_t *tok_map, uint8_t *codes, uint8_t *scales,
+                             int64_t packed_rows, moe_stream_t stream);
+int moe_swiglu_quant_mxfp4(const void *u, int dtype, int64_t rows, int64_t F, uint8_t *codes,
+                           uint8_t *scales, moe_stream_t stream);
+int moe_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t groups, int64_t rows,
+                      int64_t D, void *out, int out_dtype, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The experts' product with rows and weights in MXFP4:
+ *   y[r, n] = sum_d x[r, d] * w[e, n, d]      for r in bucket e of a plan
+ * with the values that codes and scales stand for, f32 sums, rounded once to the
+ * output's type (MOE_BF16 or MOE_F32).  Output rows in no bucket are zero; such
+ * rows and experts without rows are never used, whatever they hold.  A bucket
+ * outside [0, rows) is left out and flagged (bit 5); buckets must not overlap.
+ *
+ * x_codes [rows, D / 2], x_scales [ceil(D / 128), rows, 4]; w_codes [E, N, D / 2],
+ * w_scales [E, ceil(D / 128), N, 4]: as moe_dispatch_quant_mxfp4,
+ * moe_swiglu_quant_mxfp4 and moe_quant_mxfp4 write them; a scale past D must not
+ * be 255.  y [rows, N].  cnt and off are read on the device.
+ * 0 <= rows < 2^31, N < 2^24, D <= 32768, E * ceil(N / 256) * (rows / 256 + 2) <
+ * 2^31.  Alignment: all pointers 16-byte aligned; rows a multiple of 4 (those of a
+ * buffer, not of a bucket), N of 8, D of 32.
+ * ---------------------------------------------------------------------- */
+int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64_t rows,
+                          const uint8_t *w_codes, const uint8_t *w_scales, int64_t N, int64_t D,
+                          int E, const int32_t *cnt, const int64_t *off, void *y, int y_dtype,
+                          moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Global L2 norm over many gradients, and clipping to a limit:
  *   norm[0] = sqrt(sum over all tensors of g^2)
  *   out[i]  = min(1, max_norm / (norm + 1e-6)) * grads[i], rounded once
