@@ -31,7 +31,7 @@ from typing import NamedTuple, Optional, Sequence, Union
 import torch
 
 from . import _abi
-from ._abi import MoeError, MOE_BF16, MOE_F32, MOE_FP8_E4M3  # noqa: F401
+from ._abi import MoeError, MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_MXFP4  # noqa: F401
 
 __all__ = [
     "moe_plan", "moe_group_plan", "moe_dispatch", "moe_plan_dispatch", "moe_dispatch_dedup", "moe_dispatch_quant_fp8",
@@ -40,7 +40,7 @@ __all__ = [
     "moe_combine_backward", "moe_dispatch_backward", "moe_expert_gemm", "moe_expert_gemm_dgrad",
     "moe_expert_gemm_wgrad", "moe_grad_norm", "moe_clip_grad_norm",
     "moe_quant_mxfp4", "moe_dispatch_quant_mxfp4", "moe_swiglu_quant_mxfp4", "moe_dequant_mxfp4",
-    "moe_expert_gemm_mxfp4",
+    "moe_expert_gemm_mxfp4", "moe_expert_layer", "moe_expert_layer_workspace_size",
     "moe_device_errors", "moe_plan_capacity", "Plan", "GroupPlan", "CapacityPlan", "MxFp4", "MoeError",
     "MoeOp", "Routing", "lib",
 ]
@@ -723,6 +723,50 @@ def moe_expert_gemm_mxfp4(x: MxFp4, w: MxFp4, plan: Union[Plan, CapacityPlan], *
     _abi.check("moe_expert_gemm_mxfp4", lib().moe_expert_gemm_mxfp4(
         _ptr(x.codes), _ptr(x.scales), rows, _ptr(w.codes), _ptr(w.scales), N, D, E,
         _ptr(plan.cnt), _ptr(plan.off), _ptr(out), _dt(out), _stream(stream, x.codes)))
+    return out
+
+
+def moe_expert_layer_workspace_size(S: int, H: int, K: int, E: int, F: int) -> int:
+    return int(lib().moe_expert_layer_workspace_size(S, H, K, E, F))
+
+
+def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
+                     w_up: Union[torch.Tensor, MxFp4], w_down: Union[torch.Tensor, MxFp4], *,
+                     out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[s] = sum_k topk_w[s,k] * w_down[e] (silu(gate) * up), (gate, up) =
+    w_up[e] x[s], e = topk_idx[s,k], for up to 1024 entries S * K.  x bf16
+    [S, H]; w_up [E, 2 F, H] (gates before ups) and w_down [E, H, F] both bf16
+    or both in MXFP4.  Ids outside [0, E) give nothing."""
+    mx = not isinstance(w_up, torch.Tensor)
+    if mx == isinstance(w_down, torch.Tensor):
+        raise TypeError("w_up and w_down must both be tensors or both MxFp4")
+    if mx:
+        _check_mx("w_up", w_up, (3,))
+        _check_mx("w_down", w_down, (3,))
+    elif w_up.dtype != torch.bfloat16 or w_down.dtype != torch.bfloat16:
+        raise TypeError("weights must be bfloat16 or MxFp4")
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise TypeError("x must be bfloat16 [S, H]")
+    S, H = x.shape
+    shape, down = w_up.shape, w_down.shape
+    if len(shape) != 3 or len(down) != 3 or shape[1] % 2 or shape[2] != H or \
+            tuple(down) != (shape[0], H, shape[1] // 2):
+        raise ValueError("w_up must be [E, 2 F, H] and w_down [E, H, F]")
+    if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2 or topk_idx.shape[0] != S:
+        raise TypeError("topk_idx must be int32 [S, K]")
+    if topk_w.dtype != torch.float32 or topk_w.shape != topk_idx.shape:
+        raise TypeError("topk_w must be float32 with the shape of topk_idx")
+    E, F, K = shape[0], shape[1] // 2, topk_idx.shape[1]
+    out = _expert_out(out, (S, H), out_dtype, x.device, stream)
+    L = lib()
+    nws = int(L.moe_expert_layer_workspace_size(S, H, K, E, F))
+    ws = _workspace(nws, x.device, workspace, stream)
+    up, down = (w if mx else (w, None) for w in (w_up, w_down))
+    _abi.check("moe_expert_layer", L.moe_expert_layer(
+        _ptr(x), S, H, _ptr(topk_idx), _ptr(topk_w), K, E, F, MOE_MXFP4 if mx else MOE_BF16,
+        _ptr(up[0]), _ptr(up[1]), _ptr(down[0]), _ptr(down[1]), _ptr(out), _dt(out), _ptr(ws), nws,
+        _stream(stream, x)))
     return out
 
 

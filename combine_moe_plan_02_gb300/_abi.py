@@ -16,7 +16,7 @@ LIB_PATH = os.environ.get("MOE_GB300_LIB") or os.path.join(PKG, "libmoe_gb300.so
 HEADER = os.path.join(os.path.dirname(PKG), "include", "moe_plan.h")
 
 MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_ECUDA = 0, 1, 2, 3
-MOE_BF16, MOE_F32, MOE_FP8_E4M3 = 0, 1, 2
+MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_MXFP4 = 0, 1, 2, 3
 
 P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
 
@@ -54,6 +54,9 @@ SIGNATURES = {
     "moe_swiglu_quant_mxfp4": (I32, [P, I32, I64, I64, P, P, P]),
     "moe_dequant_mxfp4": (I32, [P, P, I64, I64, I64, P, I32, P]),
     "moe_expert_gemm_mxfp4": (I32, [P, P, I64, P, P, I64, I64, I32, P, P, P, I32, P]),
+    "moe_expert_layer_workspace_size": (SZ, [I64, I64, I32, I32, I64]),
+    "moe_expert_layer": (I32, [P, I64, I64, P, P, I32, I32, I64, I32, P, P, P, P, P, I32, P, SZ,
+                               P]),
     "moe_device_errors": (I32, [P]),
     "moe_selftest_wait_timeout": (I32, [I64, P]),
     "moe_selftest_convert": (I32, [ctypes.c_uint32, I64, P, P, P]),

@@ -77,7 +77,8 @@ typedef enum {
 typedef enum {
     MOE_BF16 = 0,    /* bfloat16, 2 bytes                                 */
     MOE_F32 = 1,     /* IEEE binary32, 4 bytes                            */
-    MOE_FP8_E4M3 = 2 /* OCP E4M3, 1 byte (dispatch only: a byte copy)     */
+    MOE_FP8_E4M3 = 2, /* OCP E4M3, 1 byte (dispatch only: a byte copy)    */
+    MOE_MXFP4 = 3     /* OCP MX, E2M1 codes and E8M0 scales (see below)   */
 } moe_dtype;
 
 /* Library ABI version (this header: 2). */
@@ -540,6 +541,35 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
                           const uint8_t *w_codes, const uint8_t *w_scales, int64_t N, int64_t D,
                           int E, const int32_t *cnt, const int64_t *off, void *y, int y_dtype,
                           moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * A whole routed layer for a few tokens, in two launches:
+ *   out[s] = sum over k with topk_idx[s,k] in [0, E) of topk_w[s,k] * w_down[e] h
+ *   h      = silu(w_up[e, :F] x[s]) * (w_up[e, F:] x[s]),   e = topk_idx[s,k]
+ * Sums and h are f32 (h enters the second product as two bf16 parts, or one f16
+ * part with MXFP4 weights; three and two parts for f32 outputs); out is rounded
+ * once.  The sum over k is in increasing k.  Ids outside [0, E) give nothing; a
+ * token without a valid id gives zeros.  Results are reproducible.
+ *
+ * x         bf16 [S, H]; topk_idx int32 [S, K]; topk_w f32 [S, K]
+ * w_dtype   MOE_BF16: w_up [E, 2 F, H], w_down [E, H, F] (gates before ups);
+ *           MOE_MXFP4: their codes, with up_scales and down_scales as
+ *           moe_quant_mxfp4 writes them (ignored for MOE_BF16); scales past a
+ *           row's end must not be 255
+ * out       [S, H] of out_dtype (MOE_BF16 or MOE_F32)
+ * workspace moe_expert_layer_workspace_size(S, H, K, E, F) bytes, 256-byte
+ *           aligned, dead after the call (0 bytes for sizes out of range)
+ * S * K <= 1024 (larger batches: the plan, the dispatch and the experts' products
+ * above), K <= 32, E <= 1024, H, F <= 16384.  S = 0 enqueues nothing.
+ * Alignment: all row pointers 16-byte aligned; H and F multiples of 8 (bf16) or
+ * 32 (MXFP4).
+ * ---------------------------------------------------------------------- */
+size_t moe_expert_layer_workspace_size(int64_t S, int64_t H, int K, int E, int64_t F);
+int moe_expert_layer(const void *x, int64_t S, int64_t H, const int32_t *topk_idx,
+                     const float *topk_w, int K, int E, int64_t F, int w_dtype, const void *w_up,
+                     const uint8_t *up_scales, const void *w_down, const uint8_t *down_scales,
+                     void *out, int out_dtype, void *workspace, size_t workspace_bytes,
+                     moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * Global L2 norm over many gradients, and clipping to a limit:

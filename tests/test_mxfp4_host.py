@@ -103,3 +103,77 @@ def test_binding_refuses():
         moe.moe_swiglu_quant_mxfp4(torch.zeros(4, 33))
     with pytest.raises(ValueError):   # tensors of the host are refused before the call
         moe.moe_quant_mxfp4(x)
+
+
+def test_product_validation(L):
+    f = lambda **k: L.moe_expert_gemm_mxfp4(
+        k.get("x", FAKE), k.get("xs", FAKE), k.get("rows", 8), k.get("w", FAKE), k.get("ws", FAKE),
+        k.get("N", 64), k.get("D", 64), k.get("E", 4), k.get("cnt", FAKE), k.get("off", FAKE), k.get("y", FAKE),
+        k.get("dt", 0), None)
+    for bad in (dict(dt=2), dict(dt=3), dict(rows=-1), dict(rows=1 << 31), dict(E=0), dict(E=1025), dict(N=0),
+                dict(N=1 << 24), dict(D=0), dict(D=32800), dict(x=None), dict(xs=None), dict(w=None), dict(ws=None),
+                dict(cnt=None), dict(off=None), dict(y=None), dict(rows=1 << 28, E=1024, N=4096)):
+        assert f(**bad) == EINVAL, bad
+    for bad in (dict(rows=6), dict(N=12), dict(D=48), dict(x=MIS8), dict(xs=MIS8), dict(w=MIS8), dict(ws=MIS8),
+                dict(y=MIS8)):
+        assert f(**bad) == EALIGN, bad
+    assert f(rows=0) == OK
+
+
+def test_layer_validation(L):
+    def f(**k):
+        a = dict(x=FAKE, S=2, H=64, idx=FAKE, w=FAKE, K=2, E=8, F=32, dt=0, up=FAKE, us=FAKE, down=FAKE, ds=FAKE,
+                 out=FAKE, odt=0, ws=FAKE, bytes=1 << 30)
+        a.update(k)
+        return L.moe_expert_layer(a["x"], a["S"], a["H"], a["idx"], a["w"], a["K"], a["E"], a["F"], a["dt"], a["up"],
+                                  a["us"], a["down"], a["ds"], a["out"], a["odt"], a["ws"], a["bytes"], None)
+    for bad in (dict(dt=1), dict(dt=2), dict(dt=4), dict(odt=2), dict(odt=3), dict(S=-1), dict(S=513), dict(H=0),
+                dict(H=16392), dict(K=0), dict(K=33), dict(E=0), dict(E=1025), dict(F=0), dict(F=16392), dict(x=None),
+                dict(idx=None), dict(w=None), dict(up=None), dict(down=None), dict(out=None), dict(ws=None),
+                dict(bytes=64), dict(dt=3, us=None), dict(dt=3, ds=None)):
+        assert f(**bad) == EINVAL, bad
+    for bad in (dict(H=60), dict(F=28), dict(dt=3, H=48), dict(dt=3, F=40), dict(x=MIS8), dict(up=MIS8),
+                dict(down=MIS8), dict(out=MIS8), dict(ws=MIS8)):
+        assert f(**bad) == EALIGN, bad
+    assert f(S=0) == OK
+    need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32)
+    assert need == 1024 + 512 + 256
+    assert f(bytes=need - 1) == EINVAL
+    for out_of_range in ((-1, 64, 2, 8, 32), (2, 0, 2, 8, 32), (1024, 64, 2, 8, 32), (2, 64, 2, 0, 32)):
+        assert L.moe_expert_layer_workspace_size(*out_of_range) == 0
+
+
+def test_layer_binding_refuses():
+    import combine_moe_plan_02_gb300 as moe
+    bf = torch.bfloat16
+    x, idx, w = torch.zeros(2, 64, dtype=bf), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+    up, down = torch.zeros(4, 64, 64, dtype=bf), torch.zeros(4, 64, 32, dtype=bf)
+    q = moe.MxFp4(torch.zeros(4, 64, 32, dtype=torch.uint8), torch.zeros(4, 1, 64, 4, dtype=torch.uint8))
+    for args, error in (((x.float(), idx, w, up, down), TypeError), ((x, idx.long(), w, up, down), TypeError),
+                        ((x, idx, w.double(), up, down), TypeError), ((x, idx, w[:, :1], up, down), TypeError),
+                        ((x, idx[:1], w[:1], up, down), TypeError), ((x, idx, w, up.float(), down), TypeError),
+                        ((x, idx, w, q, down), TypeError), ((x, idx, w, up, q), TypeError),
+                        ((x, idx, w, up[:, :63], down), ValueError), ((x, idx, w, up, down[:3]), ValueError),
+                        ((x, idx, w, up[0], down), ValueError), ((x[:, :32], idx, w, up, down), ValueError)):
+        with pytest.raises(error):
+            moe.moe_expert_layer(*args)
+    with pytest.raises(ValueError):
+        moe.moe_expert_layer(x, idx, w, up, down, out=torch.zeros(2, 32, dtype=bf))
+
+
+def test_product_binding_refuses():
+    import combine_moe_plan_02_gb300 as moe
+    rows = moe.MxFp4(torch.zeros(8, 32, dtype=torch.uint8), torch.zeros(1, 8, 4, dtype=torch.uint8))
+    w = moe.MxFp4(torch.zeros(4, 64, 32, dtype=torch.uint8), torch.zeros(4, 1, 64, 4, dtype=torch.uint8))
+    none = torch.zeros(0)
+    plan = moe.Plan(torch.zeros(4, dtype=torch.int32), torch.zeros(5, dtype=torch.int64), none, none, none)
+    for args, error in (((w, w, plan), ValueError), ((rows, rows, plan), ValueError),
+                        ((rows, w, plan._replace(cnt=plan.cnt.long())), TypeError),
+                        ((rows, w, plan._replace(cnt=plan.cnt[:3])), ValueError),
+                        ((rows, w._replace(codes=w.codes[:, :, :16].contiguous()), plan), ValueError)):
+        with pytest.raises(error):
+            moe.moe_expert_gemm_mxfp4(*args)
+    with pytest.raises(TypeError):
+        moe.moe_expert_gemm_mxfp4(rows, w, plan, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        moe.moe_expert_gemm_mxfp4(rows, w, plan, out=torch.zeros(8, 32))
