@@ -726,8 +726,10 @@ def moe_expert_gemm_mxfp4(x: MxFp4, w: MxFp4, plan: Union[Plan, CapacityPlan], *
     return out
 
 
-def moe_expert_layer_workspace_size(S: int, H: int, K: int, E: int, F: int) -> int:
-    return int(lib().moe_expert_layer_workspace_size(S, H, K, E, F))
+def moe_expert_layer_workspace_size(S: int, H: int, K: int, E: int, F: int,
+                                    mxfp4: bool = False) -> int:
+    return int(lib().moe_expert_layer_workspace_size(S, H, K, E, F,
+                                                     MOE_MXFP4 if mxfp4 else MOE_BF16))
 
 
 def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tensor,
@@ -760,11 +762,12 @@ def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
     E, F, K = shape[0], shape[1] // 2, topk_idx.shape[1]
     out = _expert_out(out, (S, H), out_dtype, x.device, stream)
     L = lib()
-    nws = int(L.moe_expert_layer_workspace_size(S, H, K, E, F))
+    kind = MOE_MXFP4 if mx else MOE_BF16
+    nws = int(L.moe_expert_layer_workspace_size(S, H, K, E, F, kind))
     ws = _workspace(nws, x.device, workspace, stream)
     up, down = (w if mx else (w, None) for w in (w_up, w_down))
     _abi.check("moe_expert_layer", L.moe_expert_layer(
-        _ptr(x), S, H, _ptr(topk_idx), _ptr(topk_w), K, E, F, MOE_MXFP4 if mx else MOE_BF16,
+        _ptr(x), S, H, _ptr(topk_idx), _ptr(topk_w), K, E, F, kind,
         _ptr(up[0]), _ptr(up[1]), _ptr(down[0]), _ptr(down[1]), _ptr(out), _dt(out), _ptr(ws), nws,
         _stream(stream, x)))
     return out

@@ -54,7 +54,7 @@ SIGNATURES = {
     "moe_swiglu_quant_mxfp4": (I32, [P, I32, I64, I64, P, P, P]),
     "moe_dequant_mxfp4": (I32, [P, P, I64, I64, I64, P, I32, P]),
     "moe_expert_gemm_mxfp4": (I32, [P, P, I64, P, P, I64, I64, I32, P, P, P, I32, P]),
-    "moe_expert_layer_workspace_size": (SZ, [I64, I64, I32, I32, I64]),
+    "moe_expert_layer_workspace_size": (SZ, [I64, I64, I32, I32, I64, I32]),
     "moe_expert_layer": (I32, [P, I64, I64, P, P, I32, I32, I64, I32, P, P, P, P, P, I32, P, SZ,
                                P]),
     "moe_device_errors": (I32, [P]),

@@ -87,6 +87,7 @@ cudaError_t read_backward_errors(uint32_t *flags);
 cudaError_t read_expert_errors(uint32_t *flags);
 cudaError_t read_mxfp4_errors(uint32_t *flags);
 cudaError_t read_mxgemm_errors(uint32_t *flags);
+cudaError_t read_layer_errors(uint32_t *flags);
 
 // moe_dispatch's body; early_src: the source rows were complete before the
 // previous kernel of the stream started waiting (see CopyArgs::early_src).

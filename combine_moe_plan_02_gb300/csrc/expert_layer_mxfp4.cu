@@ -1,0 +1,706 @@
+// A whole routed layer for a few tokens on MXFP4 weights.
+//
+//   out[s] = sum_k topk_w[s,k] * w_down[e] h,   e = topk_idx[s,k]
+//   h      = silu(w_gate[e] x[s]) * (w_up[e] x[s])
+//
+// The weights bound the call, and the block-scaled matrix instruction
+// (kind::mxf4) takes them as they are, with no instruction spent on a weight;
+// decoding them in registers for mma.sync takes 2.7 instructions a weight and ran at
+// 2.3 TB/s.  The other operand has to be E2M1 too, so x and h are written as sums of
+// eight MXFP4 rows: of a block of 32 with largest magnitude a, 2^e <= a < 2^(e + 1),
+// the first row is the block rounded to multiples of 2^(e - 1) and less (values up
+// to 4 units, steps of at most one), the next what that left (at most half a unit) in units of 2^(e - 4),
+// and so on, each three bits further.  The eighth leaves at most 2^-23 of a, less than f32 sums do.
+// Each row is a column of the product, and the columns' sums are added in f32.
+//
+// Three launches, each of which begins while the one before ends:
+//   split  x of every entry to eight rows, ordered by expert
+//   up     gates and ups of 64 outputs for up to 16 entries of an expert (128 columns),
+//          the activation, and h to eight rows
+//   down   128 outputs for up to 16 entries; the CTA that brings the last expert's
+//          share of them sums over k
+// Up and down are one kernel: a CTA per SM walks tiles of 128 weight rows.  One warp
+// copies weights with TMA, one the rows, into a ring of six stages of 256 elements, a third
+// issues the products, four more read the sums.  The copies of weights begin
+// before the launch waits for the one before it: nothing there writes weights.
+// csrc/expert_gemm_mxfp4.cu explains the scales' way to tensor memory and the order of
+// rows that follows from it (row 4 q + j in lane, or column, 32 j + q).
+
+#include "few.cuh"
+#include "pair.cuh"
+
+#include <cuda_fp16.h>
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kParts = 8;            // rows that stand for one
+constexpr int kRows = 16;            // entries of a tile
+constexpr int kCols = kRows * kParts;
+constexpr int kTile = 128;           // weight rows of a tile
+constexpr int kK = 256;              // elements of a stage
+constexpr int kCodes = kTile * kK / 2;
+constexpr int kScales = kTile * 8;
+constexpr int kStageBytes = 2 * (kCodes + kScales);
+constexpr int kStages = 6;
+constexpr int kScaleAt = 2 * kCols;  // first TMEM column of the scales
+constexpr int kTmemCols = 512;
+constexpr int kBoxBytes = kRows * kTile * 4;
+
+__device__ uint32_t g_layer_error;  // kErrExpertTimeout
+
+// --- x and h as eight rows ------------------------------------------------------
+
+// Eight neighbouring values, four lanes a block of 32: the codes of row p (one
+// word) and the block's scale byte.  `byte` is that of row 0, 255 where the block
+// has an infinity or a NaN; rows whose scale would be below 2^-127 are zero.
+struct Split {
+    float v[8];
+    int byte;
+
+    __device__ __forceinline__ void begin()
+    {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = (int)(top >> 23);
+        byte = e == 255 ? 255 : e - 1;  // -1 for zeros and what is below 2^-126
+    }
+    __device__ __forceinline__ int scale(int p) const
+    {
+        return byte == 255 ? (p ? 0 : 255) : max(byte - 3 * p, 0);
+    }
+    __device__ __forceinline__ uint32_t next(int p)
+    {
+        if (byte == 255) return p ? 0 : 0x22222222u;  // ones, times NaN
+        if (byte - 3 * p < 0) return 0;
+        const float inv = __uint_as_float((uint32_t)(254 - (byte - 3 * p)) << 23);
+        const float unit = byte - 3 * p ? __uint_as_float((uint32_t)(byte - 3 * p) << 23)
+                                        : __uint_as_float(0x00400000u);
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t code, back;
+            asm("{\n\t.reg .b8 c;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 c, %3, %2;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, c;\n\t"
+                "mov.b32 %0, {c, 0, 0, 0};\n\t}"
+                : "=r"(code), "=r"(back)
+                : "f"(v[2 * i] * inv), "f"(v[2 * i + 1] * inv));
+            word |= (code & 255u) << (8 * i);
+            const __half2 h = *reinterpret_cast<const __half2 *>(&back);
+            // exact: what is left is a multiple of the value's last bit
+            v[2 * i] = fmaf(-unit, __low2float(h), v[2 * i]);
+            v[2 * i + 1] = fmaf(-unit, __high2float(h), v[2 * i + 1]);
+        }
+        return word;
+    }
+};
+
+struct SplitArgs {
+    const uint8_t *x;
+    const int32_t *idx;
+    uint8_t *codes;      // [8 n, H / 2]
+    uint32_t *scales;    // [ceil(H / 128), 8 n]
+    uint32_t *arrived;   // cleared for the third launch
+    int S, K, E, H, columns;
+};
+
+// A warp takes 256 elements of a token and stores them for its K entries.
+__global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
+{
+    extern __shared__ int16_t lists[];
+    const int n = a.S * a.K;
+    Routing rt(lists, n, a.E);
+    const int tid = threadIdx.x, lane = tid & 31;
+    griddep_wait();
+    griddep_launch_dependents();
+    for (int i = blockIdx.x * kThreads + tid; i < a.columns; i += gridDim.x * kThreads)
+        a.arrived[i] = 0;
+    route<kThreads>(a.idx, n, a.E, kRows, rt);
+    const int chunks = (a.H + 255) / 256, words = (a.H + 127) / 128;
+    for (int u = blockIdx.x * (kThreads / 32) + (tid >> 5); u < a.S * chunks;
+         u += gridDim.x * (kThreads / 32)) {
+        const int s = u / chunks, c = u - s * chunks, at = c * 256 + lane * 8;
+        const bool in = at < a.H;
+        Split sp;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in) v = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)s * a.H + at) * 2));
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sp.v[2 * i] = __uint_as_float(q[i] << 16);
+            sp.v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+        }
+        sp.begin();
+        for (int p = 0; p < kParts; ++p) {
+            const uint32_t code = sp.next(p);
+            uint32_t word = (uint32_t)sp.scale(p);  // of four blocks, in every 16th lane
+            word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
+            word = (word & 0xffffu) | __shfl_down_sync(0xffffffffu, word, 8) << 16;
+            const int w = 2 * c + (lane >> 4);
+            for (int k = 0; k < a.K; ++k) {
+                const int place = rt.place[s * a.K + k];
+                if (place < 0) continue;
+                const int64_t row = (int64_t)place * kParts + p;
+                if (in) *reinterpret_cast<uint32_t *>(a.codes + row * (a.H / 2) + at / 2) = code;
+                if ((lane & 15) == 0 && w < words)
+                    a.scales[(int64_t)w * n * kParts + row] = word;
+            }
+        }
+    }
+}
+
+// --- the products -----------------------------------------------------------------
+
+struct LayerArgs {
+    const int32_t *idx;
+    const float *topk_w;
+    uint8_t *h_codes;     // [8 n, F / 2]
+    uint8_t *h_scales;    // [ceil(F / 128), 8 n, 4]
+    float *y;             // [n, H]
+    uint32_t *arrived;    // [ceil(H / 128)]
+    uint8_t *out;
+    int S, K, E, H, F;
+    int f32;
+};
+
+// Codes and scales of the weights and of the rows (all four quarters, or 8, 16, 24
+// rows of one).
+struct LayerMaps {
+    CUtensorMap a, sa, b, sb, part[3];
+};
+
+__device__ __forceinline__ void copy_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y, int z)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y, int z, int w)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y, int z, int w, int v)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t scale_a, uint32_t scale_b, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t d, uint64_t src)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+
+// Shared-memory descriptors: codes in rows of 128 bytes under the 128-byte swizzle,
+// scales in rows of 16 bytes.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool codes)
+{
+    return ((uint64_t)(addr & 0x3ffff) >> 4) | (1ull << 16) |
+           ((uint64_t)((codes ? 1024 : 128) >> 4) << 32) | (1ull << 46) |
+           ((codes ? 2ull : 0ull) << 61);
+}
+
+// E2M1 operands, E8M0 scales; `half`: which two of a word's four scales.
+__device__ __forceinline__ uint32_t instr_desc(int half)
+{
+    return ((uint32_t)(2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kCols >> 3) << 17) |
+           (1u << 23) | ((uint32_t)(kTile >> 4) << 24) | ((uint32_t)(2 * half) << 29);
+}
+
+struct Tile {
+    int e;        // expert
+    int m;        // tile of its weights
+    int row;      // first packed row
+    int rows;     // of them, 1 .. 16
+};
+
+// Tiles are numbered by part, then by the weights' tile, so that parts of one expert
+// read the same weights one after another; asked for in order.
+struct Walk {
+    const Routing &rt;
+    int tiles_m, at = 0;
+    __device__ Walk(const Routing &r, int m) : rt(r), tiles_m(m) {}
+    __device__ __forceinline__ Tile operator()(int t)
+    {
+        while (t >= rt.parts[at + 1] * tiles_m) ++at;
+        const int parts = rt.parts[at + 1] - rt.parts[at];
+        const int local = t - rt.parts[at] * tiles_m;
+        Tile r;
+        r.e = rt.hit[at];
+        r.m = local / parts;
+        r.row = rt.first[at] + (local - r.m * parts) * kRows;
+        r.rows = min(kRows, rt.first[at + 1] - r.row);
+        return r;
+    }
+};
+
+struct Shared {
+    uint64_t full[kStages], empty[kStages];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    volatile int stop;
+    int last;
+};
+
+template <bool UP>
+__global__ void __launch_bounds__(kThreads, 1)
+layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    float *box = reinterpret_cast<float *>(ring + kStages * kStageBytes);  // [16][64 or 128]
+    const int n = a.S * a.K;
+    Routing rt(box + kBoxBytes / 4, n, a.E);
+    __shared__ Shared sh;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&sh.full[i], 2);   // both operands
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    // topk_idx and the weights were complete when the first launch began
+    route<kThreads>(a.idx, n, a.E, kRows, rt);  // begins and ends with a barrier
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int reduction = UP ? a.H : a.F, outputs = UP ? a.F : a.H;
+    const int per_tile = UP ? kTile / 2 : kTile;
+    const int tiles_m = (outputs + per_tile - 1) / per_tile;
+    const int tiles = rt.parts[rt.hits] * tiles_m;
+    const int blocks = (reduction + kK - 1) / kK;
+    Walk walk(rt, tiles_m);
+
+    if (warp == 0 || warp == 2) {
+        const bool weights = warp == 0;
+        if (!weights) griddep_wait();  // the rows
+        if (elect_one()) {
+            Ring r(kStages);
+            int64_t j = 0;  // blocks copied
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile c = walk(t);
+                const int eights = (c.rows * 2 + 7) / 8;  // rows of a quarter, in eights
+                for (int b = 0; b < blocks; ++b, ++j) {
+                    if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *stage = ring + r.at * kStageBytes;
+                    uint64_t *bar = &sh.full[r.at];
+                    if (weights) {
+                        mbar_arrive_expect_tx(bar, kCodes + kScales);
+                        const int m = c.m * per_tile;
+                        uint8_t *scales = stage + 2 * kCodes;
+                        if (UP) {
+                            // 64 gates and 64 ups: row 4 q + j of either in lane
+                            // 32 j + q, ups 16 lanes on
+                            copy_5d(stage, &maps.a, bar, b * 128, m / 4, 0, 0, c.e);
+                            copy_4d(scales, &maps.sa, bar, m, 0, 2 * b, c.e);
+                        } else {
+                            copy_4d(stage, &maps.a, bar, b * 128, m / 4, 0, c.e);
+                            copy_3d(scales, &maps.sa, bar, m, 2 * b, c.e);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(bar, eights * 4096 + kScales);
+                        uint8_t *codes = stage + kCodes;
+                        const int row = c.row * kParts;
+                        if (eights == 4) {
+                            copy_3d(codes, &maps.b, bar, b * 128, row / 4, 0);
+                        } else {
+                            for (int i = 0; i < 4; ++i)
+                                copy_3d(codes + i * 4096, &maps.part[eights - 1], bar, b * 128,
+                                        row / 4, i);
+                        }
+                        copy_2d(stage + 2 * kCodes + kScales, &maps.sb, bar, row, 2 * b);
+                    }
+                    r.next();
+                }
+            }
+            if (!ok) {
+                // leave no copy in flight
+                for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
+                    (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        Ring r(kStages), done(kStages);  // `done`: the block two before
+        int64_t j = 0;
+        int i = 0;  // tiles begun
+        bool ok = true;
+        const uint32_t idesc[2] = {instr_desc(0), instr_desc(1)};
+        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+            if (i >= 2 && !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + (i & 1) * kCols;
+            for (int b = 0; b < blocks; ++b, ++j) {
+                // the products that used these columns of scales are done
+                if (j >= 2) {
+                    if (!wait(&sh.empty[done.at], done.round, &sh.stop)) {
+                        ok = false;
+                        break;
+                    }
+                    done.next();
+                }
+                if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t stage = smem_u32(ring) + r.at * kStageBytes;
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t sa = tmem + kScaleAt + (uint32_t)(j & 1) * 16, sb = sa + 8;
+                    const uint64_t from_a = desc_of(stage + 2 * kCodes, false);
+                    const uint64_t from_b = desc_of(stage + 2 * kCodes + kScales, false);
+                    const int steps = min((reduction - b * kK + 63) / 64, 4);  // 64 elements each
+                    for (int h = 0; 2 * h < steps; ++h) {
+                        copy_scales(sa + 4 * h, from_a + 32 * h);
+                        copy_scales(sb + 4 * h, from_b + 32 * h);
+                    }
+                    const uint64_t da = desc_of(stage, true), db = desc_of(stage + kCodes, true);
+                    for (int s = 0; s < steps; ++s)
+                        mma_mxf4(acc, da + 2 * s, db + 2 * s, idesc[s & 1], sa + 4 * (s >> 1),
+                                 sb + 4 * (s >> 1), b > 0 || s > 0);
+                    commit(&sh.empty[r.at]);
+                }
+                __syncwarp();
+                r.next();
+            }
+            if (ok && elect_one()) commit(&sh.acc_full[i & 1]);
+            __syncwarp();
+        }
+        if (elect_one()) commit(&sh.drain);  // nothing is issued after this
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int q = warp & 3, me = tid - 128;  // this warp's quarter; of 128 threads
+        auto join = [&] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        // whether all four warps go on: one that gave up must not leave the others
+        // at their next meeting
+        auto agree = [&](bool ok) {
+            uint32_t all;
+            asm volatile("{\n\t.reg .pred p, q;\n\t"
+                         "setp.ne.u32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, 1, 128, p;\n\t"
+                         "selp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all)
+                         : "r"((uint32_t)ok)
+                         : "memory");
+            return all != 0;
+        };
+        griddep_wait();
+        griddep_launch_dependents();
+        if (!UP && tiles == 0) {
+            for (int64_t i = (int64_t)blockIdx.x * 128 + me; i < (int64_t)a.S * a.H;
+                 i += (int64_t)gridDim.x * 128) {
+                if (a.f32) reinterpret_cast<float *>(a.out)[i] = 0.0f;
+                else reinterpret_cast<uint16_t *>(a.out)[i] = 0;
+            }
+        }
+        int i = 0;
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x, ++i) {
+            const Tile c = walk(t);
+            const int buf = i & 1;
+            if (!agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop))) break;
+            tc_fence_after();
+            // column 32 j + x is row 4 x + j: entry x / 2, part 4 (x & 1) + j
+            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kCols;
+            float sum[kRows];
+#pragma unroll
+            for (int x = 0; x < kRows; ++x) sum[x] = 0.0f;
+#pragma unroll
+            for (int j = 3; j >= 0; --j) {  // the small parts first
+                uint32_t v[32];
+                tmem_load(acc + j * 32, v);
+                tmem_wait(v);
+#pragma unroll
+                for (int x = 0; x < kRows; ++x)
+                    sum[x] += __uint_as_float(v[2 * x]) + __uint_as_float(v[2 * x + 1]);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+            if constexpr (UP) {
+                // lane q of a quarter j: gate of output 4 q + j, lane 16 + q its up
+#pragma unroll
+                for (int x = 0; x < kRows; ++x) {
+                    const float up = __shfl_down_sync(0xffffffffu, sum[x], 16);
+                    if (lane < 16 && x < c.rows)
+                        box[x * 64 + 4 * lane + q] = sum[x] / (1.0f + expf(-sum[x])) * up;
+                }
+                join();
+                // 4 threads a block, two blocks an entry
+                const int x = me >> 3, b = me >> 2 & 1, l = me & 3;
+                const int f0 = c.m * 64 + b * 32;
+                Split sp;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    sp.v[k] = x < c.rows ? box[x * 64 + b * 32 + l * 8 + k] : 0.0f;
+                sp.begin();
+                if (x < c.rows && f0 < a.F) {
+                    const int64_t row = (int64_t)(c.row + x) * kParts;
+                    uint8_t *codes = a.h_codes + row * (a.F / 2) + f0 / 2 + l * 4;
+                    uint8_t *scales =
+                        a.h_scales + ((int64_t)(f0 / 128) * n * kParts + row) * 4 + f0 / 32 % 4;
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+                        *reinterpret_cast<uint32_t *>(codes + p * (a.F / 2)) = sp.next(p);
+                        if (l == (p & 3)) {
+                            scales[p * 4] = (uint8_t)sp.scale(p);
+                            // the end of the last word
+                            if (f0 + 32 == a.F)
+                                for (int k = 1; k <= 3 - f0 / 32 % 4; ++k) scales[p * 4 + k] = 0;
+                        }
+                    }
+                }
+                join();  // the box has been read
+            } else {
+#pragma unroll
+                for (int x = 0; x < kRows; ++x)
+                    if (x < c.rows) box[x * kTile + 4 * lane + q] = sum[x];
+                join();
+                const int o = c.m * kTile + me;
+                if (o < a.H)
+                    for (int x = 0; x < c.rows; ++x)
+                        a.y[(int64_t)rt.order[c.row + x] * a.H + o] = box[x * kTile + me];
+                join();
+                if (me == 0) {
+                    __threadfence();
+                    sh.last = atomicAdd(a.arrived + c.m, 1u) == (uint32_t)rt.parts[rt.hits] - 1;
+                    __threadfence();
+                }
+                join();
+                if (sh.last && o < a.H)
+                    few_combine(a.y, a.topk_w, a.idx, a.S, a.K, a.E, a.H, o, 0, 1, a.out, a.f32);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        (void)wait_slow(&sh.drain, 0, nullptr);  // the last matrix instruction
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols));
+    }
+    if (tid == 0 && sh.stop) atomicOr(&g_layer_error, kErrExpertTimeout);
+}
+
+// --- host ----------------------------------------------------------------------
+
+struct Shape {
+    int rank;
+    cuuint64_t dims[5], strides[4];   // strides of all but the innermost, in bytes
+    cuuint32_t box[5];
+};
+
+cudaError_t encode(CUtensorMap *map, const void *base, bool words, const Shape &s)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    const CUresult r = fn(
+        map, words ? CU_TENSOR_MAP_DATA_TYPE_UINT32 : CU_TENSOR_MAP_DATA_TYPE_UINT8, s.rank,
+        const_cast<void *>(base), s.dims, s.strides, s.box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+        words ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Rows of D elements as the other operand: `rows` of them, a multiple of 8.
+cudaError_t encode_rows(LayerMaps &m, const uint8_t *codes, const uint8_t *scales, int rows, int D)
+{
+    const cuuint64_t row = D / 2, R = rows;
+    Shape s = {3, {row, R / 4, 4}, {4 * row, row}, {128, 32, 4}};
+    cudaError_t e = encode(&m.b, codes, false, s);
+    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
+        s.box[1] = 8 * (i + 1);
+        s.box[2] = 1;
+        e = encode(&m.part[i], codes, false, s);
+    }
+    if (e != cudaSuccess) return e;
+    return encode(&m.sb, scales, true,
+                  {2, {R, (cuuint64_t)(D + 127) / 128}, {R * 4}, {kCols, 2}});
+}
+
+template <bool UP>
+int launch_layer(const LayerMaps &maps, const LayerArgs &a, int n, cudaStream_t stream)
+{
+    static KernelCache kc;
+    const size_t smem = 1024 + kStages * kStageBytes + kBoxBytes + Routing::bytes(n, a.E);
+    cudaError_t e = prepare_kernel(layer_kernel<UP>, smem, kThreads, kc, nullptr);
+    if (e == cudaSuccess) {
+        const int per_tile = UP ? kTile / 2 : kTile;
+        const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
+        // an expert's part for every 16 of its rows and what is left
+        const int64_t parts = n < a.E ? n : a.E + n / kRows;
+        const int64_t most = tiles_m * (parts < n ? parts : n), sms = sm_count();
+        e = launch_pdl(layer_kernel<UP>, dim3((unsigned)(most < sms ? most : sms)),
+                       dim3(kThreads), smem, stream, maps, a);
+    }
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    return check_launch();
+}
+
+// The workspace: x and h as eight rows, y, and the counters.
+struct Places {
+    int64_t x_codes, x_scales, h_codes, h_scales, y, arrived, bytes;
+    Places(int64_t n, int64_t H, int64_t F)
+    {
+        int64_t at = 0;
+        auto take = [&](int64_t size) {
+            const int64_t p = at;
+            at += round_up(size, 256);
+            return p;
+        };
+        x_codes = take(n * kParts * H / 2);
+        x_scales = take((H + 127) / 128 * n * kParts * 4);
+        h_codes = take(n * kParts * F / 2);
+        h_scales = take((F + 127) / 128 * n * kParts * 4);
+        y = take(n * H * 4);
+        arrived = take((H + kTile - 1) / kTile * 4);
+        bytes = at;
+    }
+};
+
+} // namespace
+
+size_t layer_mxfp4_workspace(int64_t n, int64_t H, int64_t F)
+{
+    return (size_t)Places(n, H, F).bytes;
+}
+
+int layer_mxfp4(const LayerCall &c, cudaStream_t stream)
+{
+    const int n = c.S * c.K;
+    const Places at(n, c.H, c.F);
+    uint8_t *ws = c.workspace;
+    LayerArgs a = {};
+    a.idx = c.idx;
+    a.topk_w = c.topk_w;
+    a.h_codes = ws + at.h_codes;
+    a.h_scales = ws + at.h_scales;
+    a.y = reinterpret_cast<float *>(ws + at.y);
+    a.arrived = reinterpret_cast<uint32_t *>(ws + at.arrived);
+    a.out = c.out;
+    a.S = c.S;
+    a.K = c.K;
+    a.E = c.E;
+    a.H = c.H;
+    a.F = c.F;
+    a.f32 = c.f32;
+    LayerMaps up = {}, down = {};
+    const cuuint64_t E = c.E, H = c.H, F = c.F;
+    const cuuint64_t up_row = H / 2, up_words = (H + 127) / 128;
+    const cuuint64_t down_row = F / 2, down_words = (F + 127) / 128;
+    // gates and ups as two runs of F rows
+    cudaError_t e = encode(&up.a, c.up, false,
+                           {5,
+                            {up_row, F / 4, 2, 4, E},
+                            {4 * up_row, F * up_row, up_row, 2 * F * up_row},
+                            {128, 16, 2, 4, 1}});
+    if (e == cudaSuccess)
+        e = encode(&up.sa, c.up_scales, true,
+                   {4, {F, 2, up_words, E}, {F * 4, 2 * F * 4, up_words * 2 * F * 4}, {64, 2, 2, 1}});
+    if (e == cudaSuccess)
+        e = encode_rows(up, ws + at.x_codes, ws + at.x_scales, n * kParts, c.H);
+    if (e == cudaSuccess)
+        e = encode(&down.a, c.down, false,
+                   {4, {down_row, H / 4, 4, E}, {4 * down_row, down_row, H * down_row}, {128, 32, 4, 1}});
+    if (e == cudaSuccess)
+        e = encode(&down.sa, c.down_scales, true,
+                   {3, {H, down_words, E}, {H * 4, down_words * H * 4}, {kTile, 2, 1}});
+    if (e == cudaSuccess)
+        e = encode_rows(down, a.h_codes, a.h_scales, n * kParts, c.F);
+    static KernelCache kc;
+    const size_t smem = Routing::bytes(n, c.E);
+    if (e == cudaSuccess) e = prepare_kernel(split_kernel, smem, kThreads, kc, nullptr);
+    if (e == cudaSuccess) {
+        SplitArgs s = {c.x, c.idx, ws + at.x_codes, reinterpret_cast<uint32_t *>(ws + at.x_scales),
+                       a.arrived, c.S, c.K, c.E, c.H, (c.H + kTile - 1) / kTile};
+        const int64_t units = (int64_t)c.S * ((c.H + 255) / 256), most = 2 * sm_count();
+        const int64_t grid = (units + kThreads / 32 - 1) / (kThreads / 32);
+        e = launch_pdl(split_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(kThreads),
+                       smem, stream, s);
+    }
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    int r = check_launch();
+    if (r == MOE_OK) r = launch_layer<true>(up, a, n, stream);
+    if (r == MOE_OK) r = launch_layer<false>(down, a, n, stream);
+    return r;
+}
+
+// Reads and clears this file's device error bits.
+cudaError_t read_layer_errors(uint32_t *flags)
+{
+    uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_layer_error, sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_layer_error, &zero, sizeof(uint32_t));
+    return e;
+}
+
+} // namespace moe

@@ -50,7 +50,7 @@ MOE_EXPORT int moe_last_cuda_error(void) { return moe::t_last_cuda_error; }
 MOE_EXPORT int moe_device_errors(uint32_t *flags)
 {
     if (!flags) return MOE_EINVAL;
-    uint32_t a = 0, b = 0, c = 0, d = 0, x = 0, m = 0, g = 0;
+    uint32_t a = 0, b = 0, c = 0, d = 0, x = 0, m = 0, g = 0, l = 0;
     cudaError_t e = moe::read_dispatch_errors(&a);
     if (e == cudaSuccess) e = moe::read_combine_errors(&b);
     if (e == cudaSuccess) e = moe::read_plan_dispatch_errors(&c);
@@ -58,10 +58,11 @@ MOE_EXPORT int moe_device_errors(uint32_t *flags)
     if (e == cudaSuccess) e = moe::read_expert_errors(&x);
     if (e == cudaSuccess) e = moe::read_mxfp4_errors(&m);
     if (e == cudaSuccess) e = moe::read_mxgemm_errors(&g);
+    if (e == cudaSuccess) e = moe::read_layer_errors(&l);
     if (e != cudaSuccess) {
         moe::set_cuda_error(e);
         return MOE_ECUDA;
     }
-    *flags = a | b | c | d | x | m | g;
+    *flags = a | b | c | d | x | m | g | l;
     return MOE_OK;
 }

@@ -543,12 +543,14 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
                           moe_stream_t stream);
 
 /* ------------------------------------------------------------------------
- * A whole routed layer for a few tokens, in two launches:
+ * A whole routed layer for a few tokens, in two launches (three with MXFP4
+ * weights):
  *   out[s] = sum over k with topk_idx[s,k] in [0, E) of topk_w[s,k] * w_down[e] h
  *   h      = silu(w_up[e, :F] x[s]) * (w_up[e, F:] x[s]),   e = topk_idx[s,k]
- * Sums and h are f32 (h enters the second product as two bf16 parts, or one f16
- * part with MXFP4 weights; three and two parts for f32 outputs); out is rounded
- * once.  The sum over k is in increasing k.  Ids outside [0, E) give nothing; a
+ * Sums and h are f32 and out is rounded once.  bf16 weights: h enters the second
+ * product as two bf16 parts, 16 bits of it, or three, all of it, for f32 outputs.
+ * MXFP4 weights: x and h enter the products with an error of at most 2^-23 of the
+ * largest of 32 neighbours; a token with an infinite x or h gives NaN.  The sum over k is in increasing k.  Ids outside [0, E) give nothing; a
  * token without a valid id gives zeros.  Results are reproducible.
  *
  * x         bf16 [S, H]; topk_idx int32 [S, K]; topk_w f32 [S, K]
@@ -557,14 +559,14 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
  *           moe_quant_mxfp4 writes them (ignored for MOE_BF16); scales past a
  *           row's end must not be 255
  * out       [S, H] of out_dtype (MOE_BF16 or MOE_F32)
- * workspace moe_expert_layer_workspace_size(S, H, K, E, F) bytes, 256-byte
+ * workspace moe_expert_layer_workspace_size(S, H, K, E, F, w_dtype) bytes, 256-byte
  *           aligned, dead after the call (0 bytes for sizes out of range)
  * S * K <= 1024 (larger batches: the plan, the dispatch and the experts' products
  * above), K <= 32, E <= 1024, H, F <= 16384.  S = 0 enqueues nothing.
  * Alignment: all row pointers 16-byte aligned; H and F multiples of 8 (bf16) or
  * 32 (MXFP4).
  * ---------------------------------------------------------------------- */
-size_t moe_expert_layer_workspace_size(int64_t S, int64_t H, int K, int E, int64_t F);
+size_t moe_expert_layer_workspace_size(int64_t S, int64_t H, int K, int E, int64_t F, int w_dtype);
 int moe_expert_layer(const void *x, int64_t S, int64_t H, const int32_t *topk_idx,
                      const float *topk_w, int K, int E, int64_t F, int w_dtype, const void *w_up,
                      const uint8_t *up_scales, const void *w_down, const uint8_t *down_scales,

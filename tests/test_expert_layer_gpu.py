@@ -3,9 +3,10 @@
 Bounds, all relative to the sums of the magnitudes that a value is made of:
 products are exact, sums f32 with the tensor core's truncation (2^-23 a step of 16
 products, at most K / 16 + 16 steps), so (K / 16 + 16) 2^-23 of each projection;
-silu adds 2^-20 relative and at most 1.1 of its input's error; h is cut to 16 bits
-(bf16 weights) or 11 (MXFP4) of which half a step is lost, 24 and 22 for f32 outputs; the
-output's rounding is 2^-8 (bf16) or 2^-24 of the value."""
+silu adds 2^-20 relative and at most 1.1 of its input's error.  With bf16 weights h
+is cut to 16 bits, of which half a step is lost (24 for f32 outputs); with MXFP4 weights x and
+h lose at most 2^-23 of the largest of 32 neighbours.  The output's rounding is 2^-8
+(bf16) or 2^-24 of the value."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -37,6 +38,7 @@ def plain(x, idx, w, up, down):
     E, F2, H = up.shape
     F = F2 // 2
     step = lambda n: (n / 16 + 16) * 2.0 ** -23  # noqa: E731
+    top = lambda v: v.abs().unflatten(-1, (-1, 32)).amax(-1).repeat_interleave(32, -1)  # noqa: E731
     out = torch.zeros(x.shape, dtype=F64, device="cuda")
     wide, fine = torch.zeros_like(out), torch.zeros_like(out)
     for e in idx.unique().tolist():
@@ -45,16 +47,16 @@ def plain(x, idx, w, up, down):
         s, k = (idx == e).nonzero(as_tuple=True)
         v, wu, wd = x[s].to(F64), f(up, e), f(down, e)
         p, off = v @ wu.T, step(H) * (v.abs() @ wu.abs().T)
+        if mx:
+            off = off + 2.0 ** -23 * (top(v) @ wu.abs().T)
         gate, lift = p[:, :F], p[:, F:]
         act = gate / (1 + torch.exp(-gate))
         h = act * lift
         off = (1.1 * off[:, :F] + 2.0 ** -20 * act.abs()) * (lift.abs() + off[:, F:]) + act.abs() * off[:, F:]
         c = w[s, k].to(F64)[:, None]
         out.index_add_(0, s, c * (h @ wd.T))
-        for total, bits in ((wide, 12 if mx else 17), (fine, 22 if mx else 23)):
-            part = off + (2.0 ** -bits + step(F)) * h.abs()
-            if mx:  # what lies 2^-39 below the largest of a slice is lost
-                part = part + 2.0 ** -38 * h.abs().amax(1, keepdim=True)
+        for total, bits in ((wide, 17), (fine, 24)):
+            part = off + step(F) * h.abs() + (2.0 ** -23 * top(h.abs() + off) if mx else 2.0 ** -bits * h.abs())
             total.index_add_(0, s, c.abs() * (part @ wd.abs().T) + 2.0 ** -22 * (c * (h @ wd.T)).abs())
     return out, wide, fine
 
@@ -186,7 +188,7 @@ def test_reproducible_graph_and_streams(mx):
             to.copy_(t)
         graph.replay()
         assert torch.equal(out, f)
-    ws = torch.empty(moe.moe_expert_layer_workspace_size(16, 1024, 4, 8, 256), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(moe.moe_expert_layer_workspace_size(16, 1024, 4, 8, 256, mx), dtype=torch.uint8, device="cuda")
     ws.fill_(0xff)   # needs no initialisation
     assert torch.equal(moe.moe_expert_layer(*sets[1][:3], *weights, workspace=ws), first[1])
     streams = [torch.cuda.Stream() for _ in range(3)]

@@ -133,13 +133,17 @@ def test_layer_validation(L):
                 dict(bytes=64), dict(dt=3, us=None), dict(dt=3, ds=None)):
         assert f(**bad) == EINVAL, bad
     for bad in (dict(H=60), dict(F=28), dict(dt=3, H=48), dict(dt=3, F=40), dict(x=MIS8), dict(up=MIS8),
-                dict(down=MIS8), dict(out=MIS8), dict(ws=MIS8)):
+                dict(down=MIS8), dict(out=MIS8), dict(ws=MIS8), dict(dt=3, us=MIS8), dict(dt=3, ds=MIS8)):
         assert f(**bad) == EALIGN, bad
     assert f(S=0) == OK
-    need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32)
+    need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32, 0)
     assert need == 1024 + 512 + 256
     assert f(bytes=need - 1) == EINVAL
-    for out_of_range in ((-1, 64, 2, 8, 32), (2, 0, 2, 8, 32), (1024, 64, 2, 8, 32), (2, 64, 2, 0, 32)):
+    need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32, 3)
+    assert need == 1024 + 256 + 512 + 256 + 1024 + 256
+    assert f(dt=3, bytes=need - 1) == EINVAL
+    for out_of_range in ((-1, 64, 2, 8, 32, 0), (2, 0, 2, 8, 32, 0), (1024, 64, 2, 8, 32, 3), (2, 64, 2, 0, 32, 0),
+                         (2, 64, 2, 8, 32, 1)):
         assert L.moe_expert_layer_workspace_size(*out_of_range) == 0
 
 
