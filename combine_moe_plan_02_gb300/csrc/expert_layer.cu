@@ -148,7 +148,8 @@ __global__ void __launch_bounds__(kThreads, 2) layer_kernel(LayerArgs a)
     const int staged_rows = a.rows * PARTS;
     uint8_t *mine = smem + warp * staged_rows * a.pitch;
     float *sums = reinterpret_cast<float *>(smem + kWarps * staged_rows * a.pitch);
-    Routing rt(sums + 2 * kWarps * kMaxRows * kTile, n, a.E);
+    float *weights = sums + 2 * kWarps * kMaxRows * kTile;  // of the entries
+    Routing rt(weights + n, n, a.E);
     __shared__ int s_last;
 
     const int K = UP ? a.H : a.F;                    // reduction
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) layer_kernel(LayerArgs a)
     }
     // The second launch lists and begins to read its weights while the first one
     // ends: what it reads until its wait was complete when that one began.
+    if (!UP) load_weights(a.topk_w, n, weights);
     route<kThreads>(a.idx, n, a.E, a.rows, rt);
     const int64_t items = (int64_t)rt.hits * tiles;
     const int begin = (int)(items * blockIdx.x / gridDim.x);
@@ -271,11 +273,16 @@ __global__ void __launch_bounds__(kThreads, 2) layer_kernel(LayerArgs a)
             uint4 b = make_uint4(0, 0, 0, 0);
             if (row < rows && part < PARTS)
                 b = *reinterpret_cast<const uint4 *>(b0 + (row * PARTS + part) * a.pitch);
+            // The instruction cuts a sum's low bits off: after 100 of them an f32
+            // output is off by 1e-6.  Two at a time, added in f32, 2e-7.
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
                 const uint4 u = w[d][2 * m], v = w[d][2 * m + 1];
-                mma(acc[m][j], u.x, v.x, u.y, v.y, b.x, b.y);
-                mma(acc[m][j], u.z, v.z, u.w, v.w, b.z, b.w);
+                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                mma(c, u.x, v.x, u.y, v.y, b.x, b.y);
+                mma(c, u.z, v.z, u.w, v.w, b.z, b.w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[m][j][i] += c[i];
             }
         }
     };
@@ -343,9 +350,19 @@ __global__ void __launch_bounds__(kThreads, 2) layer_kernel(LayerArgs a)
             __threadfence();
         }
         __syncthreads();
-        if (s_last && o < a.H)
-            few_combine(a.y, a.topk_w, a.idx, a.S, a.K, a.E, a.H, o, warp, kWarps, a.out,
-                        a.out_f32);
+        if (!s_last || o >= a.H) return;
+        // a token a warp where that is enough
+        const int each = a.S > kWarps ? kFewTokens : 1;
+        for (int s0 = warp * each; s0 < a.S; s0 += kWarps * each) {
+            int s[kFewTokens];
+#pragma unroll
+            for (int j = 0; j < kFewTokens; ++j) s[j] = min(s0 + j, a.S - 1);
+            if (each == 1)
+                few_combine<1>(a.y, weights, rt.place, a.K, a.H, o, s, 1, a.out, a.out_f32);
+            else
+                few_combine<kFewTokens>(a.y, weights, rt.place, a.K, a.H, o, s, a.S - s0, a.out,
+                                        a.out_f32);
+        }
     };
 
     while (now.item < end) {
@@ -384,7 +401,7 @@ template <bool UP, int PARTS, int NT> int launch_layer(LayerArgs a, cudaStream_t
     if (rows > most) rows = most;
     if (rows > a.S) rows = a.S;  // more only where a token has an expert twice
     a.rows = rows < 1 ? 1 : rows;
-    const size_t smem = (size_t)a.rows * row + 2 * kWarps * kMaxRows * kTile * 4 +
+    const size_t smem = (size_t)a.rows * row + 2 * kWarps * kMaxRows * kTile * 4 + n * 4 +
                         Routing::bytes(n, a.E);
     int per_sm = 0;
     cudaError_t e = prepare_kernel(kernel, smem, kThreads, kc, &per_sm);
@@ -453,7 +470,7 @@ MOE_EXPORT size_t moe_expert_layer_workspace_size(int64_t S, int64_t H, int K, i
                                                   int w_dtype)
 {
     if (!in_range(S, H, K, E, F)) return 0;
-    if (w_dtype == MOE_MXFP4) return layer_mxfp4_workspace(S * K, H, F);
+    if (w_dtype == MOE_MXFP4) return layer_mxfp4_workspace(S, K, E, H, F);
     return w_dtype == MOE_BF16 ? (size_t)Places(S * K, H, F).bytes : 0;
 }
 

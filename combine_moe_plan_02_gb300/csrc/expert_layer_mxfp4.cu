@@ -15,16 +15,21 @@
 //
 // Three launches, each of which begins while the one before ends:
 //   split  x of every entry to eight rows, ordered by expert
-//   up     gates and ups of 64 outputs for up to 16 entries of an expert (128 columns),
+//   up     gates and ups of 64 outputs for up to 8 entries of an expert (64 columns),
 //          the activation, and h to eight rows
-//   down   128 outputs for up to 16 entries; the CTA that brings the last expert's
-//          share of them sums over k
-// Up and down are one kernel: a CTA per SM walks tiles of 128 weight rows.  One warp
-// copies weights with TMA, one the rows, into a ring of six stages of 256 elements, a third
-// issues the products, four more read the sums.  The copies of weights begin
+//   down   128 outputs for up to 8 entries; a token's are summed over k as the last of
+//          its experts arrives
+// Up and down are one kernel: CTAs, two an SM, walk tiles of 128 weight rows.  One
+// warp copies weights with TMA, one the rows, into a ring of stages of 256 elements, a
+// third issues the products, four more read the sums.  The copies of weights begin
 // before the launch waits for the one before it: nothing there writes weights.
-// csrc/expert_gemm_mxfp4.cu explains the scales' way to tensor memory and the order of
-// rows that follows from it (row 4 q + j in lane, or column, 32 j + q).
+//
+// The instruction wants the scales of 128 rows and 128 elements as words in 32 lanes
+// x 4 columns of tensor memory, row 32 j + q in column j of lane q, and a copy from
+// shared memory puts 16 bytes into one lane.  The rows' scales are written in that
+// order here.  The weights' scales lie one word after another, so that their row
+// 4 q + j arrives in column j of lane q, and TMA lays row 4 q + j of the codes in row 32 j
+// + q of the stage to match (as in csrc/expert_gemm_mxfp4.cu).
 
 #include "few.cuh"
 #include "pair.cuh"
@@ -36,17 +41,19 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kParts = 8;            // rows that stand for one
-constexpr int kRows = 16;            // entries of a tile
+constexpr int kRows = 8;             // entries of a tile
 constexpr int kCols = kRows * kParts;
 constexpr int kTile = 128;           // weight rows of a tile
 constexpr int kK = 256;              // elements of a stage
-constexpr int kCodes = kTile * kK / 2;
-constexpr int kScales = kTile * 8;
-constexpr int kStageBytes = 2 * (kCodes + kScales);
-constexpr int kStages = 6;
+constexpr int kCodesA = kTile * kK / 2;
+constexpr int kCodesB = kCols * kK / 2;
+constexpr int kScales = 2 * 512;     // of 128 rows, or places for them
+constexpr int kStageBytes = kCodesA + kCodesB + 2 * kScales;
+constexpr int kMaxStages = 7;
 constexpr int kScaleAt = 2 * kCols;  // first TMEM column of the scales
-constexpr int kTmemCols = 512;
-constexpr int kBoxBytes = kRows * kTile * 4;
+constexpr int kTmemCols = 256;       // so that two CTAs fit an SM
+constexpr int kSmem = 115712;        // of shared memory, likewise
+constexpr int kBoxBytes = kRows * kTile / 2 * 4;  // h of a tile
 
 __device__ uint32_t g_layer_error;  // kErrExpertTimeout
 
@@ -100,13 +107,20 @@ struct Split {
     }
 };
 
+// Where the word of row p of an entry lies among the words of all parts.
+__device__ __forceinline__ int scale_place(int place, int p)
+{
+    const int part = place / kRows, slot = place % kRows;  // column 8 slot + p = 32 j + q
+    return part * 128 + (slot % 4 * kParts + p) * 4 + slot / 4;
+}
+
 struct SplitArgs {
     const uint8_t *x;
     const int32_t *idx;
-    uint8_t *codes;      // [8 n, H / 2]
-    uint32_t *scales;    // [ceil(H / 128), 8 n]
+    uint8_t *codes;      // [parts, 64, H / 2]
+    uint32_t *scales;    // [ceil(H / 128), parts, 32, 4]
     uint32_t *arrived;   // cleared for the third launch
-    int S, K, E, H, columns;
+    int S, K, E, H, parts, counters;
 };
 
 // A warp takes 256 elements of a token and stores them for its K entries.
@@ -118,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
     const int tid = threadIdx.x, lane = tid & 31;
     griddep_wait();
     griddep_launch_dependents();
-    for (int i = blockIdx.x * kThreads + tid; i < a.columns; i += gridDim.x * kThreads)
+    for (int i = blockIdx.x * kThreads + tid; i < a.counters; i += gridDim.x * kThreads)
         a.arrived[i] = 0;
     route<kThreads>(a.idx, n, a.E, kRows, rt);
     const int chunks = (a.H + 255) / 256, words = (a.H + 127) / 128;
@@ -131,24 +145,29 @@ __global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
         if (in) v = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)s * a.H + at) * 2));
         const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sp.v[2 * i] = __uint_as_float(q[i] << 16);
-            sp.v[2 * i + 1] = __uint_as_float(q[i] & 0xffff0000u);
+        for (int k = 0; k < 4; ++k) {
+            sp.v[2 * k] = __uint_as_float(q[k] << 16);
+            sp.v[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
         }
         sp.begin();
+        uint32_t code[kParts], word[kParts];
+#pragma unroll
         for (int p = 0; p < kParts; ++p) {
-            const uint32_t code = sp.next(p);
-            uint32_t word = (uint32_t)sp.scale(p);  // of four blocks, in every 16th lane
-            word |= __shfl_down_sync(0xffffffffu, word, 4) << 8;
-            word = (word & 0xffffu) | __shfl_down_sync(0xffffffffu, word, 8) << 16;
-            const int w = 2 * c + (lane >> 4);
-            for (int k = 0; k < a.K; ++k) {
-                const int place = rt.place[s * a.K + k];
-                if (place < 0) continue;
-                const int64_t row = (int64_t)place * kParts + p;
-                if (in) *reinterpret_cast<uint32_t *>(a.codes + row * (a.H / 2) + at / 2) = code;
-                if ((lane & 15) == 0 && w < words)
-                    a.scales[(int64_t)w * n * kParts + row] = word;
+            code[p] = sp.next(p);
+            uint32_t b = (uint32_t)sp.scale(p);  // of four blocks, in every 16th lane
+            b |= __shfl_down_sync(0xffffffffu, b, 4) << 8;
+            word[p] = (b & 0xffffu) | __shfl_down_sync(0xffffffffu, b, 8) << 16;
+        }
+        const int w = 2 * c + (lane >> 4);
+        uint32_t *scales = a.scales + (int64_t)w * a.parts * 128;
+        for (int k = 0; k < a.K; ++k) {
+            const int place = rt.place[s * a.K + k];
+            if (place < 0) continue;
+            uint8_t *codes = a.codes + (int64_t)place * kParts * (a.H / 2) + at / 2;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                if (in) *reinterpret_cast<uint32_t *>(codes + p * (a.H / 2)) = code[p];
+                if ((lane & 15) == 0 && w < words) scales[scale_place(place, p)] = word[p];
             }
         }
     }
@@ -159,19 +178,20 @@ __global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
 struct LayerArgs {
     const int32_t *idx;
     const float *topk_w;
-    uint8_t *h_codes;     // [8 n, F / 2]
-    uint8_t *h_scales;    // [ceil(F / 128), 8 n, 4]
+    uint8_t *h_codes;     // [parts, 64, F / 2]
+    uint8_t *h_scales;    // [ceil(F / 128), parts, 32, 4, 4]
     float *y;             // [n, H]
-    uint32_t *arrived;    // [ceil(H / 128)]
+    uint32_t *arrived;    // [ceil(H / 128), 4, S] experts whose share of these outputs is there
     uint8_t *out;
     int S, K, E, H, F;
+    int parts;            // that there is room for
+    int stages;
     int f32;
 };
 
-// Codes and scales of the weights and of the rows (all four quarters, or 8, 16, 24
-// rows of one).
+// Codes and scales of the weights and of the rows (of 4 entries, or 8).
 struct LayerMaps {
-    CUtensorMap a, sa, b, sb, part[3];
+    CUtensorMap a, sa, b[2], sb;
 };
 
 __device__ __forceinline__ void copy_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
@@ -244,17 +264,18 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool codes)
 }
 
 // E2M1 operands, E8M0 scales; `half`: which two of a word's four scales.
-__device__ __forceinline__ uint32_t instr_desc(int half)
+__device__ __forceinline__ uint32_t instr_desc(int n, int half)
 {
-    return ((uint32_t)(2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(kCols >> 3) << 17) |
+    return ((uint32_t)(2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
            (1u << 23) | ((uint32_t)(kTile >> 4) << 24) | ((uint32_t)(2 * half) << 29);
 }
 
 struct Tile {
     int e;        // expert
     int m;        // tile of its weights
+    int part;     // of its entries
     int row;      // first packed row
-    int rows;     // of them, 1 .. 16
+    int rows;     // of them, 1 .. 8
 };
 
 // Tiles are numbered by part, then by the weights' tile, so that parts of one expert
@@ -271,6 +292,7 @@ struct Walk {
         Tile r;
         r.e = rt.hit[at];
         r.m = local / parts;
+        r.part = rt.parts[at] + local - r.m * parts;
         r.row = rt.first[at] + (local - r.m * parts) * kRows;
         r.rows = min(kRows, rt.first[at + 1] - r.row);
         return r;
@@ -278,27 +300,29 @@ struct Walk {
 };
 
 struct Shared {
-    uint64_t full[kStages], empty[kStages];
+    uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     volatile int stop;
-    int last;
 };
 
 template <bool UP>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 2)
 layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
-    float *box = reinterpret_cast<float *>(ring + kStages * kStageBytes);  // [16][64 or 128]
+    const int stages = a.stages;
+    float *box = reinterpret_cast<float *>(ring + stages * kStageBytes);  // [8][64]
     const int n = a.S * a.K;
-    Routing rt(box + kBoxBytes / 4, n, a.E);
+    float *weights = box + kBoxBytes / 4;                       // [n]
+    int16_t *valid = reinterpret_cast<int16_t *>(weights + n);  // [S] experts of a token
+    Routing rt(valid + a.S, n, a.E);
     __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh.full[i], 2);   // both operands
             mbar_init(&sh.empty[i], 1);
         }
@@ -318,8 +342,17 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     tc_fence_before();
-    // topk_idx and the weights were complete when the first launch began
+    // topk_idx, topk_w and the experts' weights were complete when the first launch began
+    if (!UP) load_weights(a.topk_w, n, weights);
     route<kThreads>(a.idx, n, a.E, kRows, rt);  // begins and ends with a barrier
+    if (!UP) {
+        for (int s = tid; s < a.S; s += kThreads) {
+            int k = 0;
+            for (int i = s * a.K; i < (s + 1) * a.K; ++i) k += rt.place[i] >= 0;
+            valid[s] = (int16_t)k;
+        }
+        __syncthreads();
+    }
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int reduction = UP ? a.H : a.F, outputs = UP ? a.F : a.H;
@@ -333,23 +366,23 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
         const bool weights = warp == 0;
         if (!weights) griddep_wait();  // the rows
         if (elect_one()) {
-            Ring r(kStages);
+            Ring r(stages);
             int64_t j = 0;  // blocks copied
             bool ok = true;
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const Tile c = walk(t);
-                const int eights = (c.rows * 2 + 7) / 8;  // rows of a quarter, in eights
+                const bool all = c.rows > kRows / 2;
                 for (int b = 0; b < blocks; ++b, ++j) {
-                    if (j >= kStages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
+                    if (j >= stages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
                         ok = false;
                         break;
                     }
                     uint8_t *stage = ring + r.at * kStageBytes;
                     uint64_t *bar = &sh.full[r.at];
                     if (weights) {
-                        mbar_arrive_expect_tx(bar, kCodes + kScales);
+                        mbar_arrive_expect_tx(bar, kCodesA + kScales);
                         const int m = c.m * per_tile;
-                        uint8_t *scales = stage + 2 * kCodes;
+                        uint8_t *scales = stage + kCodesA + kCodesB;
                         if (UP) {
                             // 64 gates and 64 ups: row 4 q + j of either in lane
                             // 32 j + q, ups 16 lanes on
@@ -360,35 +393,29 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                             copy_3d(scales, &maps.sa, bar, m, 2 * b, c.e);
                         }
                     } else {
-                        mbar_arrive_expect_tx(bar, eights * 4096 + kScales);
-                        uint8_t *codes = stage + kCodes;
-                        const int row = c.row * kParts;
-                        if (eights == 4) {
-                            copy_3d(codes, &maps.b, bar, b * 128, row / 4, 0);
-                        } else {
-                            for (int i = 0; i < 4; ++i)
-                                copy_3d(codes + i * 4096, &maps.part[eights - 1], bar, b * 128,
-                                        row / 4, i);
-                        }
-                        copy_2d(stage + 2 * kCodes + kScales, &maps.sb, bar, row, 2 * b);
+                        mbar_arrive_expect_tx(bar, kCodesB / (all ? 1 : 2) + kScales);
+                        copy_2d(stage + kCodesA, &maps.b[all], bar, b * 128, c.part * kCols);
+                        copy_2d(stage + kCodesA + kCodesB + kScales, &maps.sb, bar, c.part * 128,
+                                2 * b);
                     }
                     r.next();
                 }
             }
             if (!ok) {
                 // leave no copy in flight
-                for (int64_t i = j > kStages ? j - kStages : 0; i < j; ++i)
-                    (void)wait_slow(&sh.full[i % kStages], (uint32_t)(i / kStages) & 1, nullptr);
+                for (int64_t i = j > stages ? j - stages : 0; i < j; ++i)
+                    (void)wait_slow(&sh.full[i % stages], (uint32_t)(i / stages) & 1, nullptr);
             }
         }
         __syncwarp();
     } else if (warp == 1) {
-        Ring r(kStages), done(kStages);  // `done`: the block two before
+        Ring r(stages), done(stages);  // `done`: the block two before
         int64_t j = 0;
         int i = 0;  // tiles begun
         bool ok = true;
-        const uint32_t idesc[2] = {instr_desc(0), instr_desc(1)};
         for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+            const int cols = walk(t).rows > kRows / 2 ? kCols : kCols / 2;
+            const uint32_t idesc[2] = {instr_desc(cols, 0), instr_desc(cols, 1)};
             if (i >= 2 && !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) break;
             tc_fence_after();
             const uint32_t acc = tmem + (i & 1) * kCols;
@@ -409,14 +436,14 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 tc_fence_after();
                 if (elect_one()) {
                     const uint32_t sa = tmem + kScaleAt + (uint32_t)(j & 1) * 16, sb = sa + 8;
-                    const uint64_t from_a = desc_of(stage + 2 * kCodes, false);
-                    const uint64_t from_b = desc_of(stage + 2 * kCodes + kScales, false);
+                    const uint64_t from_a = desc_of(stage + kCodesA + kCodesB, false);
+                    const uint64_t from_b = from_a + (kScales >> 4);
                     const int steps = min((reduction - b * kK + 63) / 64, 4);  // 64 elements each
                     for (int h = 0; 2 * h < steps; ++h) {
                         copy_scales(sa + 4 * h, from_a + 32 * h);
                         copy_scales(sb + 4 * h, from_b + 32 * h);
                     }
-                    const uint64_t da = desc_of(stage, true), db = desc_of(stage + kCodes, true);
+                    const uint64_t da = desc_of(stage, true), db = desc_of(stage + kCodesA, true);
                     for (int s = 0; s < steps; ++s)
                         mma_mxf4(acc, da + 2 * s, db + 2 * s, idesc[s & 1], sa + 4 * (s >> 1),
                                  sb + 4 * (s >> 1), b > 0 || s > 0);
@@ -448,11 +475,14 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
         };
         griddep_wait();
         griddep_launch_dependents();
-        if (!UP && tiles == 0) {
-            for (int64_t i = (int64_t)blockIdx.x * 128 + me; i < (int64_t)a.S * a.H;
-                 i += (int64_t)gridDim.x * 128) {
-                if (a.f32) reinterpret_cast<float *>(a.out)[i] = 0.0f;
-                else reinterpret_cast<uint16_t *>(a.out)[i] = 0;
+        if (!UP) {
+            // tokens without an expert
+            for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+                if (valid[s]) continue;
+                for (int i = me; i < a.H; i += 128) {
+                    if (a.f32) reinterpret_cast<float *>(a.out)[(int64_t)s * a.H + i] = 0.0f;
+                    else reinterpret_cast<uint16_t *>(a.out)[(int64_t)s * a.H + i] = 0;
+                }
             }
         }
         int i = 0;
@@ -461,19 +491,21 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
             const int buf = i & 1;
             if (!agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop))) break;
             tc_fence_after();
-            // column 32 j + x is row 4 x + j: entry x / 2, part 4 (x & 1) + j
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kCols;
             float sum[kRows];
 #pragma unroll
-            for (int x = 0; x < kRows; ++x) sum[x] = 0.0f;
-#pragma unroll
-            for (int j = 3; j >= 0; --j) {  // the small parts first
-                uint32_t v[32];
+            for (int j = 0; j < 2; ++j) {
+                if (j * 4 >= c.rows) break;
+                uint32_t v[32];  // column 8 x + p: row p of entry 4 j + x
                 tmem_load(acc + j * 32, v);
                 tmem_wait(v);
 #pragma unroll
-                for (int x = 0; x < kRows; ++x)
-                    sum[x] += __uint_as_float(v[2 * x]) + __uint_as_float(v[2 * x + 1]);
+                for (int x = 0; x < 4; ++x) {
+                    float f = __uint_as_float(v[8 * x + 7]);  // the small ones first
+#pragma unroll
+                    for (int p = 6; p >= 0; --p) f += __uint_as_float(v[8 * x + p]);
+                    sum[4 * j + x] = f;
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -488,48 +520,74 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 }
                 join();
                 // 4 threads a block, two blocks an entry
-                const int x = me >> 3, b = me >> 2 & 1, l = me & 3;
+                const int x = me >> 3 & 7, b = me >> 2 & 1, l = me & 3;
                 const int f0 = c.m * 64 + b * 32;
-                Split sp;
+                if (me < 64) {
+                    Split sp;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    sp.v[k] = x < c.rows ? box[x * 64 + b * 32 + l * 8 + k] : 0.0f;
-                sp.begin();
-                if (x < c.rows && f0 < a.F) {
-                    const int64_t row = (int64_t)(c.row + x) * kParts;
-                    uint8_t *codes = a.h_codes + row * (a.F / 2) + f0 / 2 + l * 4;
-                    uint8_t *scales =
-                        a.h_scales + ((int64_t)(f0 / 128) * n * kParts + row) * 4 + f0 / 32 % 4;
+                    for (int k = 0; k < 8; ++k)
+                        sp.v[k] = x < c.rows ? box[x * 64 + b * 32 + l * 8 + k] : 0.0f;
+                    sp.begin();
+                    if (x < c.rows && f0 < a.F) {
+                        const int place = c.part * kRows + x;
+                        uint8_t *codes = a.h_codes + (int64_t)place * kParts * (a.F / 2) +
+                                         f0 / 2 + l * 4;
+                        uint8_t *scales = a.h_scales + (int64_t)(f0 / 128) * a.parts * 512 +
+                                          f0 / 32 % 4;
 #pragma unroll
-                    for (int p = 0; p < kParts; ++p) {
-                        *reinterpret_cast<uint32_t *>(codes + p * (a.F / 2)) = sp.next(p);
-                        if (l == (p & 3)) {
-                            scales[p * 4] = (uint8_t)sp.scale(p);
-                            // the end of the last word
-                            if (f0 + 32 == a.F)
-                                for (int k = 1; k <= 3 - f0 / 32 % 4; ++k) scales[p * 4 + k] = 0;
+                        for (int p = 0; p < kParts; ++p) {
+                            *reinterpret_cast<uint32_t *>(codes + p * (a.F / 2)) = sp.next(p);
+                            if (l == (p & 3)) {
+                                uint8_t *to = scales + scale_place(place, p) * 4;
+                                to[0] = (uint8_t)sp.scale(p);
+                                // the end of the last word
+                                if (f0 + 32 == a.F)
+                                    for (int k = 1; k <= 3 - f0 / 32 % 4; ++k) to[k] = 0;
+                            }
                         }
                     }
                 }
                 join();  // the box has been read
             } else {
-#pragma unroll
-                for (int x = 0; x < kRows; ++x)
-                    if (x < c.rows) box[x * kTile + 4 * lane + q] = sum[x];
-                join();
-                const int o = c.m * kTile + me;
+                // Each warp stores its outputs (every fourth) and counts them for
+                // itself: the warps need not meet.  A token's outputs are summed by the
+                // warp that brings the last of its experts, which spreads the sums over
+                // the call: summed for all 32 tokens by the last expert's they took 55 us at
+                // its end.
+                const int o = c.m * kTile + 4 * lane + q;
                 if (o < a.H)
-                    for (int x = 0; x < c.rows; ++x)
-                        a.y[(int64_t)rt.order[c.row + x] * a.H + o] = box[x * kTile + me];
-                join();
-                if (me == 0) {
-                    __threadfence();
-                    sh.last = atomicAdd(a.arrived + c.m, 1u) == (uint32_t)rt.parts[rt.hits] - 1;
-                    __threadfence();
+#pragma unroll
+                    for (int x = 0; x < kRows; ++x)
+                        if (x < c.rows) a.y[(int64_t)rt.order[c.row + x] * a.H + o] = sum[x];
+                __syncwarp();
+                int token = 0;
+                bool last = false;
+                __threadfence();
+                if (lane < c.rows) {
+                    token = rt.order[c.row + lane] / a.K;
+                    last = atomicAdd(a.arrived + (c.m * 4 + q) * a.S + token, 1u) + 1 ==
+                           (uint32_t)valid[token];
                 }
-                join();
-                if (sh.last && o < a.H)
-                    few_combine(a.y, a.topk_w, a.idx, a.S, a.K, a.E, a.H, o, 0, 1, a.out, a.f32);
+                uint32_t ready = __ballot_sync(0xffffffffu, last);
+                if (ready) __threadfence();
+                while (ready) {
+                    int s[kFewTokens], count = 0, from = 0;
+#pragma unroll
+                    for (int j = 0; j < kFewTokens; ++j) {
+                        if (ready) {
+                            from = __ffs(ready) - 1;
+                            ready &= ready - 1;
+                            ++count;
+                        }
+                        s[j] = __shfl_sync(0xffffffffu, token, from);
+                    }
+                    if (o >= a.H) continue;
+                    if (count == 1)
+                        few_combine<1>(a.y, weights, rt.place, a.K, a.H, o, s, 1, a.out, a.f32);
+                    else
+                        few_combine<kFewTokens>(a.y, weights, rt.place, a.K, a.H, o, s, count,
+                                                a.out, a.f32);
+                }
             }
         }
     }
@@ -565,35 +623,33 @@ cudaError_t encode(CUtensorMap *map, const void *base, bool words, const Shape &
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows of D elements as the other operand: `rows` of them, a multiple of 8.
-cudaError_t encode_rows(LayerMaps &m, const uint8_t *codes, const uint8_t *scales, int rows, int D)
+// Parts of 64 rows of D elements as the other operand.
+cudaError_t encode_rows(LayerMaps &m, const uint8_t *codes, const uint8_t *scales, int parts, int D)
 {
-    const cuuint64_t row = D / 2, R = rows;
-    Shape s = {3, {row, R / 4, 4}, {4 * row, row}, {128, 32, 4}};
-    cudaError_t e = encode(&m.b, codes, false, s);
-    for (int i = 0; i < 3 && e == cudaSuccess; ++i) {
-        s.box[1] = 8 * (i + 1);
-        s.box[2] = 1;
-        e = encode(&m.part[i], codes, false, s);
-    }
+    const cuuint64_t row = D / 2, P = parts, words = (D + 127) / 128;
+    cudaError_t e = cudaSuccess;
+    for (cuuint32_t i = 0; i < 2 && e == cudaSuccess; ++i)
+        e = encode(&m.b[i], codes, false, {2, {row, P * kCols}, {row}, {128, kCols / 2 * (i + 1)}});
     if (e != cudaSuccess) return e;
-    return encode(&m.sb, scales, true,
-                  {2, {R, (cuuint64_t)(D + 127) / 128}, {R * 4}, {kCols, 2}});
+    return encode(&m.sb, scales, true, {2, {P * 128, words}, {P * 512}, {128, 2}});
 }
 
-template <bool UP>
-int launch_layer(const LayerMaps &maps, const LayerArgs &a, int n, cudaStream_t stream)
+template <bool UP> int launch_layer(const LayerMaps &maps, LayerArgs a, cudaStream_t stream)
 {
     static KernelCache kc;
-    const size_t smem = 1024 + kStages * kStageBytes + kBoxBytes + Routing::bytes(n, a.E);
+    const size_t rest = 1024 + kBoxBytes + a.S * a.K * 4 + a.S * 2 +
+                        Routing::bytes(a.S * a.K, a.E);
+    // Two CTAs of an SM have four stages each; where the lists leave less, one CTA has
+    // as many as fit.
+    a.stages = (int)((kSmem - rest) / kStageBytes);
+    if (a.stages < 4) a.stages = kMaxStages;
+    const size_t smem = rest + (size_t)a.stages * kStageBytes;
     cudaError_t e = prepare_kernel(layer_kernel<UP>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess) {
         const int per_tile = UP ? kTile / 2 : kTile;
         const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
-        // an expert's part for every 16 of its rows and what is left
-        const int64_t parts = n < a.E ? n : a.E + n / kRows;
-        const int64_t most = tiles_m * (parts < n ? parts : n), sms = sm_count();
-        e = launch_pdl(layer_kernel<UP>, dim3((unsigned)(most < sms ? most : sms)),
+        const int64_t most = tiles_m * a.parts, room = (int64_t)sm_count() * (a.stages < kMaxStages ? 2 : 1);
+        e = launch_pdl(layer_kernel<UP>, dim3((unsigned)(most < room ? most : room)),
                        dim3(kThreads), smem, stream, maps, a);
     }
     if (e != cudaSuccess) {
@@ -603,38 +659,42 @@ int launch_layer(const LayerMaps &maps, const LayerArgs &a, int n, cudaStream_t 
     return check_launch();
 }
 
+// Parts of n entries: one for every eight of an expert and one for what is left.
+int64_t most_parts(int64_t n, int64_t E) { return n < E + n / kRows ? n : E + n / kRows; }
+
 // The workspace: x and h as eight rows, y, and the counters.
 struct Places {
     int64_t x_codes, x_scales, h_codes, h_scales, y, arrived, bytes;
-    Places(int64_t n, int64_t H, int64_t F)
+    Places(int64_t S, int64_t K, int64_t E, int64_t H, int64_t F)
     {
+        const int64_t n = S * K, parts = most_parts(n, E);
         int64_t at = 0;
         auto take = [&](int64_t size) {
             const int64_t p = at;
             at += round_up(size, 256);
             return p;
         };
-        x_codes = take(n * kParts * H / 2);
-        x_scales = take((H + 127) / 128 * n * kParts * 4);
-        h_codes = take(n * kParts * F / 2);
-        h_scales = take((F + 127) / 128 * n * kParts * 4);
+        x_codes = take(parts * kCols * H / 2);
+        x_scales = take((H + 127) / 128 * parts * 512);
+        h_codes = take(parts * kCols * F / 2);
+        h_scales = take((F + 127) / 128 * parts * 512);
         y = take(n * H * 4);
-        arrived = take((H + kTile - 1) / kTile * 4);
+        arrived = take((H + kTile - 1) / kTile * 4 * S * 4);
         bytes = at;
     }
 };
 
 } // namespace
 
-size_t layer_mxfp4_workspace(int64_t n, int64_t H, int64_t F)
+size_t layer_mxfp4_workspace(int64_t S, int64_t K, int64_t E, int64_t H, int64_t F)
 {
-    return (size_t)Places(n, H, F).bytes;
+    return (size_t)Places(S, K, E, H, F).bytes;
 }
 
 int layer_mxfp4(const LayerCall &c, cudaStream_t stream)
 {
     const int n = c.S * c.K;
-    const Places at(n, c.H, c.F);
+    const Places at(c.S, c.K, c.E, c.H, c.F);
     uint8_t *ws = c.workspace;
     LayerArgs a = {};
     a.idx = c.idx;
@@ -649,6 +709,7 @@ int layer_mxfp4(const LayerCall &c, cudaStream_t stream)
     a.E = c.E;
     a.H = c.H;
     a.F = c.F;
+    a.parts = (int)most_parts(n, c.E);
     a.f32 = c.f32;
     LayerMaps up = {}, down = {};
     const cuuint64_t E = c.E, H = c.H, F = c.F;
@@ -664,7 +725,7 @@ int layer_mxfp4(const LayerCall &c, cudaStream_t stream)
         e = encode(&up.sa, c.up_scales, true,
                    {4, {F, 2, up_words, E}, {F * 4, 2 * F * 4, up_words * 2 * F * 4}, {64, 2, 2, 1}});
     if (e == cudaSuccess)
-        e = encode_rows(up, ws + at.x_codes, ws + at.x_scales, n * kParts, c.H);
+        e = encode_rows(up, ws + at.x_codes, ws + at.x_scales, a.parts, c.H);
     if (e == cudaSuccess)
         e = encode(&down.a, c.down, false,
                    {4, {down_row, H / 4, 4, E}, {4 * down_row, down_row, H * down_row}, {128, 32, 4, 1}});
@@ -672,13 +733,13 @@ int layer_mxfp4(const LayerCall &c, cudaStream_t stream)
         e = encode(&down.sa, c.down_scales, true,
                    {3, {H, down_words, E}, {H * 4, down_words * H * 4}, {kTile, 2, 1}});
     if (e == cudaSuccess)
-        e = encode_rows(down, a.h_codes, a.h_scales, n * kParts, c.F);
+        e = encode_rows(down, a.h_codes, a.h_scales, a.parts, c.F);
     static KernelCache kc;
     const size_t smem = Routing::bytes(n, c.E);
     if (e == cudaSuccess) e = prepare_kernel(split_kernel, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess) {
         SplitArgs s = {c.x, c.idx, ws + at.x_codes, reinterpret_cast<uint32_t *>(ws + at.x_scales),
-                       a.arrived, c.S, c.K, c.E, c.H, (c.H + kTile - 1) / kTile};
+                       a.arrived, c.S, c.K, c.E, c.H, a.parts, (c.H + kTile - 1) / kTile * 4 * c.S};
         const int64_t units = (int64_t)c.S * ((c.H + 255) / 256), most = 2 * sm_count();
         const int64_t grid = (units + kThreads / 32 - 1) / (kThreads / 32);
         e = launch_pdl(split_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(kThreads),
@@ -689,8 +750,8 @@ int layer_mxfp4(const LayerCall &c, cudaStream_t stream)
         return MOE_ECUDA;
     }
     int r = check_launch();
-    if (r == MOE_OK) r = launch_layer<true>(up, a, n, stream);
-    if (r == MOE_OK) r = launch_layer<false>(down, a, n, stream);
+    if (r == MOE_OK) r = launch_layer<true>(up, a, stream);
+    if (r == MOE_OK) r = launch_layer<false>(down, a, stream);
     return r;
 }
 

@@ -15,12 +15,13 @@ constexpr int kFewWidth = 16384;    // H, F
 // 1024 entries, 1 to 2 us, where a launch that makes them for all would cost as
 // much.  Ranks are those of the entries' order, so all CTAs and launches agree.
 struct Routing {
-    int16_t *count;   // [E] scratch
+    int16_t *count;   // [E] entries of each expert, then its place among those with tokens
     int16_t *hit;     // [hits] experts with tokens, in increasing order
     int16_t *first;   // [hits + 1] first packed row of each
     int16_t *parts;   // [hits + 1] parts of at most `rows` rows before each
     int16_t *order;   // [rows] the entry of each packed row
-    int16_t *place;   // [S K] the packed row of each entry, -1 without an expert
+    int16_t *place;   // [S K] the row of each entry where parts have `rows` rows each, full
+                      // or not; -1 without an expert
     int hits;
 
     static size_t bytes(int n, int E) { return (size_t)(E + 3 * (n < E ? n : E) + 2 + 2 * n) * 2; }
@@ -92,7 +93,7 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
-        if (e < E) r.count[e] = a;
+        if (e < E) r.count[e] = b;
         if (c[j] > 0) r.hit[b] = e, r.first[b] = a, r.parts[b] = d, ++b;
         a += c[j];
         d += (c[j] + rows - 1) / rows;
@@ -102,43 +103,57 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
     for (int i = tid; i < n; i += THREADS) {
         const int e = __ldg(idx + i);
         if (e >= 0 && e < E) {
-            const int at = r.count[e] + r.place[i];
-            r.order[at] = i;
-            r.place[i] = at;
+            const int h = r.count[e], slot = r.place[i];
+            r.order[r.first[h] + slot] = i;
+            r.place[i] = r.parts[h] * rows + slot;
         }
     }
     __syncthreads();
 }
 
-// out[s, o] = sum over the valid entries of s, in increasing k, for s from `s0` in
-// steps: y [S K, H] holds the experts' rows by entry.
-__device__ __forceinline__ void few_combine(const float *y, const float *topk_w, const int32_t *idx,
-                                            int S, int K, int E, int H, int o, int s0, int step,
-                                            void *out, bool f32)
+// The entries' weights, in shared memory.
+__device__ __forceinline__ void load_weights(const float *topk_w, int n, float *to)
 {
-    for (int s = s0; s < S; s += step) {
-        float sum = 0.0f;
-        for (int k0 = 0; k0 < K; k0 += 8) {
-            float v[8], w[8];
-            const int m = min(8, K - k0);
+    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = __ldg(topk_w + i);
+}
+
+// out[s, o] = sum over the valid entries of s, in increasing k, for N tokens of which
+// the first `count` are stored: y [S K, H] holds the experts' rows by entry.  The
+// loads are unconditional, so that 8 N of them are under way: with a condition
+// each, or a token at a time, 32 tokens took 30 to 50 us.
+constexpr int kFewTokens = 4;
+template <int N>
+__device__ __forceinline__ void few_combine(const float *y, const float *weights,
+                                            const int16_t *place, int K, int H, int o,
+                                            const int (&s)[kFewTokens], int count, void *out,
+                                            bool f32)
+{
+    constexpr int kAtOnce = 8;
+    float sum[N];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int i = s * K + k0 + k;
-                v[k] = w[k] = 0.0f;
-                if (k < m) {
-                    const int e = __ldg(idx + i);
-                    if (e >= 0 && e < E) {
-                        w[k] = __ldg(topk_w + i);
-                        v[k] = __ldcg(y + (int64_t)i * H + o);
-                    }
-                }
+    for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+    for (int k0 = 0; k0 < K; k0 += kAtOnce) {
+        float v[N][kAtOnce];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                v[j][k] = __ldcg(y + (int64_t)(s[j] * K + min(k0 + k, K - 1)) * H + o);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = s[j] * K + min(k0 + k, K - 1);
+                // rows of entries without an expert hold anything
+                if (k0 + k < K && place[i] >= 0) sum[j] = fmaf(weights[i], v[j][k], sum[j]);
             }
+    }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sum = fmaf(w[k], v[k], sum);
-        }
-        if (f32) static_cast<float *>(out)[(int64_t)s * H + o] = sum;
+    for (int j = 0; j < N; ++j) {
+        if (j >= count) break;
+        if (f32) static_cast<float *>(out)[(int64_t)s[j] * H + o] = sum[j];
         else
-            static_cast<__nv_bfloat16 *>(out)[(int64_t)s * H + o] = __float2bfloat16_rn(sum);
+            static_cast<__nv_bfloat16 *>(out)[(int64_t)s[j] * H + o] = __float2bfloat16_rn(sum[j]);
     }
 }
 
@@ -155,7 +170,7 @@ struct LayerCall {
 };
 
 // The layer on MXFP4 weights (csrc/expert_layer_mxfp4.cu).
-size_t layer_mxfp4_workspace(int64_t n, int64_t H, int64_t F);
+size_t layer_mxfp4_workspace(int64_t S, int64_t K, int64_t E, int64_t H, int64_t F);
 int layer_mxfp4(const LayerCall &c, cudaStream_t stream);
 
 inline int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }

@@ -46,7 +46,6 @@ struct QuantArgs {
 
 template <typename T> struct Sixteen;
 template <> struct Sixteen<float> {
-    static constexpr int kBytes = 64;
     __device__ __forceinline__ static void load(const uint8_t *p, float (&f)[kLane])
     {
         uint4 v[4];
@@ -70,7 +69,6 @@ template <> struct Sixteen<float> {
     }
 };
 template <> struct Sixteen<__nv_bfloat16> {
-    static constexpr int kBytes = 32;
     __device__ __forceinline__ static void load(const uint8_t *p, float (&f)[kLane])
     {
         const uint4 v[2] = {ld_stream16(p), ld_stream16(p + 16)};

@@ -140,7 +140,7 @@ def test_layer_validation(L):
     assert need == 1024 + 512 + 256
     assert f(bytes=need - 1) == EINVAL
     need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32, 3)
-    assert need == 1024 + 256 + 512 + 256 + 1024 + 256
+    assert need == 4 * 64 * 32 + 4 * 512 + 4 * 64 * 16 + 4 * 512 + 1024 + 256   # four parts of 64 rows
     assert f(dt=3, bytes=need - 1) == EINVAL
     for out_of_range in ((-1, 64, 2, 8, 32, 0), (2, 0, 2, 8, 32, 0), (1024, 64, 2, 8, 32, 3), (2, 64, 2, 0, 32, 0),
                          (2, 64, 2, 8, 32, 1)):
