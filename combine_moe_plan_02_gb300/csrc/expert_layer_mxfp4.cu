@@ -194,6 +194,11 @@ struct LayerMaps {
     CUtensorMap a, sa, b[2], sb;
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 __device__ __forceinline__ void copy_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
                                         int y, int z)
 {
@@ -321,6 +326,13 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
     __shared__ Shared sh;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 96) {
+        prefetch_map(&maps.a);
+        prefetch_map(&maps.sa);
+        prefetch_map(&maps.b[0]);
+        prefetch_map(&maps.b[1]);
+        prefetch_map(&maps.sb);
+    }
     if (tid == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&sh.full[i], 2);   // both operands

@@ -16,7 +16,7 @@ constexpr int kFewWidth = 16384;    // H, F
 // much.  Ranks are those of the entries' order, so all CTAs and launches agree.
 struct Routing {
     int16_t *count;   // [E] entries of each expert, then its place among those with tokens
-    int16_t *hit;     // [hits] experts with tokens, in increasing order
+    int16_t *hit;     // [hits] experts with tokens
     int16_t *first;   // [hits + 1] first packed row of each
     int16_t *parts;   // [hits + 1] parts of at most `rows` rows before each
     int16_t *order;   // [rows] the entry of each packed row
@@ -45,6 +45,36 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
     constexpr int kWarps = THREADS / 32, kEach = kFewExperts / THREADS;
     __shared__ int s_sum[kWarps], s_hits[kWarps], s_parts[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (n <= 32) {
+        // A warp does it alone, without a look at every expert, which are listed as
+        // they come.
+        if (warp == 0) {
+            int e = lane < n ? __ldg(idx + lane) : -1;
+            if (e < 0 || e >= E) e = -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int count = __popc(same), slot = __popc(same & lanemask_lt());
+            const bool leads = e >= 0 && slot == 0;
+            const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+            int a = leads ? count : 0, d = leads ? (count + rows - 1) / rows : 0;
+            const int mine = a, part = d;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, a, o), w = __shfl_up_sync(0xffffffffu, d, o);
+                if (lane >= o) a += u, d += w;
+            }
+            const int h = __popc(leaders & lanemask_lt()), hits = __popc(leaders);
+            const int leader = __ffs(same) - 1;
+            const int first = __shfl_sync(0xffffffffu, a - mine, leader);
+            const int parts = __shfl_sync(0xffffffffu, d - part, leader);
+            if (leads) r.hit[h] = e, r.first[h] = first, r.parts[h] = parts;
+            if (e >= 0) r.order[first + slot] = lane;
+            if (lane < n) r.place[lane] = e >= 0 ? parts * rows + slot : -1;
+            if (lane == 31) r.first[hits] = a, r.parts[hits] = d, s_hits[0] = hits;
+        }
+        __syncthreads();
+        r.hits = s_hits[0];
+        return;
+    }
     for (int e = tid; e < E; e += THREADS) r.count[e] = 0;
     for (int i = tid; i < n; i += THREADS) {
         const int e = __ldg(idx + i);
