@@ -23,9 +23,9 @@
 // independent).  Rows of a tensor are a multiple of 4.
 //
 // Tensor memory.  Two accumulators of 256 columns would leave no room for scales.
-// They overlap by 64 columns (0 .. 255 and 192 .. 447): the storing warps read the
-// shared columns first and hand them on, so the next tile waits for a quarter of
-// the reads only.  Columns 448 .. 495 hold the scales of two blocks.
+// They overlap by 96 columns (0 .. 255 and 160 .. 415): the storing warps take the
+// shared columns into registers first and hand them on, so the next tile waits for
+// half of the reads and no store.  Columns 416 .. 511 hold the scales of four blocks.
 //
 // Output.  Lane 32 j + q of the accumulator is output 4 q + j: the four warps that
 // read its quarters meet in shared memory, and whole output rows leave in 16-byte
@@ -51,9 +51,10 @@ constexpr int kStageBytes = 2 * kABytes + 3 * kSABytes;
 constexpr int kStages = 5;
 constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kMaxStages = 6;       // of 128 columns
-constexpr int kAccTwo = 192;        // first column of the second accumulator
-constexpr int kScaleAt = 448;       // first column of the scales
+constexpr int kAccTwo = 160;        // first column of the second accumulator
+constexpr int kScaleAt = 416;       // first column of the scales
 constexpr int kScaleCols = 24;      // of a block: 2 x (4 + 8)
+constexpr int kScaleBlocks = 4;
 constexpr int kTmemCols = 512;
 constexpr int64_t kLongest = 32768;
 
@@ -333,7 +334,7 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
             __syncwarp();
         } else if (warp == 1 && rank == 0) {
             Ring r(stages);
-            Ring done(stages);  // the block two before
+            Ring done(stages);  // the block kScaleBlocks before
             int64_t j = 0;
             int i = 0;  // tiles begun
             bool ok = true;
@@ -347,7 +348,7 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
                 const uint32_t idesc[2] = {instr_desc(c.cols, 0), instr_desc(c.cols, 1)};
                 for (int b = 0; b < blocks; ++b, ++j) {
                     // the products that used these columns of scales are done
-                    if (j >= 2) {
+                    if (j >= kScaleBlocks) {
                         if (!wait(&sh.empty[done.at], done.round, &sh.stop)) {
                             ok = false;
                             break;
@@ -361,7 +362,7 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
                     const uint32_t stage = smem_u32(ring) + r.at * stage_bytes;
                     tc_fence_after();
                     if (elect_one()) {
-                        const uint32_t sa = tmem + kScaleAt + (uint32_t)(j & 1) * kScaleCols;
+                        const uint32_t sa = tmem + kScaleAt + (uint32_t)(j % kScaleBlocks) * kScaleCols;
                         const uint32_t sb = sa + 8;
                         const uint64_t from_a = scale_desc(stage + scales_at);
                         const uint64_t from_b = scale_desc(stage + scales_at + kSABytes);
@@ -422,18 +423,19 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
             const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccTwo;
             const int count = c.cols / 64, used = ceil_div(c.to, 4);
             const int m = c.m0 + rank * kLanes;
-            for (int k = 0; k < count; ++k) {
-                // the shared columns first: the last ones of accumulator 0, the
-                // first ones of accumulator 1
-                const int jj = 2 * (buf ? k : count - 1 - k) + odd;
-                uint32_t v[32];
-                tmem_load(acc + jj * 32, v);
-                tmem_wait(v);
-                if (k == 0) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_at(free_at);
-                }
+            // This warp's blocks, the shared columns first: the last ones of
+            // accumulator 0, the first ones of accumulator 1.  The first two are read
+            // before anything is stored; that covers what is shared.
+            auto block = [&](int k) { return 2 * (buf ? k : count - 1 - k) + odd; };
+            uint32_t two[2][32];
+            tmem_load(acc + block(0) * 32, two[0]);
+            tmem_load(acc + block(1) * 32, two[1]);
+            tmem_wait(two[0]);
+            tmem_wait(two[1]);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_at(free_at);
+            auto store = [&](int jj, const uint32_t(&v)[32]) {
                 const int before = (jj >> 2) * 128 + (jj & 3);  // token of x: before + 4 x
                 join();  // what was here has been read
                 uint8_t *mine = box + q * Me::kQuarter + lane * (int)sizeof(Tout);
@@ -470,6 +472,13 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
                                         : make_uint4(w[0], w[1], w[2], w[3]);
                     st16(a.out + ((int64_t)(c.n0 + token) * a.M + first) * (int)sizeof(Tout), o);
                 }
+            };
+            store(block(0), two[0]);
+            store(block(1), two[1]);
+            for (int k = 2; k < count; ++k) {
+                tmem_load(acc + block(k) * 32, two[0]);
+                tmem_wait(two[0]);
+                store(block(k), two[0]);
             }
         }
     }
