@@ -23,9 +23,11 @@
 // independent).  Rows of a tensor are a multiple of 4.
 //
 // Tensor memory.  Two accumulators of 256 columns would leave no room for scales.
-// They overlap by 96 columns (0 .. 255 and 160 .. 415): the storing warps take the
+// They overlap by 128 columns (0 .. 255 and 128 .. 383): the storing warps take the
 // shared columns into registers first and hand them on, so the next tile waits for
-// half of the reads and no store.  Columns 416 .. 511 hold the scales of four blocks.
+// half of the reads and no store.  The rest holds the scales of each stage's block, so
+// that a stage's copy into it, which begins when the products that read the stage before
+// are done, frees its columns too.
 //
 // Output.  Lane 32 j + q of the accumulator is output 4 q + j: the four warps that
 // read its quarters meet in shared memory, and whole output rows leave in 16-byte
@@ -51,10 +53,9 @@ constexpr int kStageBytes = 2 * kABytes + 3 * kSABytes;
 constexpr int kStages = 5;
 constexpr int kRingBytes = kStages * kStageBytes;
 constexpr int kMaxStages = 6;       // of 128 columns
-constexpr int kAccTwo = 160;        // first column of the second accumulator
-constexpr int kScaleAt = 416;       // first column of the scales
+constexpr int kAccTwo = 128;        // first column of the second accumulator
+constexpr int kScaleAt = 384;       // first column of the scales
 constexpr int kScaleCols = 24;      // of a block: 2 x (4 + 8)
-constexpr int kScaleBlocks = 4;
 constexpr int kTmemCols = 512;
 constexpr int64_t kLongest = 32768;
 
@@ -333,59 +334,55 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
             }
             __syncwarp();
         } else if (warp == 1 && rank == 0) {
-            Ring r(stages);
-            Ring done(stages);  // the block kScaleBlocks before
-            int64_t j = 0;
-            int i = 0;  // tiles begun
-            bool ok = true;
-            for (int t = pair; t < tiles && ok; t += pairs, ++i) {
-                const Tile c = tile_of(a, sched, t);
-                // the columns that this accumulator shares with the one before have
-                // been read, and all of the one before that
-                if (i > 0 && !wait(&sh.acc_free, (uint32_t)(i - 1) & 1, &sh.stop)) break;
-                tc_fence_after();
-                const uint32_t acc = tmem + (i & 1) * kAccTwo;
-                const uint32_t idesc[2] = {instr_desc(c.cols, 0), instr_desc(c.cols, 1)};
-                for (int b = 0; b < blocks; ++b, ++j) {
-                    // the products that used these columns of scales are done
-                    if (j >= kScaleBlocks) {
-                        if (!wait(&sh.empty[done.at], done.round, &sh.stop)) {
+            // One thread does it all: what it issues in a block (two waits, up to six
+            // copies of scales, four products) is close to what bounds the kernel.
+            if (elect_one()) {
+                Ring r(stages);
+                int i = 0;  // tiles begun
+                bool ok = true;
+                const uint32_t scale_cols = narrow ? 16 : kScaleCols;
+                for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+                    const Tile c = tile_of(a, sched, t);
+                    // the columns that this accumulator shares with the one before have
+                    // been read, and all of the one before that
+                    if (i > 0 && !wait(&sh.acc_free, (uint32_t)(i - 1) & 1, &sh.stop)) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem + (i & 1) * kAccTwo;
+                    const uint32_t low = instr_desc(c.cols, 0), high = instr_desc(c.cols, 1);
+                    const bool wide = c.cols == kN;
+                    for (int b = 0; b < blocks; ++b) {
+                        if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
                             ok = false;
                             break;
                         }
-                        done.next();
-                    }
-                    if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t stage = smem_u32(ring) + r.at * stage_bytes;
-                    tc_fence_after();
-                    if (elect_one()) {
-                        const uint32_t sa = tmem + kScaleAt + (uint32_t)(j % kScaleBlocks) * kScaleCols;
+                        const uint32_t stage = smem_u32(ring) + r.at * stage_bytes;
+                        tc_fence_after();
+                        const uint32_t sa = tmem + kScaleAt + (uint32_t)r.at * scale_cols;
                         const uint32_t sb = sa + 8;
                         const uint64_t from_a = scale_desc(stage + scales_at);
-                        const uint64_t from_b = scale_desc(stage + scales_at + kSABytes);
-                        const int left = a.K - b * kK;
-                        const int steps = min(ceil_div(left, 64), 4);  // 64 elements each
-                        for (int h = 0; 2 * h < steps; ++h) {
-                            copy_scales(sa + 4 * h, from_a + 32 * h);
-                            copy_scales(sb + 8 * h, from_b + (c.cols >> 2) * h);
-                            if (c.cols == kN) copy_scales(sb + 8 * h + 4, from_b + 64 * h + 32);
+                        const uint64_t from_b = from_a + (kSABytes >> 4);
+                        const uint64_t da = code_desc(stage), db = da + (kABytes >> 4);
+                        const int left = a.K - b * kK;  // 64 elements a product
+                        copy_scales(sa, from_a);
+                        copy_scales(sb, from_b);
+                        if (wide) copy_scales(sb + 4, from_b + 32);
+                        mma_mxf4(acc, da, db, low, sa, sb, b > 0);
+                        if (left > 64) mma_mxf4(acc, da + 2, db + 2, high, sa, sb, true);
+                        if (left > 128) {
+                            const uint32_t sa1 = sa + 4, sb1 = sb + (wide ? 8 : 4);
+                            copy_scales(sa1, from_a + 32);
+                            copy_scales(sb1, from_b + (c.cols >> 2));
+                            if (wide) copy_scales(sb1 + 4, from_b + 96);
+                            mma_mxf4(acc, da + 4, db + 4, low, sa1, sb1, true);
+                            if (left > 192) mma_mxf4(acc, da + 6, db + 6, high, sa1, sb1, true);
                         }
-                        const uint64_t da = code_desc(stage), db = code_desc(stage + kABytes);
-                        for (int s = 0; s < steps; ++s)
-                            mma_mxf4(acc, da + 2 * s, db + 2 * s, idesc[s & 1], sa + 4 * (s >> 1),
-                                     sb + 8 * (s >> 1), b > 0 || s > 0);
                         mma_commit(&sh.empty[r.at], 0);
+                        r.next();
                     }
-                    __syncwarp();
-                    r.next();
+                    if (ok) mma_commit(&sh.acc_full[i & 1], 0);
                 }
-                if (ok && elect_one()) mma_commit(&sh.acc_full[i & 1], 0);
-                __syncwarp();
+                mma_commit(&sh.drain, 0);  // nothing is issued after this
             }
-            if (elect_one()) mma_commit(&sh.drain, 0);  // nothing is issued after this
             __syncwarp();
         } else if (warp == 3) {
             zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
