@@ -421,53 +421,48 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
         }
         __syncwarp();
     } else if (warp == 1) {
-        Ring r(stages), done(stages);  // `done`: the block two before
-        int64_t j = 0;
-        int i = 0;  // tiles begun
-        bool ok = true;
-        for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
-            const int cols = walk(t).rows > kRows / 2 ? kCols : kCols / 2;
-            const uint32_t idesc[2] = {instr_desc(cols, 0), instr_desc(cols, 1)};
-            if (i >= 2 && !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + (i & 1) * kCols;
-            for (int b = 0; b < blocks; ++b, ++j) {
-                // the products that used these columns of scales are done
-                if (j >= 2) {
-                    if (!wait(&sh.empty[done.at], done.round, &sh.stop)) {
+        // One thread issues.  A stage has its own columns of scales: the copy into it,
+        // which begins when the products that read it before are done, frees both.
+        if (elect_one()) {
+            Ring r(stages);
+            int i = 0;  // tiles begun
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x, ++i) {
+                const int cols = walk(t).rows > kRows / 2 ? kCols : kCols / 2;
+                const uint32_t low = instr_desc(cols, 0), high = instr_desc(cols, 1);
+                if (i >= 2 && !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop))
+                    break;
+                tc_fence_after();
+                const uint32_t acc = tmem + (i & 1) * kCols;
+                for (int b = 0; b < blocks; ++b) {
+                    if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
                         ok = false;
                         break;
                     }
-                    done.next();
-                }
-                if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t stage = smem_u32(ring) + r.at * kStageBytes;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t sa = tmem + kScaleAt + (uint32_t)(j & 1) * 16, sb = sa + 8;
+                    const uint32_t stage = smem_u32(ring) + r.at * kStageBytes;
+                    tc_fence_after();
+                    const uint32_t sa = tmem + kScaleAt + (uint32_t)r.at * 16, sb = sa + 8;
                     const uint64_t from_a = desc_of(stage + kCodesA + kCodesB, false);
                     const uint64_t from_b = from_a + (kScales >> 4);
-                    const int steps = min((reduction - b * kK + 63) / 64, 4);  // 64 elements each
-                    for (int h = 0; 2 * h < steps; ++h) {
-                        copy_scales(sa + 4 * h, from_a + 32 * h);
-                        copy_scales(sb + 4 * h, from_b + 32 * h);
+                    const uint64_t da = desc_of(stage, true), db = da + (kCodesA >> 4);
+                    const int left = reduction - b * kK;  // 64 elements a product
+                    copy_scales(sa, from_a);
+                    copy_scales(sb, from_b);
+                    mma_mxf4(acc, da, db, low, sa, sb, b > 0);
+                    if (left > 64) mma_mxf4(acc, da + 2, db + 2, high, sa, sb, true);
+                    if (left > 128) {
+                        copy_scales(sa + 4, from_a + 32);
+                        copy_scales(sb + 4, from_b + 32);
+                        mma_mxf4(acc, da + 4, db + 4, low, sa + 4, sb + 4, true);
+                        if (left > 192) mma_mxf4(acc, da + 6, db + 6, high, sa + 4, sb + 4, true);
                     }
-                    const uint64_t da = desc_of(stage, true), db = desc_of(stage + kCodesA, true);
-                    for (int s = 0; s < steps; ++s)
-                        mma_mxf4(acc, da + 2 * s, db + 2 * s, idesc[s & 1], sa + 4 * (s >> 1),
-                                 sb + 4 * (s >> 1), b > 0 || s > 0);
                     commit(&sh.empty[r.at]);
+                    r.next();
                 }
-                __syncwarp();
-                r.next();
+                if (ok) commit(&sh.acc_full[i & 1]);
             }
-            if (ok && elect_one()) commit(&sh.acc_full[i & 1]);
-            __syncwarp();
+            commit(&sh.drain);  // nothing is issued after this
         }
-        if (elect_one()) commit(&sh.drain);  // nothing is issued after this
         __syncwarp();
     } else if (warp >= 4) {
         const int q = warp & 3, me = tid - 128;  // this warp's quarter; of 128 threads

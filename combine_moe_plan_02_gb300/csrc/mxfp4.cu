@@ -59,14 +59,6 @@ template <> struct Sixteen<float> {
             f[4 * q + 3] = __uint_as_float(v[q].w);
         }
     }
-    __device__ __forceinline__ static void store(uint8_t *p, const float (&f)[kLane])
-    {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            st16_cs(p + 16 * q,
-                    make_uint4(__float_as_uint(f[4 * q]), __float_as_uint(f[4 * q + 1]),
-                               __float_as_uint(f[4 * q + 2]), __float_as_uint(f[4 * q + 3])));
-    }
 };
 template <> struct Sixteen<__nv_bfloat16> {
     __device__ __forceinline__ static void load(const uint8_t *p, float (&f)[kLane])
@@ -81,17 +73,6 @@ template <> struct Sixteen<__nv_bfloat16> {
                 f[8 * q + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
             }
         }
-    }
-    __device__ __forceinline__ static void store(uint8_t *p, const float (&f)[kLane])
-    {
-        uint32_t u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            u[i] = *reinterpret_cast<const uint32_t *>(&b);
-        }
-        st16_cs(p, make_uint4(u[0], u[1], u[2], u[3]));
-        st16_cs(p + 16, make_uint4(u[4], u[5], u[6], u[7]));
     }
 };
 
@@ -110,32 +91,54 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *f)
     return r;
 }
 
-template <typename T, bool GATED>
+// A walk over (row, chunk) by all warps of the grid, without a division in it.
+struct Walk {
+    uint32_t row, chunk, chunks, rows_on, chunks_on;
+    __device__ __forceinline__ explicit Walk(uint32_t n) : chunks(n)
+    {
+        const uint32_t first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+        const uint32_t all = gridDim.x * (kThreads / 32);
+        row = first / n;
+        chunk = first - row * n;
+        rows_on = all / n;
+        chunks_on = all - rows_on * n;
+    }
+    __device__ __forceinline__ void next()
+    {
+        row += rows_on;
+        chunk += chunks_on;
+        if (chunk >= chunks) {
+            chunk -= chunks;
+            ++row;
+        }
+    }
+};
+
+template <typename T, bool GATED, bool MAP>
 __global__ void __launch_bounds__(kThreads) quant_kernel(QuantArgs a)
 {
     const int lane = threadIdx.x & 31;
-    const int64_t W = (int64_t)gridDim.x * (kThreads / 32);
-    const int64_t chunks = (a.D + kUnit - 1) / kUnit, words = (a.D + 127) / 128;
+    const uint32_t D = (uint32_t)a.D, words = (D + 127) / 128, S = (uint32_t)a.S;
+    const uint32_t rows = (uint32_t)a.rows, group = (uint32_t)a.group;
     griddep_wait();
     griddep_launch_dependents();
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); u < a.S * chunks;
-         u += W) {
-        const int64_t s = u / chunks, c = u - s * chunks;
-        const int64_t at = c * kUnit + lane * kLane;  // first element of this lane
-        const bool in = at < a.D;                     // D is a multiple of two lanes
-        const int64_t mine = a.map && lane < a.K ? __ldg(a.map + s * a.K + lane) : s;
+    for (Walk at((D + kUnit - 1) / kUnit); at.row < S; at.next()) {
+        const uint32_t s = at.row, e0 = at.chunk * kUnit + lane * kLane;  // this lane's elements
+        const bool in = e0 < D;                     // D is a multiple of two lanes
+        int64_t mine = -1;
+        if (MAP && lane < a.K) mine = __ldg(a.map + (int64_t)s * a.K + lane);
         float f[kLane];
 #pragma unroll
         for (int i = 0; i < kLane; ++i) f[i] = 0.0f;
         if (in) {
-            const uint8_t *p = a.x + (s * a.D * (GATED ? 2 : 1) + at) * (int64_t)sizeof(T);
+            const uint8_t *p = a.x + ((int64_t)s * (GATED ? 2 * D : D) + e0) * (int)sizeof(T);
             Sixteen<T>::load(p, f);
             if (GATED) {
                 // f32 with the fast exponential and division: a few units in the
                 // last place of 24 bits (2^-17 where exp(-gate) is 2^100), where
                 // the codes that follow keep two bits
                 float up[kLane];
-                Sixteen<T>::load(p + a.D * (int64_t)sizeof(T), up);
+                Sixteen<T>::load(p + (int64_t)D * (int)sizeof(T), up);
 #pragma unroll
                 for (int i = 0; i < kLane; ++i)
                     f[i] = __fdividef(f[i], 1.0f + __expf(-f[i])) * up[i];
@@ -155,20 +158,23 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(QuantArgs a)
         uint32_t word = byte;
         word |= __shfl_down_sync(0xffffffffu, word, 2) << 8;
         word = (word & 0xffffu) | __shfl_down_sync(0xffffffffu, word, 4) << 16;
-        const int64_t w = c * 4 + (lane >> 3);
+        const uint32_t w = at.chunk * 4 + (lane >> 3);
         const bool holds = (lane & 7) == 0 && w < words;
-        const int n = a.map ? a.K : 1;
-        for (int k = 0; k < n; ++k) {
-            const int64_t r = __shfl_sync(0xffffffffu, mine, k);
-            if (r < 0 || r >= a.rows) {
-                if (r != -1 && lane == 0) atomicOr(&g_mxfp4_error, kErrDispatchIndex);
-                continue;
+        uint8_t *codes = a.codes + e0 / 2;
+        uint32_t *scales = a.scales + (int64_t)w * group;
+        if (MAP) {
+            // the entries' rows that can be stored, one after another
+            const bool fits = mine >= 0 && mine < rows;
+            if (!fits && mine != -1) atomicOr(&g_mxfp4_error, kErrDispatchIndex);
+            for (uint32_t left = __ballot_sync(0xffffffffu, fits); left; left &= left - 1) {
+                const uint32_t r = __shfl_sync(0xffffffffu, (uint32_t)mine, __ffs(left) - 1);
+                if (in) st8(codes + (int64_t)r * (D / 2), code);
+                if (holds) scales[r] = word;
             }
-            if (in) st8(a.codes + r * (a.D / 2) + at / 2, code);
-            if (holds) {
-                const int64_t g = a.map ? 0 : r / a.group;
-                a.scales[(g * words + w) * a.group + (r - g * a.group)] = word;
-            }
+        } else {
+            if (in) st8(codes + (int64_t)s * (D / 2), code);
+            const uint32_t g = s / group;
+            if (holds) scales[(int64_t)g * words * group + (s - g * group)] = word;
         }
     }
 }
@@ -180,36 +186,67 @@ struct DequantArgs {
     uint8_t *out;  // [rows, D]
 };
 
+// 16 bytes of values a lane and step, so that a warp's stores are whole lines; `kSteps`
+// of them at a time.
+template <typename T> struct Dequant {
+    static constexpr int kEach = 16 / (int)sizeof(T);   // elements of a lane
+    static constexpr int kSteps = 4;
+    static constexpr int kUnit = 32 * kEach * kSteps;
+};
+
 template <typename T> __global__ void __launch_bounds__(kThreads) dequant_kernel(DequantArgs a)
 {
+    using Dq = Dequant<T>;
     const int lane = threadIdx.x & 31;
-    const int64_t W = (int64_t)gridDim.x * (kThreads / 32);
-    const int64_t chunks = (a.D + kUnit - 1) / kUnit, words = (a.D + 127) / 128;
+    const uint32_t D = (uint32_t)a.D, words = (D + 127) / 128, rows = (uint32_t)a.rows;
+    const uint32_t group = (uint32_t)a.group;
     griddep_wait();
     griddep_launch_dependents();
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-         u < a.rows * chunks; u += W) {
-        const int64_t r = u / chunks, c = u - r * chunks;
-        const int64_t at = c * kUnit + lane * kLane;
-        if (at >= a.D) continue;
-        const int64_t g = r / a.group;
-        const uint2 code = ld_stream8(a.codes + r * (a.D / 2) + at / 2);
-        const uint32_t word = __ldg(a.scales + (g * words + c * 4 + (lane >> 3)) * a.group +
-                                    (r - g * a.group));
-        const uint32_t byte = word >> ((lane >> 1 & 3) * 8) & 255u;
-        const float scale = __uint_as_float(byte == 255 ? 0x7fffffffu
-                                            : byte     ? byte << 23
-                                                       : 0x00400000u);
-        const uint32_t q[2] = {code.x, code.y};
-        float f[kLane];
+    for (Walk at((D + Dq::kUnit - 1) / Dq::kUnit); at.row < rows; at.next()) {
+        const uint32_t r = at.row, g = r / group;
+        const uint8_t *codes = a.codes + (int64_t)r * (D / 2);
+        const uint32_t *scales = a.scales + (int64_t)g * words * group + (r - g * group);
+        uint8_t *out = a.out + (int64_t)r * D * (int)sizeof(T);
+        uint32_t code[Dq::kSteps], word[Dq::kSteps];
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) {
-            // the code's exponent and mantissa as those of an f32: 2^-126 of its
-            // value, subnormal where it is
-            const uint32_t nibble = q[i >> 3] >> (4 * (i & 7));
-            f[i] = __uint_as_float((nibble & 7u) << 22 | (nibble & 8u) << 28) * 0x1p126f * scale;
+        for (int k = 0; k < Dq::kSteps; ++k) {
+            const uint32_t e = at.chunk * Dq::kUnit + (k * 32 + lane) * Dq::kEach;
+            code[k] = word[k] = 0;
+            if (e < D) {
+                code[k] = Dq::kEach == 8 ? __ldg(reinterpret_cast<const uint32_t *>(codes + e / 2))
+                                         : __ldg(reinterpret_cast<const uint16_t *>(codes + e / 2));
+                word[k] = __ldg(scales + (int64_t)(e / 128) * group);
+            }
         }
-        Sixteen<T>::store(a.out + (r * a.D + at) * (int64_t)sizeof(T), f);
+#pragma unroll
+        for (int k = 0; k < Dq::kSteps; ++k) {
+            const uint32_t e = at.chunk * Dq::kUnit + (k * 32 + lane) * Dq::kEach;
+            if (e >= D) break;
+            const uint32_t byte = word[k] >> (e / 32 % 4 * 8) & 255u;
+            const float scale = __uint_as_float(byte == 255 ? 0x7fffffffu
+                                                : byte     ? byte << 23
+                                                           : 0x00400000u);
+            float f[Dq::kEach];
+#pragma unroll
+            for (int i = 0; i < Dq::kEach; ++i) {
+                // the code's exponent and mantissa as those of an f32: 2^-126 of its
+                // value, subnormal where it is
+                const uint32_t nibble = code[k] >> (4 * i);
+                f[i] = __uint_as_float((nibble & 7u) << 22 | (nibble & 8u) << 28) * 0x1p126f * scale;
+            }
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (sizeof(T) == 4) {
+                    u[i] = __float_as_uint(f[i]);
+                } else {
+                    const __nv_bfloat162 b =
+                        __floats2bfloat162_rn(f[2 * i % Dq::kEach], f[(2 * i + 1) % Dq::kEach]);
+                    u[i] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+            }
+            st16_cs(out + (int64_t)e * (int)sizeof(T), make_uint4(u[0], u[1], u[2], u[3]));
+        }
     }
 }
 
@@ -232,7 +269,7 @@ int launch_units(const Args &a, int64_t units, cudaStream_t stream)
     return check_launch();
 }
 
-int64_t units_of(int64_t rows, int64_t D) { return rows * ((D + kUnit - 1) / kUnit); }
+int64_t units_of(int64_t rows, int64_t D, int unit) { return rows * ((D + unit - 1) / unit); }
 
 constexpr int64_t kMaxWidth = 1 << 24;
 
@@ -246,11 +283,11 @@ int check_tensor(int64_t groups, int64_t rows, int64_t D)
     return MOE_OK;
 }
 
-template <bool GATED> int run_quant(QuantArgs a, int dtype, cudaStream_t stream)
+template <bool GATED, bool MAP> int run_quant(const QuantArgs &a, int dtype, cudaStream_t stream)
 {
-    const int64_t units = units_of(a.S, a.D);
-    if (dtype == MOE_F32) return launch_units<quant_kernel<float, GATED>>(a, units, stream);
-    return launch_units<quant_kernel<__nv_bfloat16, GATED>>(a, units, stream);
+    const int64_t units = units_of(a.S, a.D, kUnit);
+    if (dtype == MOE_F32) return launch_units<quant_kernel<float, GATED, MAP>>(a, units, stream);
+    return launch_units<quant_kernel<__nv_bfloat16, GATED, MAP>>(a, units, stream);
 }
 
 } // namespace
@@ -274,7 +311,7 @@ MOE_EXPORT int moe_quant_mxfp4(const void *x, int dtype, int64_t groups, int64_t
     a.group = rows;
     a.codes = codes;
     a.scales = reinterpret_cast<uint32_t *>(scales);
-    return run_quant<false>(a, dtype, (cudaStream_t)stream);
+    return run_quant<false, false>(a, dtype, (cudaStream_t)stream);
 }
 
 MOE_EXPORT int moe_dispatch_quant_mxfp4(const void *x, int dtype, int64_t S, int64_t D, int K,
@@ -297,7 +334,7 @@ MOE_EXPORT int moe_dispatch_quant_mxfp4(const void *x, int dtype, int64_t S, int
     a.K = K;
     a.codes = codes;
     a.scales = reinterpret_cast<uint32_t *>(scales);
-    return run_quant<false>(a, dtype, (cudaStream_t)stream);
+    return run_quant<false, true>(a, dtype, (cudaStream_t)stream);
 }
 
 MOE_EXPORT int moe_swiglu_quant_mxfp4(const void *u, int dtype, int64_t rows, int64_t F,
@@ -315,7 +352,7 @@ MOE_EXPORT int moe_swiglu_quant_mxfp4(const void *u, int dtype, int64_t rows, in
     a.D = F;
     a.codes = codes;
     a.scales = reinterpret_cast<uint32_t *>(scales);
-    return run_quant<true>(a, dtype, (cudaStream_t)stream);
+    return run_quant<true, false>(a, dtype, (cudaStream_t)stream);
 }
 
 MOE_EXPORT int moe_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t groups,
@@ -330,10 +367,11 @@ MOE_EXPORT int moe_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, in
     if (D % 32 || !aligned16(codes) || !aligned4(scales) || !aligned16(out)) return MOE_EALIGN;
     DequantArgs a = {codes, reinterpret_cast<const uint32_t *>(scales), groups * rows, D, rows,
                      static_cast<uint8_t *>(out)};
-    const int64_t units = units_of(a.rows, D);
     return out_dtype == MOE_F32
-               ? launch_units<dequant_kernel<float>>(a, units, (cudaStream_t)stream)
-               : launch_units<dequant_kernel<__nv_bfloat16>>(a, units, (cudaStream_t)stream);
+               ? launch_units<dequant_kernel<float>>(a, units_of(a.rows, D, Dequant<float>::kUnit),
+                                                     (cudaStream_t)stream)
+               : launch_units<dequant_kernel<__nv_bfloat16>>(
+                     a, units_of(a.rows, D, Dequant<__nv_bfloat16>::kUnit), (cudaStream_t)stream);
 }
 
 namespace moe {
