@@ -607,35 +607,47 @@ class MxFp4(NamedTuple):
         return torch.Size((*self.codes.shape[:-1], 2 * self.codes.shape[-1]))
 
 
+_U8 = torch.uint8
+
+
 def _check_mx(name: str, q: MxFp4, dims: Sequence[int] = (2, 3)):
-    """Raises unless codes and scales are what the kernels read."""
+    """Raises unless codes and scales are what the kernels read; (groups, rows,
+    D) of the values."""
     codes, scales = q
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not _U8 or scales.dtype is not _U8:
         raise TypeError(f"{name} must have uint8 codes and scales")
     shape = codes.shape
-    if len(shape) not in dims or shape[-1] % 16:
+    n = len(shape)
+    if n not in dims or shape[-1] % 16:
         raise ValueError(f"{name} must hold rows of a multiple of 32 elements")
-    if tuple(scales.shape) != (*shape[:-2], -(-shape[-1] // 64), shape[-2], 4):
+    half, rows = shape[-1], shape[-2]
+    words = -(-half // 64)
+    if scales.shape != ((words, rows, 4) if n == 2 else (shape[0], words, rows, 4)):
         raise ValueError(f"{name}'s scales must be [.., ceil(D / 128), rows, 4]")
-    if codes.device != scales.device:
+    if codes.get_device() != scales.get_device():
         raise ValueError(f"{name}'s codes and scales must live on one device")
+    return (1 if n == 2 else shape[0]), rows, 2 * half
 
 
 def _mx_out(name: str, out: Optional[MxFp4], lead, rows: int, D: int, device, stream) -> MxFp4:
     if out is None:
-        return MxFp4(_empty((*lead, rows, D // 2), torch.uint8, device, stream),
-                     _empty((*lead, -(-D // 128), rows, 4), torch.uint8, device, stream))
-    _check_mx(name, out)
-    if tuple(out.shape) != (*lead, rows, D):
+        return MxFp4(_empty((*lead, rows, D // 2), _U8, device, stream),
+                     _empty((*lead, -(-D // 128), rows, 4), _U8, device, stream))
+    _check_mx(name, out, (2 + len(lead),))
+    if out.codes.shape != (*lead, rows, D // 2):
         raise ValueError(f"{name} must be {[*lead, rows, D]}")
     return out
 
 
-def _values(x: torch.Tensor, name: str, D: int):
-    if x.dtype not in _TORCH_DT.values():
-        raise TypeError(f"{name} must be bfloat16 or float32")
+def _values(x: torch.Tensor, name: str, D: int) -> int:
+    """The code of x's type, if its rows can be MXFP4."""
     if D < 32 or D % 32:
         raise ValueError("MXFP4 rows must be a multiple of 32 elements")
+    if x.dtype is torch.bfloat16:
+        return MOE_BF16
+    if x.dtype is torch.float32:
+        return MOE_F32
+    raise TypeError(f"{name} must be bfloat16 or float32")
 
 
 def moe_quant_mxfp4(x: torch.Tensor, *, out: Optional[MxFp4] = None, stream=None) -> MxFp4:
@@ -643,10 +655,10 @@ def moe_quant_mxfp4(x: torch.Tensor, *, out: Optional[MxFp4] = None, stream=None
     if x.dim() not in (2, 3):
         raise ValueError("x must be [rows, D] or [E, rows, D]")
     *lead, rows, D = x.shape
-    _values(x, "x", D)
+    dt = _values(x, "x", D)
     out = _mx_out("out", out, lead, rows, D, x.device, stream)
     _abi.check("moe_quant_mxfp4", lib().moe_quant_mxfp4(
-        _ptr(x), _dt(x), lead[0] if lead else 1, rows, D, _ptr(out.codes), _ptr(out.scales),
+        _ptr(x), dt, lead[0] if lead else 1, rows, D, _ptr(out.codes), _ptr(out.scales),
         _stream(stream, x)))
     return out
 
@@ -656,21 +668,24 @@ def moe_dispatch_quant_mxfp4(x: torch.Tensor, tok_map: torch.Tensor, *,
     """Rows [S, D] (bf16 or f32) to MXFP4 in the K packed rows of each token.
     Without `out` there are S * K packed rows, rounded up to a multiple of 4 as
     moe_expert_gemm_mxfp4 asks."""
-    if x.dim() != 2 or tok_map.dim() != 2 or tok_map.shape[0] != x.shape[0]:
+    if x.dim() != 2 or tok_map.dim() != 2:
         raise ValueError("x must be [S, D] and tok_map [S, K]")
-    if tok_map.dtype != torch.int64:
-        raise TypeError("tok_map must be int64")
     S, D = x.shape
-    _values(x, "x", D)
-    K = tok_map.shape[1]
+    if tok_map.dtype is not torch.int64:
+        raise TypeError("tok_map must be int64")
+    n, K = tok_map.shape
+    if n != S:
+        raise ValueError("x must be [S, D] and tok_map [S, K]")
+    dt = _values(x, "x", D)
     if out is None:
-        out = _mx_out("out", None, (), max(-(-S * K // 4) * 4, 4), D, x.device, stream)
+        rows = max(-(-S * K // 4) * 4, 4)
+        out = _mx_out("out", None, (), rows, D, x.device, stream)
     else:
-        _check_mx("out", out, (2,))
-        if out.shape[1] != D:
+        _, rows, width = _check_mx("out", out, (2,))
+        if width != D:
             raise ValueError("out must hold rows of D elements")
     _abi.check("moe_dispatch_quant_mxfp4", lib().moe_dispatch_quant_mxfp4(
-        _ptr(x), _dt(x), S, D, K, _ptr(tok_map), _ptr(out.codes), _ptr(out.scales), out.shape[0],
+        _ptr(x), dt, S, D, K, _ptr(tok_map), _ptr(out.codes), _ptr(out.scales), rows,
         _stream(stream, x)))
     return out
 
@@ -681,28 +696,29 @@ def moe_swiglu_quant_mxfp4(u: torch.Tensor, *, out: Optional[MxFp4] = None,
     in f32, to MXFP4 [rows, F]."""
     if u.dim() != 2 or u.shape[1] % 2:
         raise ValueError("u must be [rows, 2 F]")
-    rows, F = u.shape[0], u.shape[1] // 2
-    _values(u, "u", F)
+    rows, F = u.shape
+    F //= 2
+    dt = _values(u, "u", F)
     out = _mx_out("out", out, (), rows, F, u.device, stream)
     _abi.check("moe_swiglu_quant_mxfp4", lib().moe_swiglu_quant_mxfp4(
-        _ptr(u), _dt(u), rows, F, _ptr(out.codes), _ptr(out.scales), _stream(stream, u)))
+        _ptr(u), dt, rows, F, _ptr(out.codes), _ptr(out.scales), _stream(stream, u)))
     return out
 
 
 def moe_dequant_mxfp4(q: MxFp4, *, out_dtype: torch.dtype = torch.bfloat16,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values that MXFP4 rows or weights stand for."""
-    _check_mx("q", q)
-    shape = q.shape
+    groups, rows, D = _check_mx("q", q)
+    codes, scales = q
+    shape = (*codes.shape[:-1], D)
     if out is None:
         if out_dtype not in _TORCH_DT.values():
             raise TypeError(f"unsupported output dtype {out_dtype}")
-        out = _empty(shape, out_dtype, q.codes.device, stream)
+        out = _empty(shape, out_dtype, codes.device, stream)
     elif out.shape != shape or out.dtype not in _TORCH_DT.values():
         raise ValueError("out must be bfloat16 or float32 with the shape of the values")
     _abi.check("moe_dequant_mxfp4", lib().moe_dequant_mxfp4(
-        _ptr(q.codes), _ptr(q.scales), shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1],
-        _ptr(out), _dt(out), _stream(stream, q.codes)))
+        _ptr(codes), _ptr(scales), groups, rows, D, _ptr(out), _dt(out), _stream(stream, codes)))
     return out
 
 
@@ -712,17 +728,16 @@ def moe_expert_gemm_mxfp4(x: MxFp4, w: MxFp4, plan: Union[Plan, CapacityPlan], *
     """y[r] = w[e] x[r] for the rows of each bucket e of the plan, zero on rows
     in no bucket.  x [rows, D] (rows of the buffer a multiple of 4), w
     [E, N, D], both in MXFP4; y [rows, N]."""
-    _check_mx("x", x, (2,))
-    _check_mx("w", w, (3,))
-    rows, D = x.shape
-    E, N, _ = w.shape
-    if w.shape[2] != D:
+    _, rows, D = _check_mx("x", x, (2,))
+    E, N, width = _check_mx("w", w, (3,))
+    if width != D:
         raise ValueError("w must be [E, N, D] and x [rows, D]")
     _check_plan(plan, E)
-    out = _expert_out(out, (rows, N), out_dtype, x.codes.device, stream)
+    codes = x.codes
+    out = _expert_out(out, (rows, N), out_dtype, codes.device, stream)
     _abi.check("moe_expert_gemm_mxfp4", lib().moe_expert_gemm_mxfp4(
-        _ptr(x.codes), _ptr(x.scales), rows, _ptr(w.codes), _ptr(w.scales), N, D, E,
-        _ptr(plan.cnt), _ptr(plan.off), _ptr(out), _dt(out), _stream(stream, x.codes)))
+        _ptr(codes), _ptr(x.scales), rows, _ptr(w.codes), _ptr(w.scales), N, D, E,
+        _ptr(plan.cnt), _ptr(plan.off), _ptr(out), _dt(out), _stream(stream, codes)))
     return out
 
 
@@ -740,36 +755,39 @@ def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
     w_up[e] x[s], e = topk_idx[s,k], for up to 1024 entries S * K.  x bf16
     [S, H]; w_up [E, 2 F, H] (gates before ups) and w_down [E, H, F] both bf16
     or both in MXFP4.  Ids outside [0, E) give nothing."""
-    mx = not isinstance(w_up, torch.Tensor)
-    if mx == isinstance(w_down, torch.Tensor):
-        raise TypeError("w_up and w_down must both be tensors or both MxFp4")
-    if mx:
-        _check_mx("w_up", w_up, (3,))
-        _check_mx("w_down", w_down, (3,))
-    elif w_up.dtype != torch.bfloat16 or w_down.dtype != torch.bfloat16:
-        raise TypeError("weights must be bfloat16 or MxFp4")
-    if x.dtype != torch.bfloat16 or x.dim() != 2:
+    if isinstance(w_up, torch.Tensor):
+        if not isinstance(w_down, torch.Tensor):
+            raise TypeError("w_up and w_down must both be tensors or both MxFp4")
+        if w_up.dtype is not torch.bfloat16 or w_down.dtype is not torch.bfloat16:
+            raise TypeError("weights must be bfloat16 or MxFp4")
+        kind, shape, down = MOE_BF16, w_up.shape, w_down.shape
+        parts = w_up, None, w_down, None
+    else:
+        if isinstance(w_down, torch.Tensor):
+            raise TypeError("w_up and w_down must both be tensors or both MxFp4")
+        kind, shape, down = MOE_MXFP4, _check_mx("w_up", w_up, (3,)), _check_mx("w_down", w_down, (3,))
+        parts = *w_up, *w_down
+    if x.dtype is not torch.bfloat16 or x.dim() != 2:
         raise TypeError("x must be bfloat16 [S, H]")
     S, H = x.shape
-    shape, down = w_up.shape, w_down.shape
-    if len(shape) != 3 or len(down) != 3 or shape[1] % 2 or shape[2] != H or \
-            tuple(down) != (shape[0], H, shape[1] // 2):
+    if len(shape) != 3:
         raise ValueError("w_up must be [E, 2 F, H] and w_down [E, H, F]")
-    if topk_idx.dtype != torch.int32 or topk_idx.dim() != 2 or topk_idx.shape[0] != S:
+    E, F = shape[0], shape[1] // 2
+    if shape[1] % 2 or shape[2] != H or down != (E, H, F):
+        raise ValueError("w_up must be [E, 2 F, H] and w_down [E, H, F]")
+    routes = topk_idx.shape
+    if topk_idx.dtype is not torch.int32 or len(routes) != 2 or routes[0] != S:
         raise TypeError("topk_idx must be int32 [S, K]")
-    if topk_w.dtype != torch.float32 or topk_w.shape != topk_idx.shape:
+    if topk_w.dtype is not torch.float32 or topk_w.shape != routes:
         raise TypeError("topk_w must be float32 with the shape of topk_idx")
-    E, F, K = shape[0], shape[1] // 2, topk_idx.shape[1]
+    K = routes[1]
     out = _expert_out(out, (S, H), out_dtype, x.device, stream)
     L = lib()
-    kind = MOE_MXFP4 if mx else MOE_BF16
     nws = int(L.moe_expert_layer_workspace_size(S, H, K, E, F, kind))
     ws = _workspace(nws, x.device, workspace, stream)
-    up, down = (w if mx else (w, None) for w in (w_up, w_down))
     _abi.check("moe_expert_layer", L.moe_expert_layer(
-        _ptr(x), S, H, _ptr(topk_idx), _ptr(topk_w), K, E, F, kind,
-        _ptr(up[0]), _ptr(up[1]), _ptr(down[0]), _ptr(down[1]), _ptr(out), _dt(out), _ptr(ws), nws,
-        _stream(stream, x)))
+        _ptr(x), S, H, _ptr(topk_idx), _ptr(topk_w), K, E, F, kind, *map(_ptr, parts), _ptr(out),
+        _dt(out), _ptr(ws), nws, _stream(stream, x)))
     return out
 
 
