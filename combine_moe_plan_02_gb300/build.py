@@ -17,9 +17,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_gb300.so")
 SOURCES = ["plan.cu", "plan_dispatch.cu", "dispatch.cu", "combine.cu", "combine_backward.cu",
-           "expert_gemm.cu", "expert_gemm_mxfp4.cu", "mxfp4.cu", "expert_layer.cu", "expert_layer_mxfp4.cu",
+           "expert_gemm.cu", "expert_gemm_mxfp4.cu", "mxfp4.cu", "expert_layer.cu",
            "grad_norm.cu", "status.cu", "selftest.cu"]
-HEADERS = ["common.cuh", "pair.cuh", "few.cuh", os.path.join("..", "..", "include", "moe_plan.h")]
+HEADERS = ["common.cuh", "pair.cuh", os.path.join("..", "..", "include", "moe_plan.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",

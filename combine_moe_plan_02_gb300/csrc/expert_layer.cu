@@ -1,417 +1,976 @@
-// A whole routed layer for a few tokens, on bf16 weights in two launches.
+// A whole routed layer for a few tokens, weights in bf16 or MXFP4.
 //
 //   out[s] = sum_k topk_w[s,k] * w_down[e] h,   e = topk_idx[s,k]
 //   h      = silu(w_gate[e] x[s]) * (w_up[e] x[s])
-// with w_up [E, 2 F, H] (gates before ups) and w_down [E, H, F]; MXFP4 weights are in
-// csrc/expert_layer_mxfp4.cu.  Every sum is f32; out is rounded once.
+// with w_up [E, 2 F, H] (gates before ups) and w_down [E, H, F].  Every sum is f32; out
+// is rounded once.
 //
-// The first launch writes h of every entry (s, k), the second y = w_down h, and
-// the CTA that brings the last expert's share of 32 columns sums them over k.
-// Both list the experts that have tokens from topk_idx, cut their weights into tiles
-// of 32 rows and hand each CTA a contiguous run of them.
+// Two launches (up, down), and one before them that prepares x for MXFP4 weights;
+// each begins while the one before ends.  Up and down are one kernel.  Its CTAs, two
+// an SM, walk tiles of 128 weight rows (64 gates and their ups; 128 outputs) for up
+// to 8 entries (s, k) of an expert.  The weights bound the call: one token of 8
+// experts reads 604 MB of bf16 weights or 160 MB of MXFP4, its other data are 100 KB.
+// So one warp does nothing but copy weights with TMA into a ring of stages (80 or
+// 64 KB of weights in flight a CTA), and begins before the launch waits for the one before
+// it (nothing there writes weights).  A second warp copies the rows that they meet, one
+// thread issues the matrix instructions (tcgen05, weights on the M side, entries on the N
+// side: nothing is spent on a weight outside the tensor core), four warps read the sums.
+// A token's outputs are summed over k by the warp that brings the last of its experts.
 //
-// A tile's weights are read once, straight into registers, and bound the call: one
-// token of 8 experts reads 604 MB of weights, its other data are 100 KB.  The
-// eight warps of a CTA share the reduction, each 1/8 of it over all 32 rows, and
-// add their sums in shared memory, in order.  A lane's next loads are issued before it
-// uses the last ones, across tiles, so that the reads do not stop while the warps
-// meet.  The products are those of the warp-wide matrix instruction (mma.sync,
-// 16 x 8 x 16): with at most a few tokens an expert it is far from bounding, and
-// takes weights from registers, where the loads put them.
+// bf16 weights: x goes in as it is, a row an entry.  h is f32: it goes in as three
+// bf16 rows that add up to it.
 //
-// Lane (g, t) holds 8 elements of rows g and g + 8; the eight columns are tokens.  x
-// goes in as it is.  h has more bits than bf16: it goes in as two bf16 parts (16
-// bits; three parts for f32 outputs), each a column, whose sums are added.
+// MXFP4 weights: the block-scaled instruction (kind::mxf4) takes codes and scales as they
+// are, but wants E2M1 on the other side too.  So x and h are written as sums of eight
+// MXFP4 rows: of a block of 32 with largest magnitude a, 2^e <= a < 2^(e + 1), the first
+// row is the block rounded to multiples of 2^(e - 1) and less (values up to 4 units,
+// steps of at most one), the next what that left (at most half a unit) in units of
+// 2^(e - 4), and so on, each three bits further.  The eighth leaves at most 2^-23 of a,
+// about what an f32 sum does.  Each row is a column of the product, and the columns' sums
+// are added in f32.  Decoding the weights to f16 in registers for the warp-wide
+// instruction instead takes 2.7 instructions a weight: 70 us for one token of 8
+// experts (6144, 2048) and 2290 us for 32 tokens of 64 (7168, 2048).
+//
+// The instruction wants the scales of 128 rows and 128 elements as words in 32 lanes
+// x 4 columns of tensor memory, row 32 j + q in column j of lane q, and a copy from
+// shared memory puts 16 bytes into one lane.  The rows' scales are written in that
+// order here.  The weights' scales lie one word after another, so that their row
+// 4 q + j arrives in column j of lane q, and TMA lays row 4 q + j of the codes in row 32 j
+// + q of the stage to match (as in csrc/expert_gemm_mxfp4.cu).
 
-#include "few.cuh"
+#include "pair.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 32;            // weight rows of a tile: two of the instruction's 16
-constexpr int kDepth = 2;            // chunks of 64 bytes of each row in flight
-constexpr int kMaxRows = 8;          // tokens of an expert taken at once
-constexpr int kChunk = 32;           // elements of 64 bytes of weights
-constexpr int kStageBudget = 88 << 10;  // so that two CTAs fit an SM
+constexpr int kMaxEntries = 1024;    // S * K
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxWidth = 16384;     // H, F
+constexpr int kThreads = 256;
+constexpr int kRows = 8;             // entries of a tile
+constexpr int kTile = 128;           // weight rows of a tile
+constexpr int kCodesA = kTile * 128; // of weights in a stage: 128 bytes of each row
+constexpr int kScales = 2 * 512;     // of 128 rows in a stage, or places for them
+constexpr int kMaxStages = 10;
+constexpr int kAcc = 64;             // TMEM columns of an accumulator
+constexpr int kScaleAt = 2 * kAcc;   // first column of the scales
+constexpr int kTmemCols = 256;       // so that two CTAs fit an SM
+constexpr int kSmem = 115712;        // of shared memory, likewise
+constexpr int kBoxBytes = kRows * kTile / 2 * 4;  // h of a tile
+// The tensor core cuts a sum's low bits off at each step; 48 of them leave less than
+// 1e-6, and the sums of so many stages are added in f32.
+constexpr int kSumStages = 12;
+
+// What depends on the weights' type: elements of a stage, rows that stand for one of h
+// and the columns they take (one of x takes as many with MXFP4, one with bf16), bytes of
+// the rows in a stage.
+template <bool MX> struct Form;
+template <> struct Form<true> {
+    static constexpr int kK = 256, kH = 8, kColumns = 8;
+    static constexpr int kCodesB = kRows * kColumns * 128;
+    static constexpr int kStageBytes = kCodesA + kCodesB + 2 * kScales;
+};
+template <> struct Form<false> {
+    static constexpr int kK = 64, kH = 3, kColumns = 4;
+    static constexpr int kCodesB = kRows * kColumns * 128;
+    static constexpr int kStageBytes = kCodesA + kCodesB;
+};
+constexpr int kParts = Form<true>::kH;
+
+__device__ uint32_t g_layer_error;  // kErrExpertTimeout
+
+// --- which experts have tokens ----------------------------------------------------
+
+// Every CTA makes these lists for itself, in shared memory, from topk_idx: at most
+// 1024 entries, 1 to 2 us, where a launch that makes them for all would cost as
+// much.  Ranks are those of the entries' order, so all CTAs and launches agree.
+struct Routing {
+    int16_t *count;   // [E] entries of each expert, then its place among those with tokens
+    int16_t *hit;     // [hits] experts with tokens
+    int16_t *first;   // [hits + 1] first packed row of each
+    int16_t *parts;   // [hits + 1] parts of at most `rows` rows before each
+    int16_t *order;   // [rows] the entry of each packed row
+    int16_t *place;   // [S K] the row of each entry where parts have `rows` rows each, full
+                      // or not; -1 without an expert
+    int hits;
+
+    static size_t bytes(int n, int E) { return (size_t)(E + 3 * (n < E ? n : E) + 2 + 2 * n) * 2; }
+
+    __device__ Routing(void *smem, int n, int E)
+    {
+        const int most = min(n, E);
+        count = static_cast<int16_t *>(smem);
+        hit = count + E;
+        first = hit + most;
+        parts = first + most + 1;
+        order = parts + most + 1;
+        place = order + n;
+        hits = 0;
+    }
+};
+
+template <int THREADS>
+__device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
+{
+    constexpr int kWarps = THREADS / 32, kEach = kMaxExperts / THREADS;
+    __shared__ int s_sum[kWarps], s_hits[kWarps], s_parts[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (n <= 32) {
+        // A warp does it alone, without a look at every expert, which are listed as
+        // they come.
+        if (warp == 0) {
+            int e = lane < n ? __ldg(idx + lane) : -1;
+            if (e < 0 || e >= E) e = -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int count = __popc(same), slot = __popc(same & lanemask_lt());
+            const bool leads = e >= 0 && slot == 0;
+            const uint32_t leaders = __ballot_sync(0xffffffffu, leads);
+            int a = leads ? count : 0, d = leads ? (count + rows - 1) / rows : 0;
+            const int mine = a, part = d;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, a, o), w = __shfl_up_sync(0xffffffffu, d, o);
+                if (lane >= o) a += u, d += w;
+            }
+            const int h = __popc(leaders & lanemask_lt()), hits = __popc(leaders);
+            const int leader = __ffs(same) - 1;
+            const int first = __shfl_sync(0xffffffffu, a - mine, leader);
+            const int parts = __shfl_sync(0xffffffffu, d - part, leader);
+            if (leads) r.hit[h] = e, r.first[h] = first, r.parts[h] = parts;
+            if (e >= 0) r.order[first + slot] = lane;
+            if (lane < n) r.place[lane] = e >= 0 ? parts * rows + slot : -1;
+            if (lane == 31) r.first[hits] = a, r.parts[hits] = d, s_hits[0] = hits;
+        }
+        __syncthreads();
+        r.hits = s_hits[0];
+        return;
+    }
+    for (int e = tid; e < E; e += THREADS) r.count[e] = 0;
+    for (int i = tid; i < n; i += THREADS) {
+        const int e = __ldg(idx + i);
+        r.place[i] = e >= 0 && e < E ? e : -1;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const int i = i0 + lane, e = i < n ? r.place[i] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, e);
+            const int before = e >= 0 ? r.count[e] : 0;
+            __syncwarp();
+            if (e >= 0) {
+                r.place[i] = before + __popc(same & lanemask_lt());
+                if ((same & lanemask_lt()) == 0) r.count[e] = before + __popc(same);
+            }
+            __syncwarp();
+        }
+    }
+    __syncthreads();
+    // a thread owns kEach neighbouring experts
+    int c[kEach], sum = 0, some = 0, part = 0;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int e = tid * kEach + j;
+        c[j] = e < E ? r.count[e] : 0;
+        sum += c[j];
+        some += c[j] > 0;
+        part += (c[j] + rows - 1) / rows;
+    }
+    int a = sum, b = some, d = part;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, a, o), v = __shfl_up_sync(0xffffffffu, b, o),
+                  w = __shfl_up_sync(0xffffffffu, d, o);
+        if (lane >= o) a += u, b += v, d += w;
+    }
+    if (lane == 31) s_sum[warp] = a, s_hits[warp] = b, s_parts[warp] = d;
+    __syncthreads();
+    a -= sum, b -= some, d -= part;
+    r.hits = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) a += s_sum[w], b += s_hits[w], d += s_parts[w];
+        r.hits += s_hits[w];
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int e = tid * kEach + j;
+        if (e < E) r.count[e] = b;
+        if (c[j] > 0) r.hit[b] = e, r.first[b] = a, r.parts[b] = d, ++b;
+        a += c[j];
+        d += (c[j] + rows - 1) / rows;
+    }
+    if (tid == THREADS - 1) r.first[b] = a, r.parts[b] = d;
+    __syncthreads();
+    for (int i = tid; i < n; i += THREADS) {
+        const int e = __ldg(idx + i);
+        if (e >= 0 && e < E) {
+            const int h = r.count[e], slot = r.place[i];
+            r.order[r.first[h] + slot] = i;
+            r.place[i] = r.parts[h] * rows + slot;
+        }
+    }
+    __syncthreads();
+}
+
+// The entries' weights, in shared memory.
+__device__ __forceinline__ void load_weights(const float *topk_w, int n, float *to)
+{
+    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = __ldg(topk_w + i);
+}
+
+// out[s, o] = sum over the valid entries of s, in increasing k, for N tokens of which
+// the first `count` are stored: y [S K, H] holds the experts' rows by entry.  The
+// loads are unconditional, so that 8 N of them are under way: with a condition
+// each, or a token at a time, 32 tokens took 30 to 50 us.
+constexpr int kTokens = 4;
+template <int N>
+__device__ __forceinline__ void sum_entries(const float *y, const float *weights,
+                                            const int16_t *place, int K, int H, int o,
+                                            const int (&s)[kTokens], int count, void *out,
+                                            bool f32)
+{
+    constexpr int kAtOnce = 8;
+    float sum[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+    for (int k0 = 0; k0 < K; k0 += kAtOnce) {
+        float v[N][kAtOnce];
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                v[j][k] = __ldcg(y + (int64_t)(s[j] * K + min(k0 + k, K - 1)) * H + o);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int i = s[j] * K + min(k0 + k, K - 1);
+                // rows of entries without an expert hold anything
+                if (k0 + k < K && place[i] >= 0) sum[j] = fmaf(weights[i], v[j][k], sum[j]);
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        if (j >= count) break;
+        if (f32) static_cast<float *>(out)[(int64_t)s[j] * H + o] = sum[j];
+        else
+            static_cast<__nv_bfloat16 *>(out)[(int64_t)s[j] * H + o] = __float2bfloat16_rn(sum[j]);
+    }
+}
+
+// --- x and h as eight rows ------------------------------------------------------
+
+// Eight neighbouring values, four lanes a block of 32: the codes of row p (one
+// word) and the block's scale byte.  `byte` is that of row 0, 255 where the block
+// has an infinity or a NaN; rows whose scale would be below 2^-127 are zero.
+struct Split {
+    float v[8];
+    int byte;
+
+    __device__ __forceinline__ void begin()
+    {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = (int)(top >> 23);
+        byte = e == 255 ? 255 : e - 1;  // -1 for zeros and what is below 2^-126
+    }
+    __device__ __forceinline__ int scale(int p) const
+    {
+        return byte == 255 ? (p ? 0 : 255) : max(byte - 3 * p, 0);
+    }
+    __device__ __forceinline__ uint32_t next(int p)
+    {
+        if (byte == 255) return p ? 0 : 0x22222222u;  // ones, times NaN
+        if (byte - 3 * p < 0) return 0;
+        const float inv = __uint_as_float((uint32_t)(254 - (byte - 3 * p)) << 23);
+        const float unit = byte - 3 * p ? __uint_as_float((uint32_t)(byte - 3 * p) << 23)
+                                        : __uint_as_float(0x00400000u);
+        uint32_t word = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t code, back;
+            asm("{\n\t.reg .b8 c;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 c, %3, %2;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %1, c;\n\t"
+                "mov.b32 %0, {c, 0, 0, 0};\n\t}"
+                : "=r"(code), "=r"(back)
+                : "f"(v[2 * i] * inv), "f"(v[2 * i + 1] * inv));
+            word |= (code & 255u) << (8 * i);
+            const __half2 h = *reinterpret_cast<const __half2 *>(&back);
+            // exact: what is left is a multiple of the value's last bit
+            v[2 * i] = fmaf(-unit, __low2float(h), v[2 * i]);
+            v[2 * i + 1] = fmaf(-unit, __high2float(h), v[2 * i + 1]);
+        }
+        return word;
+    }
+};
+
+// Where the word of row p of an entry lies among the words of all parts.
+__device__ __forceinline__ int scale_place(int place, int p)
+{
+    const int part = place / kRows, slot = place % kRows;  // column 8 slot + p = 32 j + q
+    return part * 128 + (slot % 4 * kParts + p) * 4 + slot / 4;
+}
+
+struct SplitArgs {
+    const uint8_t *x;
+    const int32_t *idx;
+    uint8_t *codes;      // [parts, 64, H / 2]
+    uint32_t *scales;    // [ceil(H / 128), parts, 32, 4]
+    int S, K, E, H, parts;
+};
+
+// A warp takes 256 elements of a token and stores them for its K entries.
+__global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
+{
+    extern __shared__ int16_t lists[];
+    const int n = a.S * a.K;
+    Routing rt(lists, n, a.E);
+    const int tid = threadIdx.x, lane = tid & 31;
+    griddep_wait();
+    griddep_launch_dependents();
+    route<kThreads>(a.idx, n, a.E, kRows, rt);
+    const int chunks = (a.H + 255) / 256, words = (a.H + 127) / 128;
+    for (int u = blockIdx.x * (kThreads / 32) + (tid >> 5); u < a.S * chunks;
+         u += gridDim.x * (kThreads / 32)) {
+        const int s = u / chunks, c = u - s * chunks, at = c * 256 + lane * 8;
+        const bool in = at < a.H;
+        Split sp;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (in) v = __ldg(reinterpret_cast<const uint4 *>(a.x + ((int64_t)s * a.H + at) * 2));
+        const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            sp.v[2 * k] = __uint_as_float(q[k] << 16);
+            sp.v[2 * k + 1] = __uint_as_float(q[k] & 0xffff0000u);
+        }
+        sp.begin();
+        uint32_t code[kParts], word[kParts];
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+            code[p] = sp.next(p);
+            uint32_t b = (uint32_t)sp.scale(p);  // of four blocks, in every 16th lane
+            b |= __shfl_down_sync(0xffffffffu, b, 4) << 8;
+            word[p] = (b & 0xffffu) | __shfl_down_sync(0xffffffffu, b, 8) << 16;
+        }
+        const int w = 2 * c + (lane >> 4);
+        uint32_t *scales = a.scales + (int64_t)w * a.parts * 128;
+        for (int k = 0; k < a.K; ++k) {
+            const int place = rt.place[s * a.K + k];
+            if (place < 0) continue;
+            uint8_t *codes = a.codes + (int64_t)place * kParts * (a.H / 2) + at / 2;
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                if (in) *reinterpret_cast<uint32_t *>(codes + p * (a.H / 2)) = code[p];
+                if ((lane & 15) == 0 && w < words) scales[scale_place(place, p)] = word[p];
+            }
+        }
+    }
+}
+
+// --- the products -----------------------------------------------------------------
 
 struct LayerArgs {
-    const uint8_t *x;        // bf16 [S, H]
-    const int32_t *idx;      // [S, K]
-    const float *topk_w;     // [S, K]
-    const uint8_t *w;        // this launch's weights
-    float *h;                // [S K, F]
-    float *y;                // [S K, H]
-    uint32_t *arrived;       // [ceil(H / 32)] experts whose share of these columns is there
-    uint8_t *out;            // [S, H]
+    const int32_t *idx;
+    const float *topk_w;
+    uint8_t *h;           // MXFP4: codes [parts, 64, F / 2]; bf16 [parts, 32, F]
+    uint8_t *h_scales;    // MXFP4: [ceil(F / 128), parts, 32, 4, 4]
+    float *y;             // [n, H]
+    uint32_t *arrived;    // [ceil(H / 128), 4, S] experts whose share of these outputs is there
+    uint8_t *out;
     int S, K, E, H, F;
-    int rows;                // tokens of an expert taken at once
-    int pitch;               // bytes of a staged row of one warp
-    int out_f32;
+    int parts;            // that there is room for
+    int counters;
+    int stages;
+    int f32;
 };
 
-// How many rows of x or h, in so many parts each, the instruction's eight columns
-// hold, and the columns of one.
-template <int PARTS> struct Columns {
-    static constexpr int kStride = PARTS == 3 ? 4 : PARTS;
-    static constexpr int kRows = 8 / kStride;
+// The weights and the rows (of 4 entries, or 8; one of x for bf16), with MXFP4's
+// scales.
+struct LayerMaps {
+    CUtensorMap a, sa, b[2], sb;
 };
 
-__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                    uint32_t a3, uint32_t b0, uint32_t b1)
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
 {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
+__device__ __forceinline__ void copy_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y, int z)
 {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&v);
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+                 : "memory");
 }
 
-// Eight neighbouring values of a row of x or h as f32; zeros past the row.
-template <bool UP>
-__device__ __forceinline__ void load8(const LayerArgs &a, int entry, int k, int K, float (&f)[8])
+__device__ __forceinline__ void copy_2d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y)
 {
-    if (k >= K) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y, int z, int w)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void copy_5d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                        int y, int z, int w, int v)
+{
+    asm volatile("cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t scale_a, uint32_t scale_b, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(scale_a), "r"(scale_b), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t d, uint64_t src)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d), "l"(src) : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_u32(bar))
+                 : "memory");
+}
+
+// Shared-memory descriptors: rows of 128 bytes under the 128-byte swizzle, and
+// scales in rows of 16 bytes.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool rows)
+{
+    return ((uint64_t)(addr & 0x3ffff) >> 4) | (1ull << 16) |
+           ((uint64_t)((rows ? 1024 : 128) >> 4) << 32) | (1ull << 46) |
+           ((rows ? 2ull : 0ull) << 61);
+}
+
+// E2M1 operands, E8M0 scales; `half`: which two of a word's four scales.
+__device__ __forceinline__ uint32_t instr_mxf4(int n, int half)
+{
+    return ((uint32_t)(2 * half) << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
+           (1u << 23) | ((uint32_t)(kTile >> 4) << 24) | ((uint32_t)(2 * half) << 29);
+}
+
+// bf16 operands, f32 accumulator.
+__device__ __forceinline__ uint32_t instr_bf16(int n)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kTile >> 4) << 24);
+}
+
+struct Tile {
+    int e;        // expert
+    int m;        // tile of its weights
+    int part;     // of its entries
+    int row;      // first packed row
+    int rows;     // of them, 1 .. 8
+};
+
+// Tiles are numbered by part, then by the weights' tile, so that parts of one expert
+// read the same weights one after another; asked for in order.
+struct Walk {
+    const Routing &rt;
+    int tiles_m, at = 0;
+    __device__ Walk(const Routing &r, int m) : rt(r), tiles_m(m) {}
+    __device__ __forceinline__ Tile operator()(int t)
+    {
+        while (t >= rt.parts[at + 1] * tiles_m) ++at;
+        const int parts = rt.parts[at + 1] - rt.parts[at];
+        const int local = t - rt.parts[at] * tiles_m;
+        Tile r;
+        r.e = rt.hit[at];
+        r.m = local / parts;
+        r.part = rt.parts[at] + local - r.m * parts;
+        r.row = rt.first[at] + (local - r.m * parts) * kRows;
+        r.rows = min(kRows, rt.first[at + 1] - r.row);
+        return r;
+    }
+};
+
+struct Shared {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    volatile int stop;
+};
+
+// h of a tile, 64 outputs of up to 8 entries in `box`, as the rows of the next product.
+template <bool MX>
+__device__ __forceinline__ void store_h(const LayerArgs &a, const Tile &c, const float *box, int me)
+{
+    if constexpr (MX) {
+        // 4 threads a block, two blocks an entry
+        const int x = me >> 3 & 7, b = me >> 2 & 1, l = me & 3;
+        const int f0 = c.m * 64 + b * 32;
+        if (me >= 64) return;
+        Split sp;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-    } else if (UP) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(
-            a.x + ((int64_t)(entry / a.K) * K + k) * 2));
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        for (int k = 0; k < 8; ++k) sp.v[k] = x < c.rows ? box[x * 64 + b * 32 + l * 8 + k] : 0.0f;
+        sp.begin();
+        if (x >= c.rows || f0 >= a.F) return;
+        const int place = c.part * kRows + x;
+        uint8_t *codes = a.h + (int64_t)place * kParts * (a.F / 2) + f0 / 2 + l * 4;
+        uint8_t *scales = a.h_scales + (int64_t)(f0 / 128) * a.parts * 512 + f0 / 32 % 4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(u[i] << 16);
-            f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        for (int p = 0; p < kParts; ++p) {
+            *reinterpret_cast<uint32_t *>(codes + p * (a.F / 2)) = sp.next(p);
+            if (l == (p & 3)) {
+                uint8_t *to = scales + scale_place(place, p) * 4;
+                to[0] = (uint8_t)sp.scale(p);
+                // the end of the last word
+                if (f0 + 32 == a.F)
+                    for (int k = 1; k <= 3 - f0 / 32 % 4; ++k) to[k] = 0;
+            }
         }
     } else {
-        const float4 *p = reinterpret_cast<const float4 *>(a.h + (int64_t)entry * K + k);
-        const float4 u = __ldcg(p), v = __ldcg(p + 1);
-        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-        f[4] = v.x, f[5] = v.y, f[6] = v.z, f[7] = v.w;
-    }
-}
-
-// One warp's slice (elements from .. from + len of K) of up to `rows` entries.
-template <bool UP, int PARTS>
-__device__ void stage(const LayerArgs &a, const int16_t *entries, int rows, int from, int len,
-                      int K, uint8_t *to)
-{
-    const int lane = threadIdx.x & 31;
-    __syncwarp();
-    for (int r = 0; r < rows; ++r) {
-        const int entry = entries[r];
-        uint8_t *p = to + r * PARTS * a.pitch;
-        for (int k = lane * 8; k < len; k += 256) {
-            float f[8];
-            load8<UP>(a, entry, from + k, K, f);
+        // 16 threads an entry, four outputs each
+        const int x = me >> 4, f = c.m * 64 + (me & 15) * 4;
+        if (x >= c.rows || f >= a.F) return;
+        float v[4];
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part) {
-                uint32_t u[4];
+        for (int k = 0; k < 4; ++k) v[k] = box[x * 64 + (me & 15) * 4 + k];
+        const int64_t row = (int64_t)(c.part * kRows + x) * Form<false>::kColumns;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u[i] = pack_bf16(f[2 * i], f[2 * i + 1]);
-                    if (part + 1 < PARTS) {
-                        const float lo = __uint_as_float(u[i] << 16),
-                                    hi = __uint_as_float(u[i] & 0xffff0000u);
-                        // nothing is left of an infinity
-                        f[2 * i] = isinf(lo) ? 0.0f : f[2 * i] - lo;
-                        f[2 * i + 1] = isinf(hi) ? 0.0f : f[2 * i + 1] - hi;
-                    }
-                }
-                *reinterpret_cast<uint4 *>(p + part * a.pitch + k * 2) =
-                    make_uint4(u[0], u[1], u[2], u[3]);
+        for (int p = 0; p < Form<false>::kH; ++p) {
+            uint32_t u[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                u[k] = *reinterpret_cast<const uint32_t *>(&b);
+                const float lo = __low2float(b), hi = __high2float(b);
+                // nothing is left of an infinity
+                v[2 * k] = isinf(lo) ? 0.0f : v[2 * k] - lo;
+                v[2 * k + 1] = isinf(hi) ? 0.0f : v[2 * k + 1] - hi;
             }
+            st8(a.h + ((row + p) * a.F + f) * 2, make_uint2(u[0], u[1]));
         }
     }
-    __syncwarp();
 }
 
-// A place in the CTA's run of tiles: the next 64 bytes of each of a tile's rows.
-struct Cursor {
-    int item, pass, chunk;
-};
-
-template <bool UP, int PARTS, int NT>
-__global__ void __launch_bounds__(kThreads, 2) layer_kernel(LayerArgs a)
+template <bool MX, bool UP>
+__global__ void __launch_bounds__(kThreads, 2)
+layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
 {
-    using Co = Columns<PARTS>;
-    extern __shared__ __align__(128) uint8_t smem[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    using Fo = Form<MX>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    const int stages = a.stages;
+    float *box = reinterpret_cast<float *>(ring + stages * Fo::kStageBytes);  // [8][64]
     const int n = a.S * a.K;
-    // shared memory: staged rows, the warps' sums (twice), the routing
-    const int staged_rows = a.rows * PARTS;
-    uint8_t *mine = smem + warp * staged_rows * a.pitch;
-    float *sums = reinterpret_cast<float *>(smem + kWarps * staged_rows * a.pitch);
-    float *weights = sums + 2 * kWarps * kMaxRows * kTile;  // of the entries
-    Routing rt(weights + n, n, a.E);
-    __shared__ int s_last;
+    float *weights = box + kBoxBytes / 4;                       // [n]
+    int16_t *valid = reinterpret_cast<int16_t *>(weights + n);  // [S] experts of a token
+    Routing rt(valid + a.S, n, a.E);
+    __shared__ Shared sh;
 
-    const int K = UP ? a.H : a.F;                    // reduction
-    const int M = UP ? 2 * a.F : a.H;                // weight rows of an expert
-    const int per_tile = UP ? kTile / 2 : kTile;     // outputs of a tile
-    const int outputs = UP ? a.F : a.H;
-    const int tiles = (outputs + per_tile - 1) / per_tile;
-    const int row_bytes = K * 2;
-    const int chunks = (row_bytes + 63) / 64;
-    const int c0 = chunks * warp / kWarps, mc = chunks * (warp + 1) / kWarps - c0;
-    const int steps = max(mc, 1);                    // a warp without chunks takes part
-
-    if (UP) {
-        griddep_wait();
-        griddep_launch_dependents();
-        const int columns = (a.H + kTile - 1) / kTile;
-        for (int i = blockIdx.x * kThreads + tid; i < columns; i += gridDim.x * kThreads)
-            a.arrived[i] = 0;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 96) {
+        prefetch_map(&maps.a);
+        prefetch_map(&maps.b[0]);
+        if (MX || !UP) prefetch_map(&maps.b[1]);
+        if (MX) {
+            prefetch_map(&maps.sa);
+            prefetch_map(&maps.sb);
+        }
     }
-    // The second launch lists and begins to read its weights while the first one
-    // ends: what it reads until its wait was complete when that one began.
+    if (tid == 0) {
+        for (int i = 0; i < kMaxStages; ++i) {
+            mbar_init(&sh.full[i], 2);   // both operands
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.acc_full[i], 1);
+            mbar_init(&sh.acc_empty[i], 4);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.stop = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&sh.tmem)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_fence_before();
+    // The first launch waits for what came before the call.  The others do so later:
+    // topk_idx, topk_w and the experts' weights were complete when the first one began.
+    constexpr bool kFirst = UP && !MX;
+    if (kFirst) griddep_wait();
     if (!UP) load_weights(a.topk_w, n, weights);
-    route<kThreads>(a.idx, n, a.E, a.rows, rt);
-    const int64_t items = (int64_t)rt.hits * tiles;
-    const int begin = (int)(items * blockIdx.x / gridDim.x);
-    const int end = (int)(items * (blockIdx.x + 1) / gridDim.x);
-
-    auto advance = [&](Cursor &c) {
-        if (++c.chunk < steps) return false;
-        c.chunk = 0;
-        const int h = c.item / tiles;
-        if (++c.pass == rt.parts[h + 1] - rt.parts[h]) {
-            c.pass = 0;
-            ++c.item;
-        }
-        return true;
-    };
-
-    // --- loads ---
-    uint4 w[kDepth][4];     // rows g, g + 8 of both halves of the tile
-    Cursor ahead = {begin, 0, 0};
-    const uint8_t *from = nullptr;
-    uint32_t ok = 0;        // which of the four rows exist
-    const int64_t half = (int64_t)(UP ? a.F : kTile / 2) * row_bytes;  // between the halves
-    auto aim = [&] {
-        if (ahead.item >= end) return;
-        const int h = ahead.item / tiles, e = rt.hit[h];
-        const int row = (ahead.item - h * tiles) * per_tile + g;
-        ok = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = row + (i & 1) * 8 + (UP ? 0 : (i >> 1) * (kTile / 2));
-            if (r < outputs) ok |= 1u << i;
-        }
-        from = a.w + ((int64_t)e * M + row) * row_bytes + c0 * 64 + t * 16;
-    };
-    auto load = [&](int d) {
-        const int at = (c0 + ahead.chunk) * 64 + t * 16;
-        const bool in = ahead.item < end && ahead.chunk < mc && at < row_bytes;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            w[d][i] = make_uint4(0, 0, 0, 0);
-            if (in && (ok >> i & 1))
-                w[d][i] = ld_stream16(from + (i & 1) * 8 * (int64_t)row_bytes + (i >> 1) * half +
-                                      ahead.chunk * 64);
-        }
-        if (ahead.item < end && advance(ahead)) aim();
-    };
-    aim();
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d) load(d);
-
+    route<kThreads>(a.idx, n, a.E, kRows, rt);  // has barriers
     if (!UP) {
-        griddep_wait();  // h and the cleared counters
-        griddep_launch_dependents();
-        if (rt.hits == 0) {
-            for (int64_t i = (int64_t)blockIdx.x * kThreads + tid; i < (int64_t)a.S * a.H;
-                 i += (int64_t)gridDim.x * kThreads) {
-                if (a.out_f32) reinterpret_cast<float *>(a.out)[i] = 0.0f;
-                else reinterpret_cast<uint16_t *>(a.out)[i] = 0;
-            }
-            return;
+        for (int s = tid; s < a.S; s += kThreads) {
+            int k = 0;
+            for (int i = s * a.K; i < (s + 1) * a.K; ++i) k += rt.place[i] >= 0;
+            valid[s] = (int16_t)k;
         }
+        __syncthreads();
     }
-
-    // --- products ---
-    float acc[2][NT][4];
-    auto clear = [&] {
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] = 0.0f;
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int reduction = UP ? a.H : a.F, outputs = UP ? a.F : a.H;
+    const int per_tile = UP ? kTile / 2 : kTile;
+    const int tiles_m = (outputs + per_tile - 1) / per_tile;
+    const int tiles = rt.parts[rt.hits] * tiles_m;
+    const int blocks = (reduction + Fo::kK - 1) / Fo::kK;
+    // columns of a tile of so many entries: those of 4 or 8; rows of x as they are take 8,
+    // and 16 is the least there is
+    auto columns_of = [&](int rows) {
+        if (!MX && UP) return 16;
+        return rows > kRows / 2 ? kRows * Fo::kColumns : kRows / 2 * Fo::kColumns;
     };
-    clear();
-    Cursor now = {begin, 0, 0};
-    int staged = -1;                  // first row of what is staged
-    int first = 0, rows = 0, need = 0;  // of this visit
-    int turn = 0;
-    auto visit = [&] {
-        if (now.item >= end) return;
-        const int h = now.item / tiles;
-        first = rt.first[h] + now.pass * a.rows;
-        rows = min(a.rows, rt.first[h + 1] - first);
-        need = (rows + Co::kRows - 1) / Co::kRows;
-        if (first != staged)
-            stage<UP, PARTS>(a, rt.order + first, rows, c0 * kChunk, mc * kChunk, K, mine);
-        staged = first;
-    };
-    visit();
+    Walk walk(rt, tiles_m);
 
-    auto products = [&](int d) {
-        if (now.chunk >= mc) return;
-        const uint8_t *b0 = mine + now.chunk * 64 + t * 16;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j >= need) break;
-            // column g: part g % kStride of row g / kStride, or a column that is not used
-            const int row = j * Co::kRows + g / Co::kStride, part = g % Co::kStride;
-            uint4 b = make_uint4(0, 0, 0, 0);
-            if (row < rows && part < PARTS)
-                b = *reinterpret_cast<const uint4 *>(b0 + (row * PARTS + part) * a.pitch);
-            // The instruction cuts a sum's low bits off: after 100 of them an f32
-            // output is off by 1e-6.  Two at a time, added in f32, 2e-7.
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const uint4 u = w[d][2 * m], v = w[d][2 * m + 1];
-                float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                mma(c, u.x, v.x, u.y, v.y, b.x, b.y);
-                mma(c, u.z, v.z, u.w, v.w, b.z, b.w);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[m][j][i] += c[i];
+    if (warp == 0 || warp == 2) {
+        const bool is_weights = warp == 0;
+        if (!is_weights && !kFirst) griddep_wait();  // the rows
+        if (elect_one()) {
+            Ring r(stages);
+            int64_t j = 0;  // blocks copied
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const Tile c = walk(t);
+                const int cols = columns_of(c.rows);
+                for (int b = 0; b < blocks; ++b, ++j) {
+                    if (j >= stages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *stage = ring + r.at * Fo::kStageBytes;
+                    uint8_t *rows = stage + kCodesA, *scales = rows + Fo::kCodesB;
+                    uint64_t *bar = &sh.full[r.at];
+                    const int m = c.m * per_tile;
+                    if (is_weights) {
+                        mbar_arrive_expect_tx(bar, kCodesA + (MX ? kScales : 0));
+                        if (MX && UP) {
+                            // 64 gates and 64 ups: row 4 q + j of either in lane
+                            // 32 j + q, ups 16 lanes on
+                            copy_5d(stage, &maps.a, bar, b * 128, m / 4, 0, 0, c.e);
+                            copy_4d(scales, &maps.sa, bar, m, 0, 2 * b, c.e);
+                        } else if (MX) {
+                            copy_4d(stage, &maps.a, bar, b * 128, m / 4, 0, c.e);
+                            copy_3d(scales, &maps.sa, bar, m, 2 * b, c.e);
+                        } else if (UP) {
+                            // gates 8 i .. in lanes 16 i .., their ups 8 lanes on
+                            copy_5d(stage, &maps.a, bar, b * 64, 0, 0, m / 8, c.e);
+                        } else {
+                            copy_3d(stage, &maps.a, bar, b * 64, m, c.e);
+                        }
+                    } else if (!MX && UP) {
+                        mbar_arrive_expect_tx(bar, c.rows * 128);
+                        for (int x = 0; x < c.rows; ++x)
+                            copy_2d(rows + x * 128, &maps.b[0], bar, b * 64,
+                                    rt.order[c.row + x] / a.K);
+                    } else {
+                        mbar_arrive_expect_tx(bar, cols * 128 + (MX ? kScales : 0));
+                        copy_2d(rows, &maps.b[c.rows > kRows / 2], bar, b * (MX ? 128 : 64),
+                                c.part * (kRows * Fo::kColumns));
+                        if (MX) copy_2d(scales + kScales, &maps.sb, bar, c.part * 128, 2 * b);
+                    }
+                    r.next();
+                }
+            }
+            if (!ok) {
+                // leave no copy in flight
+                for (int64_t i = j > stages ? j - stages : 0; i < j; ++i)
+                    (void)wait_slow(&sh.full[i % stages], (uint32_t)(i / stages) & 1, nullptr);
             }
         }
-    };
-
-    // The warps' sums meet; a thread finishes one output.
-    auto finish = [&] {
-        float *to = sums + (turn * kWarps + warp) * kMaxRows * kTile;
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            if (j >= need) break;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                const float (&v)[4] = acc[m][j];
-                const int at = m * 16 + g;
-                if (PARTS == 1) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int row = j * 8 + 2 * t + (i & 1);
-                        if (row < rows) to[row * kTile + at + (i >> 1) * 8] = v[i];
+        __syncwarp();
+    } else if (warp == 1) {
+        // One thread issues.  A stage has its own columns of scales: the copy into it,
+        // which begins when the products that read it before are done, frees both.
+        if (elect_one()) {
+            Ring r(stages);
+            int i = 0;  // accumulators begun
+            bool ok = true;
+            for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+                const int cols = columns_of(walk(t).rows);
+                const uint32_t low = MX ? instr_mxf4(cols, 0) : instr_bf16(cols);
+                const uint32_t high = instr_mxf4(cols, 1);
+                uint32_t acc = 0;
+                for (int b = 0; b < blocks; ++b) {
+                    const bool fresh = b % kSumStages == 0;
+                    if (fresh) {
+                        if (b > 0) commit(&sh.acc_full[(i - 1) & 1]);
+                        if (i >= 2 &&
+                            !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        acc = tmem + (i & 1) * kAcc;
+                        ++i;
                     }
-                } else if (PARTS == 2) {
-                    const int row = j * 4 + t;
-                    if (row < rows) {
-                        to[row * kTile + at] = v[0] + v[1];
-                        to[row * kTile + at + 8] = v[2] + v[3];
+                    if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
+                        ok = false;
+                        break;
                     }
-                } else {  // columns 4 row .. 4 row + 2
-                    const float u0 = v[0] + v[1], u1 = v[2] + v[3];
-                    const float w0 = u0 + __shfl_xor_sync(0xffffffffu, u0, 1);
-                    const float w1 = u1 + __shfl_xor_sync(0xffffffffu, u1, 1);
-                    const int row = j * 2 + (t >> 1);
-                    if ((t & 1) == 0 && row < rows) {
-                        to[row * kTile + at] = w0;
-                        to[row * kTile + at + 8] = w1;
+                    const uint32_t stage = smem_u32(ring) + r.at * Fo::kStageBytes;
+                    tc_fence_after();
+                    const uint64_t da = desc_of(stage, true), db = da + (kCodesA >> 4);
+                    const int left = reduction - b * Fo::kK;  // a quarter of a stage a product
+                    if constexpr (MX) {
+                        const uint32_t sa = tmem + kScaleAt + (uint32_t)r.at * 16, sb = sa + 8;
+                        const uint64_t from_a = desc_of(stage + kCodesA + Fo::kCodesB, false);
+                        const uint64_t from_b = from_a + (kScales >> 4);
+                        copy_scales(sa, from_a);
+                        copy_scales(sb, from_b);
+                        mma_mxf4(acc, da, db, low, sa, sb, !fresh);
+                        if (left > 64) mma_mxf4(acc, da + 2, db + 2, high, sa, sb, true);
+                        if (left > 128) {
+                            copy_scales(sa + 4, from_a + 32);
+                            copy_scales(sb + 4, from_b + 32);
+                            mma_mxf4(acc, da + 4, db + 4, low, sa + 4, sb + 4, true);
+                            if (left > 192)
+                                mma_mxf4(acc, da + 6, db + 6, high, sa + 4, sb + 4, true);
+                        }
+                    } else {
+                        mma_bf16(acc, da, db, low, !fresh);
+                        if (left > 16) mma_bf16(acc, da + 2, db + 2, low, true);
+                        if (left > 32) mma_bf16(acc, da + 4, db + 4, low, true);
+                        if (left > 48) mma_bf16(acc, da + 6, db + 6, low, true);
                     }
+                    commit(&sh.empty[r.at]);
+                    r.next();
+                }
+                if (ok) commit(&sh.acc_full[(i - 1) & 1]);
+            }
+            commit(&sh.drain);  // nothing is issued after this
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        const int q = warp & 3, me = tid - 128;  // this warp's quarter; of 128 threads
+        auto join = [&] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        // whether all four warps go on: one that gave up must not leave the others
+        // at their next meeting
+        auto agree = [&](bool ok) {
+            uint32_t all;
+            asm volatile("{\n\t.reg .pred p, q;\n\t"
+                         "setp.ne.u32 p, %1, 0;\n\t"
+                         "bar.red.and.pred q, 1, 128, p;\n\t"
+                         "selp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(all)
+                         : "r"((uint32_t)ok)
+                         : "memory");
+            return all != 0;
+        };
+        if (!kFirst) griddep_wait();
+        griddep_launch_dependents();
+        if (UP) {
+            for (int i = blockIdx.x * 128 + me; i < a.counters; i += gridDim.x * 128)
+                a.arrived[i] = 0;
+        } else {
+            // tokens without an expert
+            for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
+                if (valid[s]) continue;
+                for (int i = me; i < a.H; i += 128) {
+                    if (a.f32) reinterpret_cast<float *>(a.out)[(int64_t)s * a.H + i] = 0.0f;
+                    else reinterpret_cast<uint16_t *>(a.out)[(int64_t)s * a.H + i] = 0;
                 }
             }
         }
-        clear();
-        __syncthreads();
-        const float *p = sums + turn * kWarps * kMaxRows * kTile;
-        turn ^= 1;
-        const int o0 = now.item % tiles * per_tile;
-        const int at = tid % per_tile, row = tid / per_tile;
-        if (row < rows && o0 + at < outputs) {
-            const int entry = rt.order[first + row];
-            float v[2] = {0.0f, 0.0f};
+        int i = 0;  // accumulators read
+        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+            const Tile c = walk(t);
+            float sum[kRows];
 #pragma unroll
-            for (int k = 0; k < kWarps; ++k) {
-                v[0] += p[(k * kMaxRows + row) * kTile + at];
-                if (UP) v[1] += p[(k * kMaxRows + row) * kTile + kTile / 2 + at];
+            for (int x = 0; x < kRows; ++x) sum[x] = 0.0f;
+            bool ok = true;
+            for (int b = 0; b < blocks && ok; b += kSumStages, ++i) {
+                const int buf = i & 1;
+                ok = agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAcc;
+                if constexpr (MX) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        if (j * 4 >= c.rows) break;
+                        uint32_t v[32];  // column 8 x + p: row p of entry 4 j + x
+                        tmem_load(acc + j * 32, v);
+                        tmem_wait(v);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            float f = __uint_as_float(v[8 * x + 7]);  // the small ones first
+#pragma unroll
+                            for (int p = 6; p >= 0; --p) f += __uint_as_float(v[8 * x + p]);
+                            sum[4 * j + x] += f;
+                        }
+                    }
+                } else if constexpr (UP) {
+                    uint32_t v[16];
+                    tmem_load(acc, v);
+                    tmem_wait(v);
+#pragma unroll
+                    for (int x = 0; x < kRows; ++x) sum[x] += __uint_as_float(v[x]);
+                } else {
+                    uint32_t v[32];  // column 4 x + p
+                    tmem_load(acc, v);
+                    tmem_wait(v);
+#pragma unroll
+                    for (int x = 0; x < kRows; ++x)
+                        sum[x] += (__uint_as_float(v[4 * x + 2]) + __uint_as_float(v[4 * x + 1])) +
+                                  __uint_as_float(v[4 * x]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
             }
-            if (UP) a.h[(int64_t)entry * a.F + o0 + at] = v[0] / (1.0f + expf(-v[0])) * v[1];
-            else a.y[(int64_t)entry * a.H + o0 + at] = v[0];
-        }
-    };
-
-    // The last expert's CTA for 32 columns sums them over each token's entries.
-    auto combine = [&](int item) {
-        const int tile = item % tiles, o = tile * kTile + lane;
-        __syncthreads();
-        if (tid == 0) {
-            __threadfence();
-            s_last = atomicAdd(a.arrived + tile, 1u) == (uint32_t)rt.hits - 1;
-            __threadfence();
-        }
-        __syncthreads();
-        if (!s_last || o >= a.H) return;
-        // a token a warp where that is enough
-        const int each = a.S > kWarps ? kFewTokens : 1;
-        for (int s0 = warp * each; s0 < a.S; s0 += kWarps * each) {
-            int s[kFewTokens];
+            if (!ok) break;
+            if constexpr (UP) {
+                // the gate of an output here, its up 16 (or 8) lanes on
+                const bool gate = MX ? lane < 16 : (lane & 8) == 0;
+                const int f = MX ? 4 * lane + q : 16 * q + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
-            for (int j = 0; j < kFewTokens; ++j) s[j] = min(s0 + j, a.S - 1);
-            if (each == 1)
-                few_combine<1>(a.y, weights, rt.place, a.K, a.H, o, s, 1, a.out, a.out_f32);
-            else
-                few_combine<kFewTokens>(a.y, weights, rt.place, a.K, a.H, o, s, a.S - s0, a.out,
-                                        a.out_f32);
-        }
-    };
-
-    while (now.item < end) {
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-            if (now.item >= end) break;
-            products(d);
-            load(d);
-            if (now.chunk + 1 == steps) {
-                finish();
-                const int item = now.item;
-                advance(now);
-                if (!UP && now.item != item) combine(item);
-                visit();
+                for (int x = 0; x < kRows; ++x) {
+                    const float up = __shfl_down_sync(0xffffffffu, sum[x], MX ? 16 : 8);
+                    if (gate && x < c.rows)
+                        box[x * 64 + f] = sum[x] / (1.0f + expf(-sum[x])) * up;
+                }
+                join();
+                store_h<MX>(a, c, box, me);
+                join();  // the box has been read
             } else {
-                ++now.chunk;
+                // Each warp stores its outputs and counts them for itself: the warps
+                // need not meet.  A token's outputs are summed by the warp that brings the
+                // last of its experts, which spreads the sums over the call: summed for all
+                // 32 tokens by the last expert's they took 55 us at its end.
+                const int o = c.m * kTile + (MX ? 4 * lane + q : 32 * q + lane);
+                if (o < a.H)
+#pragma unroll
+                    for (int x = 0; x < kRows; ++x)
+                        if (x < c.rows) a.y[(int64_t)rt.order[c.row + x] * a.H + o] = sum[x];
+                __syncwarp();
+                int token = 0;
+                bool last = false;
+                __threadfence();
+                if (lane < c.rows) {
+                    token = rt.order[c.row + lane] / a.K;
+                    last = atomicAdd(a.arrived + (c.m * 4 + q) * a.S + token, 1u) + 1 ==
+                           (uint32_t)valid[token];
+                }
+                uint32_t ready = __ballot_sync(0xffffffffu, last);
+                if (ready) __threadfence();
+                while (ready) {
+                    int s[kTokens], count = 0, from = 0;
+#pragma unroll
+                    for (int j = 0; j < kTokens; ++j) {
+                        if (ready) {
+                            from = __ffs(ready) - 1;
+                            ready &= ready - 1;
+                            ++count;
+                        }
+                        s[j] = __shfl_sync(0xffffffffu, token, from);
+                    }
+                    if (o >= a.H) continue;
+                    if (count == 1)
+                        sum_entries<1>(a.y, weights, rt.place, a.K, a.H, o, s, 1, a.out, a.f32);
+                    else
+                        sum_entries<kTokens>(a.y, weights, rt.place, a.K, a.H, o, s, count, a.out,
+                                             a.f32);
+                }
             }
         }
     }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        (void)wait_slow(&sh.drain, 0, nullptr);  // the last matrix instruction
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kTmemCols));
+    }
+    if (tid == 0 && sh.stop) atomicOr(&g_layer_error, kErrExpertTimeout);
 }
 
 // --- host ----------------------------------------------------------------------
 
-template <bool UP, int PARTS, int NT> int launch_layer(LayerArgs a, cudaStream_t stream)
+int64_t round_up(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
+
+struct Shape {
+    int rank;
+    cuuint64_t dims[5], strides[4];   // strides of all but the innermost, in bytes
+    cuuint32_t box[5];
+};
+
+cudaError_t encode(CUtensorMap *map, const void *base, CUtensorMapDataType type, const Shape &s)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint32_t step[5] = {1, 1, 1, 1, 1};
+    const bool words = type == CU_TENSOR_MAP_DATA_TYPE_UINT32;  // scales
+    const CUresult r =
+        fn(map, type, s.rank, const_cast<void *>(base), s.dims, s.strides, s.box, step,
+           CU_TENSOR_MAP_INTERLEAVE_NONE,
+           words ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr CUtensorMapDataType kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+constexpr CUtensorMapDataType kWords = CU_TENSOR_MAP_DATA_TYPE_UINT32;
+constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+
+template <bool MX, bool UP>
+int launch_layer(const LayerMaps &maps, LayerArgs a, cudaStream_t stream)
 {
     static KernelCache kc;
-    auto kernel = layer_kernel<UP, PARTS, NT>;
-    const int K = UP ? a.H : a.F, n = a.S * a.K;
-    const int chunks = (K * 2 + 63) / 64;
-    const int mine = (chunks + kWarps - 1) / kWarps;  // of one warp
-    // neighbouring staged rows begin in other banks
-    a.pitch = mine * 64 + (mine % 2 ? 0 : 64);
-    const int row = kWarps * PARTS * a.pitch;
-    int rows = kStageBudget / row;
-    const int most = NT * Columns<PARTS>::kRows < kMaxRows ? NT * Columns<PARTS>::kRows : kMaxRows;
-    if (rows > most) rows = most;
-    if (rows > a.S) rows = a.S;  // more only where a token has an expert twice
-    a.rows = rows < 1 ? 1 : rows;
-    const size_t smem = (size_t)a.rows * row + 2 * kWarps * kMaxRows * kTile * 4 + n * 4 +
-                        Routing::bytes(n, a.E);
-    int per_sm = 0;
-    cudaError_t e = prepare_kernel(kernel, smem, kThreads, kc, &per_sm);
+    constexpr int kStageBytes = Form<MX>::kStageBytes;
+    const int n = a.S * a.K;
+    const size_t rest = 1024 + kBoxBytes + n * 4 + a.S * 2 + Routing::bytes(n, a.E);
+    // Two CTAs of an SM have four or five stages each; where the lists leave less, one
+    // CTA has more.
+    const int least = MX ? 4 : 5;
+    a.stages = (int)((kSmem - rest) / kStageBytes);
+    const int ctas = a.stages < least ? 1 : 2;
+    if (ctas == 1) a.stages = MX ? 7 : 9;
+    const size_t smem = rest + (size_t)a.stages * kStageBytes;
+    cudaError_t e = prepare_kernel(layer_kernel<MX, UP>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess) {
         const int per_tile = UP ? kTile / 2 : kTile;
-        const int64_t tiles = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
-        const int64_t items = tiles * (n < a.E ? n : a.E);
-        const int64_t most_ctas = (int64_t)sm_count() * (per_sm < 1 ? 1 : per_sm);
-        e = launch_pdl(kernel, dim3((unsigned)(items < most_ctas ? items : most_ctas)),
-                       dim3(kThreads), smem, stream, a);
+        const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
+        const int64_t most = tiles_m * a.parts, room = (int64_t)sm_count() * ctas;
+        e = launch_pdl(layer_kernel<MX, UP>, dim3((unsigned)(most < room ? most : room)),
+                       dim3(kThreads), smem, stream, maps, a);
     }
     if (e != cudaSuccess) {
         set_cuda_error(e);
@@ -420,45 +979,133 @@ template <bool UP, int PARTS, int NT> int launch_layer(LayerArgs a, cudaStream_t
     return check_launch();
 }
 
-// The workspace: y, h and the counters.
+// Parts of n entries: one for every eight of an expert and one for what is left.
+int64_t most_parts(int64_t n, int64_t E) { return n < E + n / kRows ? n : E + n / kRows; }
+
+// The workspace: x and h as rows of the products, y, and the counters.
 struct Places {
-    int64_t h, arrived, bytes;
-    Places(int64_t n, int64_t H, int64_t F)
+    int64_t x, x_scales, h, h_scales, y, arrived, bytes;
+    Places(bool mx, int64_t S, int64_t K, int64_t E, int64_t H, int64_t F)
     {
-        h = round_up(n * H * 4, 256);
-        arrived = h + round_up(n * F * 4, 256);
-        bytes = arrived + round_up((H + kTile - 1) / kTile * 4, 256);
+        const int64_t n = S * K, parts = most_parts(n, E);
+        int64_t at = 0;
+        auto take = [&](int64_t size) {
+            const int64_t p = at;
+            at += round_up(size, 256);
+            return p;
+        };
+        x = take(mx ? parts * kRows * kParts * H / 2 : 0);
+        x_scales = take(mx ? (H + 127) / 128 * parts * 512 : 0);
+        h = take(parts * kRows * (mx ? kParts * F / 2 : Form<false>::kColumns * F * 2));
+        h_scales = take(mx ? (F + 127) / 128 * parts * 512 : 0);
+        y = take(n * H * 4);
+        arrived = take(counters(S, H) * 4);
+        bytes = at;
     }
+    static int64_t counters(int64_t S, int64_t H) { return (H + kTile - 1) / kTile * 4 * S; }
 };
 
-int layer_bf16(const LayerCall &c, cudaStream_t stream)
+struct LayerCall {
+    const uint8_t *x, *up, *up_scales, *down, *down_scales;
+    uint8_t *workspace;
+};
+
+// Parts of 64 rows of D elements as the other operand of MXFP4 weights.
+cudaError_t encode_mx_rows(LayerMaps &m, const uint8_t *codes, const uint8_t *scales, int parts,
+                           int D)
 {
-    const Places at(c.S * c.K, c.H, c.F);
-    LayerArgs a = {};
-    a.x = c.x;
-    a.idx = c.idx;
-    a.topk_w = c.topk_w;
-    a.w = c.up;
-    a.y = reinterpret_cast<float *>(c.workspace);
-    a.h = reinterpret_cast<float *>(c.workspace + at.h);
+    const cuuint64_t row = D / 2, P = parts, words = (D + 127) / 128;
+    constexpr cuuint32_t kCols = kRows * kParts;
+    cudaError_t e = cudaSuccess;
+    for (cuuint32_t i = 0; i < 2 && e == cudaSuccess; ++i)
+        e = encode(&m.b[i], codes, kBytes, {2, {row, P * kCols}, {row}, {128, kCols / 2 * (i + 1)}});
+    if (e != cudaSuccess) return e;
+    return encode(&m.sb, scales, kWords, {2, {P * 128, words}, {P * 512}, {128, 2}});
+}
+
+int layer_mxfp4(const LayerCall &c, LayerArgs a, cudaStream_t stream)
+{
+    const Places at(true, a.S, a.K, a.E, a.H, a.F);
+    uint8_t *ws = c.workspace;
+    a.h = ws + at.h;
+    a.h_scales = ws + at.h_scales;
+    a.y = reinterpret_cast<float *>(ws + at.y);
+    a.arrived = reinterpret_cast<uint32_t *>(ws + at.arrived);
+    LayerMaps up = {}, down = {};
+    const cuuint64_t E = a.E, H = a.H, F = a.F;
+    const cuuint64_t up_row = H / 2, up_words = (H + 127) / 128;
+    const cuuint64_t down_row = F / 2, down_words = (F + 127) / 128;
+    // gates and ups as two runs of F rows
+    cudaError_t e = encode(&up.a, c.up, kBytes,
+                           {5,
+                            {up_row, F / 4, 2, 4, E},
+                            {4 * up_row, F * up_row, up_row, 2 * F * up_row},
+                            {128, 16, 2, 4, 1}});
+    if (e == cudaSuccess)
+        e = encode(&up.sa, c.up_scales, kWords,
+                   {4, {F, 2, up_words, E}, {F * 4, 2 * F * 4, up_words * 2 * F * 4}, {64, 2, 2, 1}});
+    if (e == cudaSuccess) e = encode_mx_rows(up, ws + at.x, ws + at.x_scales, a.parts, a.H);
+    if (e == cudaSuccess)
+        e = encode(&down.a, c.down, kBytes,
+                   {4, {down_row, H / 4, 4, E}, {4 * down_row, down_row, H * down_row}, {128, 32, 4, 1}});
+    if (e == cudaSuccess)
+        e = encode(&down.sa, c.down_scales, kWords,
+                   {3, {H, down_words, E}, {H * 4, down_words * H * 4}, {kTile, 2, 1}});
+    if (e == cudaSuccess) e = encode_mx_rows(down, a.h, a.h_scales, a.parts, a.F);
+    static KernelCache kc;
+    const size_t smem = Routing::bytes(a.S * a.K, a.E);
+    if (e == cudaSuccess) e = prepare_kernel(split_kernel, smem, kThreads, kc, nullptr);
+    if (e == cudaSuccess) {
+        const SplitArgs s = {c.x, a.idx, ws + at.x, reinterpret_cast<uint32_t *>(ws + at.x_scales),
+                             a.S, a.K, a.E, a.H, a.parts};
+        const int64_t units = (int64_t)a.S * ((a.H + 255) / 256), most = 2 * sm_count();
+        const int64_t grid = (units + kThreads / 32 - 1) / (kThreads / 32);
+        e = launch_pdl(split_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(kThreads),
+                       smem, stream, s);
+    }
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    int r = check_launch();
+    if (r == MOE_OK) r = launch_layer<true, true>(up, a, stream);
+    if (r == MOE_OK) r = launch_layer<true, false>(down, a, stream);
+    return r;
+}
+
+int layer_bf16(const LayerCall &c, LayerArgs a, cudaStream_t stream)
+{
+    const Places at(false, a.S, a.K, a.E, a.H, a.F);
+    a.h = c.workspace + at.h;
+    a.y = reinterpret_cast<float *>(c.workspace + at.y);
     a.arrived = reinterpret_cast<uint32_t *>(c.workspace + at.arrived);
-    a.out = c.out;
-    a.S = c.S;
-    a.K = c.K;
-    a.E = c.E;
-    a.H = c.H;
-    a.F = c.F;
-    a.out_f32 = c.f32;
-    const int r = launch_layer<true, 1, 1>(a, stream);
-    if (r != MOE_OK) return r;
-    a.w = c.down;
-    return c.f32 ? launch_layer<false, 3, 4>(a, stream) : launch_layer<false, 2, 2>(a, stream);
+    LayerMaps up = {}, down = {};
+    const cuuint64_t E = a.E, H = a.H, F = a.F, P = a.parts;
+    constexpr cuuint32_t kCols = kRows * Form<false>::kColumns;
+    // gates and ups as two runs of F rows, eight of either by turns
+    cudaError_t e = encode(&up.a, c.up, kBf16,
+                           {5,
+                            {H, 8, 2, F / 8, E},
+                            {H * 2, F * H * 2, 8 * H * 2, 2 * F * H * 2},
+                            {64, 8, 2, 8, 1}});
+    if (e == cudaSuccess)
+        e = encode(&up.b[0], c.x, kBf16, {2, {H, (cuuint64_t)a.S}, {H * 2}, {64, 1}});
+    if (e == cudaSuccess)
+        e = encode(&down.a, c.down, kBf16, {3, {F, H, E}, {F * 2, H * F * 2}, {64, kTile, 1}});
+    for (cuuint32_t i = 0; i < 2 && e == cudaSuccess; ++i)
+        e = encode(&down.b[i], a.h, kBf16, {2, {F, P * kCols}, {F * 2}, {64, kCols / 2 * (i + 1)}});
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    const int r = launch_layer<false, true>(up, a, stream);
+    return r == MOE_OK ? launch_layer<false, false>(down, a, stream) : r;
 }
 
 bool in_range(int64_t S, int64_t H, int K, int E, int64_t F)
 {
-    return S >= 0 && K >= 1 && K <= 32 && E >= 1 && E <= kFewExperts && H >= 1 && F >= 1 &&
-           H <= kFewWidth && F <= kFewWidth && S <= kFewEntries && S * K <= kFewEntries;
+    return S >= 0 && K >= 1 && K <= 32 && E >= 1 && E <= kMaxExperts && H >= 1 && F >= 1 &&
+           H <= kMaxWidth && F <= kMaxWidth && S <= kMaxEntries && S * K <= kMaxEntries;
 }
 
 } // namespace
@@ -469,9 +1116,8 @@ using namespace moe;
 MOE_EXPORT size_t moe_expert_layer_workspace_size(int64_t S, int64_t H, int K, int E, int64_t F,
                                                   int w_dtype)
 {
-    if (!in_range(S, H, K, E, F)) return 0;
-    if (w_dtype == MOE_MXFP4) return layer_mxfp4_workspace(S, K, E, H, F);
-    return w_dtype == MOE_BF16 ? (size_t)Places(S * K, H, F).bytes : 0;
+    if (!in_range(S, H, K, E, F) || (w_dtype != MOE_BF16 && w_dtype != MOE_MXFP4)) return 0;
+    return (size_t)Places(w_dtype == MOE_MXFP4, S, K, E, H, F).bytes;
 }
 
 MOE_EXPORT int moe_expert_layer(const void *x, int64_t S, int64_t H, const int32_t *topk_idx,
@@ -494,20 +1140,34 @@ MOE_EXPORT int moe_expert_layer(const void *x, int64_t S, int64_t H, const int32
         !aligned16(out) || !aligned16(workspace) ||
         (mx && (!aligned16(up_scales) || !aligned16(down_scales))))
         return MOE_EALIGN;
+    LayerArgs a = {};
+    a.idx = topk_idx;
+    a.topk_w = topk_w;
+    a.out = static_cast<uint8_t *>(out);
+    a.S = (int)S;
+    a.K = K;
+    a.E = E;
+    a.H = (int)H;
+    a.F = (int)F;
+    a.parts = (int)most_parts(S * K, E);
+    a.counters = (int)Places::counters(S, H);
+    a.f32 = f32;
     const LayerCall c = {static_cast<const uint8_t *>(x),
-                         topk_idx,
-                         topk_w,
                          static_cast<const uint8_t *>(w_up),
                          up_scales,
                          static_cast<const uint8_t *>(w_down),
                          down_scales,
-                         static_cast<uint8_t *>(out),
-                         static_cast<uint8_t *>(workspace),
-                         (int)S,
-                         K,
-                         E,
-                         (int)H,
-                         (int)F,
-                         f32};
-    return mx ? layer_mxfp4(c, (cudaStream_t)stream) : layer_bf16(c, (cudaStream_t)stream);
+                         static_cast<uint8_t *>(workspace)};
+    return mx ? layer_mxfp4(c, a, (cudaStream_t)stream) : layer_bf16(c, a, (cudaStream_t)stream);
 }
+
+namespace moe {
+// Reads and clears this file's device error bits.
+cudaError_t read_layer_errors(uint32_t *flags)
+{
+    uint32_t zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(flags, g_layer_error, sizeof(uint32_t));
+    if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_layer_error, &zero, sizeof(uint32_t));
+    return e;
+}
+} // namespace moe

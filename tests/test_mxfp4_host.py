@@ -137,7 +137,7 @@ def test_layer_validation(L):
         assert f(**bad) == EALIGN, bad
     assert f(S=0) == OK
     need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32, 0)
-    assert need == 1024 + 512 + 256
+    assert need == 4 * 32 * 64 + 1024 + 256   # four parts of 32 rows
     assert f(bytes=need - 1) == EINVAL
     need = L.moe_expert_layer_workspace_size(2, 64, 2, 8, 32, 3)
     assert need == 4 * 64 * 32 + 4 * 512 + 4 * 64 * 16 + 4 * 512 + 1024 + 256   # four parts of 64 rows
