@@ -55,26 +55,21 @@ constexpr int kTile = 128;           // weight rows of a tile
 constexpr int kCodesA = kTile * 128; // of weights in a stage: 128 bytes of each row
 constexpr int kScales = 2 * 512;     // of 128 rows in a stage, or places for them
 constexpr int kMaxStages = 10;
-constexpr int kAcc = 64;             // TMEM columns of an accumulator
-constexpr int kScaleAt = 2 * kAcc;   // first column of the scales
+constexpr int kScaleAt = 128;        // first TMEM column of the scales, after the accumulators
 constexpr int kTmemCols = 256;       // so that two CTAs fit an SM
 constexpr int kSmem = 115712;        // of shared memory, likewise
 constexpr int kBoxBytes = kRows * kTile / 2 * 4;  // h of a tile
-// The tensor core cuts a sum's low bits off at each step; 48 of them leave less than
-// 1e-6, and the sums of so many stages are added in f32.
-constexpr int kSumStages = 12;
-
 // What depends on the weights' type: elements of a stage, rows that stand for one of h
 // and the columns they take (one of x takes as many with MXFP4, one with bf16), bytes of
-// the rows in a stage.
+// the rows in a stage, and accumulators.
 template <bool MX> struct Form;
 template <> struct Form<true> {
-    static constexpr int kK = 256, kH = 8, kColumns = 8;
+    static constexpr int kK = 256, kH = 8, kColumns = 8, kAccs = 2;
     static constexpr int kCodesB = kRows * kColumns * 128;
     static constexpr int kStageBytes = kCodesA + kCodesB + 2 * kScales;
 };
 template <> struct Form<false> {
-    static constexpr int kK = 64, kH = 3, kColumns = 4;
+    static constexpr int kK = 64, kH = 3, kColumns = 4, kAccs = 4;
     static constexpr int kCodesB = kRows * kColumns * 128;
     static constexpr int kStageBytes = kCodesA + kCodesB;
 };
@@ -387,6 +382,7 @@ struct LayerArgs {
     int parts;            // that there is room for
     int counters;
     int stages;
+    int sum_stages;       // that are summed in tensor memory, the rest in registers
     int f32;
 };
 
@@ -526,7 +522,7 @@ struct Walk {
 
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t acc_full[2], acc_empty[2], drain;
+    uint64_t acc_full[4], acc_empty[4], drain;
     uint32_t tmem;
     volatile int stop;
 };
@@ -548,7 +544,7 @@ __device__ __forceinline__ void store_h(const LayerArgs &a, const Tile &c, const
         const int place = c.part * kRows + x;
         uint8_t *codes = a.h + (int64_t)place * kParts * (a.F / 2) + f0 / 2 + l * 4;
         uint8_t *scales = a.h_scales + (int64_t)(f0 / 128) * a.parts * 512 + f0 / 32 % 4;
-#pragma unroll
+#pragma unroll 1
         for (int p = 0; p < kParts; ++p) {
             *reinterpret_cast<uint32_t *>(codes + p * (a.F / 2)) = sp.next(p);
             if (l == (p & 3)) {
@@ -589,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
 {
     using Fo = Form<MX>;
+    constexpr int kAccs = Fo::kAccs, kAcc = kRows * Fo::kColumns;  // columns of one
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const int stages = a.stages;
@@ -614,7 +611,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
             mbar_init(&sh.full[i], 2);   // both operands
             mbar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&sh.acc_full[i], 1);
             mbar_init(&sh.acc_empty[i], 4);
         }
@@ -727,17 +724,20 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 const uint32_t low = MX ? instr_mxf4(cols, 0) : instr_bf16(cols);
                 const uint32_t high = instr_mxf4(cols, 1);
                 uint32_t acc = 0;
+                int next = 0;  // first block of the next accumulator
                 for (int b = 0; b < blocks; ++b) {
-                    const bool fresh = b % kSumStages == 0;
+                    const bool fresh = b == next;  // a division here costs 3 % of a call
                     if (fresh) {
-                        if (b > 0) commit(&sh.acc_full[(i - 1) & 1]);
-                        if (i >= 2 &&
-                            !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop)) {
+                        next += a.sum_stages;
+                        if (b > 0) commit(&sh.acc_full[(i - 1) % kAccs]);
+                        const int at = i % kAccs;
+                        if (i >= kAccs &&
+                            !wait(&sh.acc_empty[at], (uint32_t)(i / kAccs - 1) & 1, &sh.stop)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        acc = tmem + (i & 1) * kAcc;
+                        acc = tmem + at * kAcc;
                         ++i;
                     }
                     if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
@@ -772,7 +772,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                     commit(&sh.empty[r.at]);
                     r.next();
                 }
-                if (ok) commit(&sh.acc_full[(i - 1) & 1]);
+                if (ok) commit(&sh.acc_full[(i - 1) % kAccs]);
             }
             commit(&sh.drain);  // nothing is issued after this
         }
@@ -815,9 +815,9 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
 #pragma unroll
             for (int x = 0; x < kRows; ++x) sum[x] = 0.0f;
             bool ok = true;
-            for (int b = 0; b < blocks && ok; b += kSumStages, ++i) {
-                const int buf = i & 1;
-                ok = agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop));
+            for (int b = 0; b < blocks && ok; b += a.sum_stages, ++i) {
+                const int buf = i % kAccs;
+                ok = wait(&sh.acc_full[buf], (uint32_t)(i / kAccs) & 1, &sh.stop);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAcc;
@@ -855,6 +855,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
             }
+            if (UP) ok = agree(ok);
             if (!ok) break;
             if constexpr (UP) {
                 // the gate of an output here, its up 16 (or 8) lanes on
@@ -957,18 +958,20 @@ int launch_layer(const LayerMaps &maps, LayerArgs a, cudaStream_t stream)
     constexpr int kStageBytes = Form<MX>::kStageBytes;
     const int n = a.S * a.K;
     const size_t rest = 1024 + kBoxBytes + n * 4 + a.S * 2 + Routing::bytes(n, a.E);
-    // Two CTAs of an SM have four or five stages each; where the lists leave less, one
-    // CTA has more.
+    const int per_tile = UP ? kTile / 2 : kTile;
+    const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
+    const int64_t most = tiles_m * a.parts, sms = sm_count();
+    // Two CTAs of an SM have four or five stages each.  Where the lists leave less, or
+    // there is no work for two, one CTA has more of them (5 tokens of 24 experts, 1416,
+    // 520, bf16: 21.1 -> 19.1 us).
     const int least = MX ? 4 : 5;
     a.stages = (int)((kSmem - rest) / kStageBytes);
-    const int ctas = a.stages < least ? 1 : 2;
+    const int ctas = a.stages < least || most <= sms ? 1 : 2;
     if (ctas == 1) a.stages = MX ? 7 : 9;
     const size_t smem = rest + (size_t)a.stages * kStageBytes;
     cudaError_t e = prepare_kernel(layer_kernel<MX, UP>, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess) {
-        const int per_tile = UP ? kTile / 2 : kTile;
-        const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
-        const int64_t most = tiles_m * a.parts, room = (int64_t)sm_count() * ctas;
+        const int64_t room = sms * ctas;
         e = launch_pdl(layer_kernel<MX, UP>, dim3((unsigned)(most < room ? most : room)),
                        dim3(kThreads), smem, stream, maps, a);
     }
@@ -1029,6 +1032,7 @@ int layer_mxfp4(const LayerCall &c, LayerArgs a, cudaStream_t stream)
     uint8_t *ws = c.workspace;
     a.h = ws + at.h;
     a.h_scales = ws + at.h_scales;
+    a.sum_stages = kMaxWidth / Form<true>::kK;
     a.y = reinterpret_cast<float *>(ws + at.y);
     a.arrived = reinterpret_cast<uint32_t *>(ws + at.arrived);
     LayerMaps up = {}, down = {};
@@ -1098,6 +1102,10 @@ int layer_bf16(const LayerCall &c, LayerArgs a, cudaStream_t stream)
         set_cuda_error(e);
         return MOE_ECUDA;
     }
+    // The tensor core cuts a sum's low bits off at each step of 16: f32 outputs are off
+    // by 2e-6 after 48 of them and 4e-7 after 8, for 4 % of time (one token of 8 experts,
+    // 6144, 2048: 95 and 99 us).  Products of E2M1 lose nothing.
+    a.sum_stages = a.f32 ? 2 : 12;
     const int r = launch_layer<false, true>(up, a, stream);
     return r == MOE_OK ? launch_layer<false, false>(down, a, stream) : r;
 }
