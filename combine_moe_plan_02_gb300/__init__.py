@@ -607,35 +607,46 @@ class MxFp4(NamedTuple):
         return torch.Size((*self.codes.shape[:-1], 2 * self.codes.shape[-1]))
 
 
-_U8 = torch.uint8
+_U8, _BF16, _F32 = torch.uint8, torch.bfloat16, torch.float32
+_device_of, _contiguous, _address = (torch.Tensor.get_device, torch.Tensor.is_contiguous,
+                                     torch.Tensor.data_ptr)
 
 
-def _check_mx(name: str, q: MxFp4, dims: Sequence[int] = (2, 3)):
-    """Raises unless codes and scales are what the kernels read; (groups, rows,
-    D) of the values."""
-    codes, scales = q
+def _pointers(*tensors: torch.Tensor):
+    """The addresses of contiguous tensors on one CUDA device (one attribute of
+    all at a time costs the host half of what one tensor at a time does)."""
+    devices = set(map(_device_of, tensors))
+    if len(devices) != 1 or -1 in devices:
+        raise ValueError("tensors must live on one CUDA device")
+    if not all(map(_contiguous, tensors)):
+        raise ValueError("tensors must be contiguous")
+    return map(_address, tensors)
+
+
+def _check_mx(name: str, codes: torch.Tensor, scales: torch.Tensor):
+    """Raises unless codes and scales are what the kernels read; the shape of the
+    values."""
     if codes.dtype is not _U8 or scales.dtype is not _U8:
         raise TypeError(f"{name} must have uint8 codes and scales")
     shape = codes.shape
-    n = len(shape)
-    if n not in dims or shape[-1] % 16:
-        raise ValueError(f"{name} must hold rows of a multiple of 32 elements")
-    half, rows = shape[-1], shape[-2]
-    words = -(-half // 64)
-    if scales.shape != ((words, rows, 4) if n == 2 else (shape[0], words, rows, 4)):
-        raise ValueError(f"{name}'s scales must be [.., ceil(D / 128), rows, 4]")
-    if codes.get_device() != scales.get_device():
-        raise ValueError(f"{name}'s codes and scales must live on one device")
-    return (1 if n == 2 else shape[0]), rows, 2 * half
+    if len(shape) == 2:
+        rows, half = shape
+        if not half % 16 and scales.shape == (-(-half // 64), rows, 4):
+            return rows, 2 * half
+    elif len(shape) == 3:
+        E, rows, half = shape
+        if not half % 16 and scales.shape == (E, -(-half // 64), rows, 4):
+            return E, rows, 2 * half
+    raise ValueError(f"{name} must be codes [.., rows, D / 2], D a multiple of 32, and scales "
+                     "[.., ceil(D / 128), rows, 4]")
 
 
-def _mx_out(name: str, out: Optional[MxFp4], lead, rows: int, D: int, device, stream) -> MxFp4:
+def _mx_out(out: Optional[MxFp4], lead, rows: int, D: int, device, stream) -> MxFp4:
     if out is None:
         return MxFp4(_empty((*lead, rows, D // 2), _U8, device, stream),
                      _empty((*lead, -(-D // 128), rows, 4), _U8, device, stream))
-    _check_mx(name, out, (2 + len(lead),))
-    if out.codes.shape != (*lead, rows, D // 2):
-        raise ValueError(f"{name} must be {[*lead, rows, D]}")
+    if _check_mx("out", *out) != (*lead, rows, D):
+        raise ValueError(f"out must be {[*lead, rows, D]}")
     return out
 
 
@@ -643,11 +654,26 @@ def _values(x: torch.Tensor, name: str, D: int) -> int:
     """The code of x's type, if its rows can be MXFP4."""
     if D < 32 or D % 32:
         raise ValueError("MXFP4 rows must be a multiple of 32 elements")
-    if x.dtype is torch.bfloat16:
+    dtype = x.dtype
+    if dtype is _BF16:
         return MOE_BF16
-    if x.dtype is torch.float32:
+    if dtype is _F32:
         return MOE_F32
     raise TypeError(f"{name} must be bfloat16 or float32")
+
+
+def _float_out(out: Optional[torch.Tensor], shape, dtype: torch.dtype, device, stream):
+    """(out, the code of its type)"""
+    if out is None:
+        if dtype is not _BF16 and dtype is not _F32:
+            raise TypeError(f"unsupported output dtype {dtype}")
+        return _empty(shape, dtype, device, stream), MOE_BF16 if dtype is _BF16 else MOE_F32
+    if out.shape != shape:
+        raise ValueError(f"out must be {list(shape)}")
+    dtype = out.dtype
+    if dtype is not _BF16 and dtype is not _F32:
+        raise TypeError(f"unsupported output dtype {dtype}")
+    return out, MOE_BF16 if dtype is _BF16 else MOE_F32
 
 
 def moe_quant_mxfp4(x: torch.Tensor, *, out: Optional[MxFp4] = None, stream=None) -> MxFp4:
@@ -656,10 +682,10 @@ def moe_quant_mxfp4(x: torch.Tensor, *, out: Optional[MxFp4] = None, stream=None
         raise ValueError("x must be [rows, D] or [E, rows, D]")
     *lead, rows, D = x.shape
     dt = _values(x, "x", D)
-    out = _mx_out("out", out, lead, rows, D, x.device, stream)
+    out = _mx_out(out, lead, rows, D, x.device, stream)
+    px, *pout = _pointers(x, *out)
     _abi.check("moe_quant_mxfp4", lib().moe_quant_mxfp4(
-        _ptr(x), dt, lead[0] if lead else 1, rows, D, _ptr(out.codes), _ptr(out.scales),
-        _stream(stream, x)))
+        px, dt, lead[0] if lead else 1, rows, D, *pout, _stream(stream, x)))
     return out
 
 
@@ -671,22 +697,22 @@ def moe_dispatch_quant_mxfp4(x: torch.Tensor, tok_map: torch.Tensor, *,
     if x.dim() != 2 or tok_map.dim() != 2:
         raise ValueError("x must be [S, D] and tok_map [S, K]")
     S, D = x.shape
+    n, K = tok_map.shape
     if tok_map.dtype is not torch.int64:
         raise TypeError("tok_map must be int64")
-    n, K = tok_map.shape
     if n != S:
         raise ValueError("x must be [S, D] and tok_map [S, K]")
     dt = _values(x, "x", D)
     if out is None:
         rows = max(-(-S * K // 4) * 4, 4)
-        out = _mx_out("out", None, (), rows, D, x.device, stream)
+        out = _mx_out(None, (), rows, D, x.device, stream)
     else:
-        _, rows, width = _check_mx("out", out, (2,))
-        if width != D:
+        rows, *width = _check_mx("out", *out)
+        if width != [D]:
             raise ValueError("out must hold rows of D elements")
+    px, pmap, *pout = _pointers(x, tok_map, *out)
     _abi.check("moe_dispatch_quant_mxfp4", lib().moe_dispatch_quant_mxfp4(
-        _ptr(x), dt, S, D, K, _ptr(tok_map), _ptr(out.codes), _ptr(out.scales), rows,
-        _stream(stream, x)))
+        px, dt, S, D, K, pmap, *pout, rows, _stream(stream, x)))
     return out
 
 
@@ -699,26 +725,23 @@ def moe_swiglu_quant_mxfp4(u: torch.Tensor, *, out: Optional[MxFp4] = None,
     rows, F = u.shape
     F //= 2
     dt = _values(u, "u", F)
-    out = _mx_out("out", out, (), rows, F, u.device, stream)
+    out = _mx_out(out, (), rows, F, u.device, stream)
+    pu, *pout = _pointers(u, *out)
     _abi.check("moe_swiglu_quant_mxfp4", lib().moe_swiglu_quant_mxfp4(
-        _ptr(u), dt, rows, F, _ptr(out.codes), _ptr(out.scales), _stream(stream, u)))
+        pu, dt, rows, F, *pout, _stream(stream, u)))
     return out
 
 
 def moe_dequant_mxfp4(q: MxFp4, *, out_dtype: torch.dtype = torch.bfloat16,
                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values that MXFP4 rows or weights stand for."""
-    groups, rows, D = _check_mx("q", q)
     codes, scales = q
-    shape = (*codes.shape[:-1], D)
-    if out is None:
-        if out_dtype not in _TORCH_DT.values():
-            raise TypeError(f"unsupported output dtype {out_dtype}")
-        out = _empty(shape, out_dtype, codes.device, stream)
-    elif out.shape != shape or out.dtype not in _TORCH_DT.values():
-        raise ValueError("out must be bfloat16 or float32 with the shape of the values")
+    shape = _check_mx("q", codes, scales)
+    out, dt = _float_out(out, shape, out_dtype, codes.device, stream)
+    pcodes, pscales, pout = _pointers(codes, scales, out)
     _abi.check("moe_dequant_mxfp4", lib().moe_dequant_mxfp4(
-        _ptr(codes), _ptr(scales), groups, rows, D, _ptr(out), _dt(out), _stream(stream, codes)))
+        pcodes, pscales, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], pout, dt,
+        _stream(stream, codes)))
     return out
 
 
@@ -728,16 +751,17 @@ def moe_expert_gemm_mxfp4(x: MxFp4, w: MxFp4, plan: Union[Plan, CapacityPlan], *
     """y[r] = w[e] x[r] for the rows of each bucket e of the plan, zero on rows
     in no bucket.  x [rows, D] (rows of the buffer a multiple of 4), w
     [E, N, D], both in MXFP4; y [rows, N]."""
-    _, rows, D = _check_mx("x", x, (2,))
-    E, N, width = _check_mx("w", w, (3,))
-    if width != D:
+    codes, scales = x
+    xs, ws = _check_mx("x", codes, scales), _check_mx("w", *w)
+    if len(xs) != 2 or len(ws) != 3 or xs[1] != ws[2]:
         raise ValueError("w must be [E, N, D] and x [rows, D]")
+    rows, D = xs
+    E, N, _ = ws
     _check_plan(plan, E)
-    codes = x.codes
-    out = _expert_out(out, (rows, N), out_dtype, codes.device, stream)
+    out, dt = _float_out(out, (rows, N), out_dtype, codes.device, stream)
+    pc, ps, pwc, pws, pcnt, poff, pout = _pointers(codes, scales, *w, plan.cnt, plan.off, out)
     _abi.check("moe_expert_gemm_mxfp4", lib().moe_expert_gemm_mxfp4(
-        _ptr(codes), _ptr(x.scales), rows, _ptr(w.codes), _ptr(w.scales), N, D, E,
-        _ptr(plan.cnt), _ptr(plan.off), _ptr(out), _dt(out), _stream(stream, codes)))
+        pc, ps, rows, pwc, pws, N, D, E, pcnt, poff, pout, dt, _stream(stream, codes)))
     return out
 
 
@@ -755,39 +779,41 @@ def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
     w_up[e] x[s], e = topk_idx[s,k], for up to 1024 entries S * K.  x bf16
     [S, H]; w_up [E, 2 F, H] (gates before ups) and w_down [E, H, F] both bf16
     or both in MXFP4.  Ids outside [0, E) give nothing."""
-    if isinstance(w_up, torch.Tensor):
-        if not isinstance(w_down, torch.Tensor):
-            raise TypeError("w_up and w_down must both be tensors or both MxFp4")
-        if w_up.dtype is not torch.bfloat16 or w_down.dtype is not torch.bfloat16:
-            raise TypeError("weights must be bfloat16 or MxFp4")
-        kind, shape, down = MOE_BF16, w_up.shape, w_down.shape
-        parts = w_up, None, w_down, None
+    mx = not isinstance(w_up, torch.Tensor)
+    if mx == isinstance(w_down, torch.Tensor):
+        raise TypeError("w_up and w_down must both be tensors or both MxFp4")
+    if mx:
+        kind, up, down = MOE_MXFP4, _check_mx("w_up", *w_up), _check_mx("w_down", *w_down)
     else:
-        if isinstance(w_down, torch.Tensor):
-            raise TypeError("w_up and w_down must both be tensors or both MxFp4")
-        kind, shape, down = MOE_MXFP4, _check_mx("w_up", w_up, (3,)), _check_mx("w_down", w_down, (3,))
-        parts = *w_up, *w_down
-    if x.dtype is not torch.bfloat16 or x.dim() != 2:
+        kind, up, down = MOE_BF16, w_up.shape, w_down.shape
+        if w_up.dtype is not _BF16 or w_down.dtype is not _BF16:
+            raise TypeError("weights must be bfloat16 or MxFp4")
+    if x.dtype is not _BF16 or x.dim() != 2:
         raise TypeError("x must be bfloat16 [S, H]")
     S, H = x.shape
-    if len(shape) != 3:
+    if len(up) != 3 or up[1] % 2 or up[2] != H or down != (up[0], H, up[1] // 2):
         raise ValueError("w_up must be [E, 2 F, H] and w_down [E, H, F]")
-    E, F = shape[0], shape[1] // 2
-    if shape[1] % 2 or shape[2] != H or down != (E, H, F):
-        raise ValueError("w_up must be [E, 2 F, H] and w_down [E, H, F]")
+    E, F = up[0], up[1] // 2
     routes = topk_idx.shape
     if topk_idx.dtype is not torch.int32 or len(routes) != 2 or routes[0] != S:
         raise TypeError("topk_idx must be int32 [S, K]")
-    if topk_w.dtype is not torch.float32 or topk_w.shape != routes:
+    if topk_w.dtype is not _F32 or topk_w.shape != routes:
         raise TypeError("topk_w must be float32 with the shape of topk_idx")
     K = routes[1]
-    out = _expert_out(out, (S, H), out_dtype, x.device, stream)
+    device = x.device
+    out, dt = _float_out(out, (S, H), out_dtype, device, stream)
     L = lib()
     nws = int(L.moe_expert_layer_workspace_size(S, H, K, E, F, kind))
-    ws = _workspace(nws, x.device, workspace, stream)
+    ws = _workspace(nws, device, workspace, stream)
+    if ws is None:   # sizes that the call refuses
+        ws = out
+    if mx:
+        px, pidx, pw, pout, pws, *weights = _pointers(x, topk_idx, topk_w, out, ws, *w_up, *w_down)
+    else:
+        px, pidx, pw, pout, pws, pup, pdown = _pointers(x, topk_idx, topk_w, out, ws, w_up, w_down)
+        weights = pup, None, pdown, None
     _abi.check("moe_expert_layer", L.moe_expert_layer(
-        _ptr(x), S, H, _ptr(topk_idx), _ptr(topk_w), K, E, F, kind, *map(_ptr, parts), _ptr(out),
-        _dt(out), _ptr(ws), nws, _stream(stream, x)))
+        px, S, H, pidx, pw, K, E, F, kind, *weights, pout, dt, pws, nws, _stream(stream, x)))
     return out
 
 

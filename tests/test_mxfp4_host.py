@@ -99,6 +99,8 @@ def test_binding_refuses():
                         ((x[None], tok_map), ValueError), ((x.half(), tok_map), TypeError)):
         with pytest.raises(error):
             moe.moe_dispatch_quant_mxfp4(*args)
+    with pytest.raises(ValueError):   # three dimensions
+        moe.moe_dispatch_quant_mxfp4(x, tok_map, out=moe.MxFp4(q.codes[None], q.scales[None]))
     with pytest.raises(ValueError):
         moe.moe_swiglu_quant_mxfp4(torch.zeros(4, 33))
     with pytest.raises(ValueError):   # tensors of the host are refused before the call
