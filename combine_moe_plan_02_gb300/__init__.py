@@ -820,7 +820,7 @@ def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
 def moe_device_errors() -> int:
     """Reads and clears the kernels' device error bits (synchronous): bit 0
     dispatch wait timeout, bit 1 dispatch row index out of range, bit 2
-    combine row index out of range, bit 4 expert product wait timeout, bit 5
+    combine row index out of range, bit 4 expert product or layer wait timeout, bit 5
     expert product bucket out of range."""
     v = ctypes.c_uint32(0)
     _abi.check("moe_device_errors", lib().moe_device_errors(ctypes.byref(v)))

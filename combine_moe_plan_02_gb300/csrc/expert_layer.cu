@@ -667,6 +667,8 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 const Tile c = walk(t);
                 const int cols = columns_of(c.rows);
                 for (int b = 0; b < blocks; ++b, ++j) {
+                    // the time until the launch before is done counts for no wait's limit
+                    if (is_weights && !kFirst && j == stages) griddep_wait();
                     if (j >= stages && !wait(&sh.empty[r.at], r.round ^ 1, &sh.stop)) {
                         ok = false;
                         break;
@@ -715,6 +717,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
     } else if (warp == 1) {
         // One thread issues.  A stage has its own columns of scales: the copy into it,
         // which begins when the products that read it before are done, frees both.
+        if (!kFirst) griddep_wait();
         if (elect_one()) {
             Ring r(stages);
             int i = 0;  // accumulators begun

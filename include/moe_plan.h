@@ -103,8 +103,8 @@ int moe_last_cuda_error(void);
  *          entry outside topk_w (that term was dropped)
  *   bit 3  reserved for a combine that waits on staged rows; the combine
  *          kernels of this version never wait and never set it
- *   bit 4  expert products: a bounded wait ran out of time (the kernel stopped
- *          early; its output is incomplete)
+ *   bit 4  expert products and layer: a bounded wait ran out of time (the kernel
+ *          stopped early; its output is incomplete)
  *   bit 5  expert products: a bucket of the plan lies outside the rows (that
  *          bucket was left out), or buckets overlap in a call of up to 64 rows
  *          and some were left out
@@ -550,7 +550,8 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
  * Sums and h are f32 and out is rounded once.  bf16 weights: h enters the second
  * product as two bf16 parts, 16 bits of it, or three, all of it, for f32 outputs.
  * MXFP4 weights: x and h enter the products with an error of at most 2^-23 of the
- * largest of 32 neighbours; a token with an infinite x or h gives NaN.  The sum over k is in increasing k.  Ids outside [0, E) give nothing; a
+ * largest of 32 neighbours (where that is below 2^-126, as zeros); a token with an
+ * infinite x or h gives NaN.  The sum over k is in increasing k.  Ids outside [0, E) give nothing; a
  * token without a valid id gives zeros.  Results are reproducible.
  *
  * x         bf16 [S, H]; topk_idx int32 [S, K]; topk_w f32 [S, K]
