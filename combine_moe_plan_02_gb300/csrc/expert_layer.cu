@@ -16,6 +16,8 @@
 // thread issues the matrix instructions (tcgen05, weights on the M side, entries on the N
 // side: nothing is spent on a weight outside the tensor core), four warps read the sums.
 // A token's outputs are summed over k by the warp that brings the last of its experts.
+// Tiles are dealt out in turn: taken from a counter, 32 tokens of 64 experts (7168, 2048,
+// MXFP4) take 257 instead of 262 us, one token of 8 40 instead of 39.
 //
 // bf16 weights: x goes in as it is, a row an entry.  h is f32: it goes in as three
 // bf16 rows that add up to it.

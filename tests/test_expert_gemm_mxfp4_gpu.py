@@ -230,3 +230,16 @@ def test_whole_layer_graph_and_streams():
     for i, o in enumerate(outs):
         assert torch.equal(o, layer(xs[i % 3]))
     assert moe.moe_device_errors() == 0
+
+
+def test_rows_of_a_buffer():
+    """A buffer's rows are a multiple of four; one that is not is refused."""
+    import combine_moe_plan_02_gb300 as moe
+    plan, rows = make_plan([3, 2])
+    x, w = operand((6, 64), 1), operand((2, 64, 64), 2)
+    with pytest.raises(moe.MoeError):
+        moe.moe_expert_gemm_mxfp4(x, w, plan)
+    x = operand((8, 64), 1)
+    want = reference(x, w, plan).to(F32)
+    assert torch.equal(moe.moe_expert_gemm_mxfp4(x, w, plan, out_dtype=F32), want)
+    assert (want[5:] == 0).all()

@@ -226,3 +226,67 @@ def test_against_the_calls_for_batches():
     want = moe.moe_combine(moe.moe_expert_gemm(h, down, plan, out_dtype=F32), w, plan.tok_map, out_dtype=F32)
     got = moe.moe_expert_layer(x, idx, w, up, down, out_dtype=F32)
     assert (got - want).norm() < 4e-3 * want.norm()   # h in bf16 there
+
+
+def test_at_once_with_the_products():
+    """Layers of both kinds and products of both kinds on four streams at once: they
+    share tensor memory and SMs and must neither wait for one another nor mix."""
+    import combine_moe_plan_02_gb300 as moe
+    E, H, F = 8, 1024, 256
+    layers = [make(12, E, 4, H, F, mx, 30 + mx) for mx in (False, True)]
+    x, idx, _, up, _ = layers[0]
+    plan, rows, _ = moe.moe_plan_dispatch(idx, x, E)
+    qplan = moe.moe_plan(layers[1][1], E)
+    q, qup = moe.moe_dispatch_quant_mxfp4(layers[1][0], qplan.tok_map), layers[1][3]
+    jobs = [lambda: moe.moe_expert_layer(*layers[0]), lambda: moe.moe_expert_layer(*layers[1]),
+            lambda: moe.moe_expert_gemm(rows, up, plan), lambda: moe.moe_expert_gemm_mxfp4(q, qup, qplan)]
+    want = [job() for job in jobs]
+    streams = [torch.cuda.Stream() for _ in jobs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(30):
+        for job, stream in zip(jobs, streams):
+            with torch.cuda.stream(stream):
+                got.append(job())
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 4]), i
+    assert moe.moe_device_errors() == 0
+
+
+@pytest.mark.parametrize("mx", [False, True])
+def test_two_graphs_share_a_workspace(mx):
+    import combine_moe_plan_02_gb300 as moe
+    a, b = (make(S, 6, 2, 512, 96, mx, 40 + S) for S in (3, 40))
+    ws = torch.empty(max(moe.moe_expert_layer_workspace_size(S, 512, 2, 6, 96, mx) for S in (3, 40)),
+                     dtype=torch.uint8, device="cuda")
+    want = [moe.moe_expert_layer(*t) for t in (a, b)]
+    graphs, outs = [], []
+    for t in (a, b):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(moe.moe_expert_layer(*t, workspace=ws))
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        assert torch.equal(outs[i], want[i])
+
+
+def test_views_and_alignment():
+    """Weights and rows inside larger tensors; rows that do not begin on 16 bytes are refused."""
+    import combine_moe_plan_02_gb300 as moe
+    x, idx, w, up, down = make(5, 4, 2, 256, 96, False, 50)
+    more = [torch.cat([t[:1], t, t[:1]]) for t in (up, down)]
+    long = torch.cat([x, x])
+    want = moe.moe_expert_layer(x, idx, w, up, down)
+    assert torch.equal(moe.moe_expert_layer(long[5:], idx, w, more[0][1:5], more[1][1:5]), want)
+    flat = torch.zeros(x.numel() + 8, dtype=BF16, device="cuda")
+    flat[4:4 + x.numel()] = x.flatten()
+    with pytest.raises(moe.MoeError):
+        moe.moe_expert_layer(flat[4:4 + x.numel()].view_as(x), idx, w, up, down)
+    with pytest.raises(ValueError):
+        moe.moe_expert_layer(x, idx.t().contiguous().t(), w, up, down)
+    with pytest.raises(ValueError):
+        moe.moe_expert_layer(x, idx.cpu(), w, up, down)
+    with pytest.raises(moe.MoeError):   # more entries than the call takes
+        moe.moe_expert_layer(x.repeat(110, 1), idx.repeat(110, 1), w.repeat(110, 1), up, down)

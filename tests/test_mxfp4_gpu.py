@@ -194,6 +194,8 @@ def test_strided_offset_and_large():
     same(moe.moe_quant_mxfp4(base[2:7]), mxfp4.quant(base[2:7]))
     with pytest.raises(ValueError):
         moe.moe_quant_mxfp4(base[:, :128])
+    with pytest.raises(moe.MoeError):   # rows that do not begin on 16 bytes
+        moe.moe_quant_mxfp4(base.flatten()[4:4 + 512].view(2, 256))
     rows, D = 70001, 32768
     x = torch.zeros(rows, D, dtype=BF16, device="cuda")
     x[-1] = spread((1, D), 5, BF16)
