@@ -15,7 +15,7 @@
 // it (nothing there writes weights).  A second warp copies the rows that they meet, one
 // thread issues the matrix instructions (tcgen05, weights on the M side, entries on the N
 // side: nothing is spent on a weight outside the tensor core), four warps read the sums.
-// A token's outputs are summed over k by the warp that brings the last of its experts.
+// A token's outputs are summed over k by the CTA that brings the last of its experts.
 // Tiles are dealt out in turn: taken from a counter, 32 tokens of 64 experts (7168, 2048,
 // MXFP4) take 257 instead of 262 us, one token of 8 40 instead of 39.
 //
@@ -85,7 +85,7 @@ __device__ uint32_t g_layer_error;  // kErrExpertTimeout
 // 1024 entries, 1 to 2 us, where a launch that makes them for all would cost as
 // much.  Ranks are those of the entries' order, so all CTAs and launches agree.
 struct Routing {
-    int16_t *count;   // [E] entries of each expert, then its place among those with tokens
+    int16_t *count;   // [E] an expert's place among those with tokens
     int16_t *hit;     // [hits] experts with tokens
     int16_t *first;   // [hits + 1] first packed row of each
     int16_t *parts;   // [hits + 1] parts of at most `rows` rows before each
@@ -94,7 +94,10 @@ struct Routing {
                       // or not; -1 without an expert
     int hits;
 
-    static size_t bytes(int n, int E) { return (size_t)(E + 3 * (n < E ? n : E) + 2 + 2 * n) * 2; }
+    static __host__ __device__ size_t bytes(int n, int E)
+    {
+        return (size_t)(E + 3 * (n < E ? n : E) + 2 + 2 * n) * 2;
+    }
 
     __device__ Routing(void *smem, int n, int E)
     {
@@ -109,8 +112,9 @@ struct Routing {
     }
 };
 
+// `table`: THREADS / 32 x E counts in shared memory, for more than 32 entries.
 template <int THREADS>
-__device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
+__device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r, uint16_t *table)
 {
     constexpr int kWarps = THREADS / 32, kEach = kMaxExperts / THREADS;
     __shared__ int s_sum[kWarps], s_hits[kWarps], s_parts[kWarps];
@@ -145,24 +149,26 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
         r.hits = s_hits[0];
         return;
     }
-    for (int e = tid; e < E; e += THREADS) r.count[e] = 0;
+    // Each warp ranks neighbouring chunks of 32 entries; then the warps' counts of an
+    // expert are added up in order.  (One warp alone takes 0.25 us a chunk.)
+    const int each = ((n + 31) / 32 + kWarps - 1) / kWarps;  // chunks of a warp
+    for (int i = tid; i < kWarps * E; i += THREADS) table[i] = 0;
     for (int i = tid; i < n; i += THREADS) {
         const int e = __ldg(idx + i);
         r.place[i] = e >= 0 && e < E ? e : -1;
     }
     __syncthreads();
-    if (warp == 0) {
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const int i = i0 + lane, e = i < n ? r.place[i] : -1;
-            const uint32_t same = __match_any_sync(0xffffffffu, e);
-            const int before = e >= 0 ? r.count[e] : 0;
-            __syncwarp();
-            if (e >= 0) {
-                r.place[i] = before + __popc(same & lanemask_lt());
-                if ((same & lanemask_lt()) == 0) r.count[e] = before + __popc(same);
-            }
-            __syncwarp();
+    uint16_t *mine = table + warp * E;
+    for (int i0 = warp * each * 32; i0 < min(n, (warp + 1) * each * 32); i0 += 32) {
+        const int i = i0 + lane, e = i < n ? r.place[i] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const int before = e >= 0 ? mine[e] : 0;
+        __syncwarp();
+        if (e >= 0) {
+            r.place[i] = before + __popc(same & lanemask_lt());
+            if ((same & lanemask_lt()) == 0) mine[e] = before + __popc(same);
         }
+        __syncwarp();
     }
     __syncthreads();
     // a thread owns kEach neighbouring experts
@@ -170,7 +176,13 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
         const int e = tid * kEach + j;
-        c[j] = e < E ? r.count[e] : 0;
+        c[j] = 0;
+        if (e < E)
+            for (int w = 0; w < kWarps; ++w) {
+                const int v = table[w * E + e];
+                table[w * E + e] = (uint16_t)c[j];
+                c[j] += v;
+            }
         sum += c[j];
         some += c[j] > 0;
         part += (c[j] + rows - 1) / rows;
@@ -203,11 +215,12 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r)
     for (int i = tid; i < n; i += THREADS) {
         const int e = __ldg(idx + i);
         if (e >= 0 && e < E) {
-            const int h = r.count[e], slot = r.place[i];
+            const int h = r.count[e], slot = table[i / (each * 32) * E + e] + r.place[i];
             r.order[r.first[h] + slot] = i;
             r.place[i] = r.parts[h] * rows + slot;
         }
     }
+    fence_proxy_async_smem();  // the table's place may be copied into from here on
     __syncthreads();
 }
 
@@ -217,43 +230,42 @@ __device__ __forceinline__ void load_weights(const float *topk_w, int n, float *
     for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = __ldg(topk_w + i);
 }
 
-// out[s, o] = sum over the valid entries of s, in increasing k, for N tokens of which
-// the first `count` are stored: y [S K, H] holds the experts' rows by entry.  The
-// loads are unconditional, so that 8 N of them are under way: with a condition
-// each, or a token at a time, 32 tokens took 30 to 50 us.
-constexpr int kTokens = 4;
-template <int N>
+// out[s, o .. o + 3] = sum over the valid entries of s, in increasing k: y [S K, H] holds
+// the experts' rows by entry.  The loads are unconditional, so that eight are under way.
 __device__ __forceinline__ void sum_entries(const float *y, const float *weights,
-                                            const int16_t *place, int K, int H, int o,
-                                            const int (&s)[kTokens], int count, void *out,
-                                            bool f32)
+                                            const int16_t *place, int K, int H, int o, int s,
+                                            void *out, bool f32)
 {
     constexpr int kAtOnce = 8;
-    float sum[N];
-#pragma unroll
-    for (int j = 0; j < N; ++j) sum[j] = 0.0f;
+    float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     for (int k0 = 0; k0 < K; k0 += kAtOnce) {
-        float v[N][kAtOnce];
+        float4 v[kAtOnce];
 #pragma unroll
-        for (int j = 0; j < N; ++j)
+        for (int k = 0; k < kAtOnce; ++k)
+            v[k] = __ldcg(reinterpret_cast<const float4 *>(
+                y + (int64_t)(s * K + min(k0 + k, K - 1)) * H + o));
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                v[j][k] = __ldcg(y + (int64_t)(s[j] * K + min(k0 + k, K - 1)) * H + o);
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const int i = s[j] * K + min(k0 + k, K - 1);
-                // rows of entries without an expert hold anything
-                if (k0 + k < K && place[i] >= 0) sum[j] = fmaf(weights[i], v[j][k], sum[j]);
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = s * K + min(k0 + k, K - 1);
+            // rows of entries without an expert hold anything
+            if (k0 + k < K && place[i] >= 0) {
+                const float w = weights[i];
+                sum.x = fmaf(w, v[k].x, sum.x);
+                sum.y = fmaf(w, v[k].y, sum.y);
+                sum.z = fmaf(w, v[k].z, sum.z);
+                sum.w = fmaf(w, v[k].w, sum.w);
             }
+        }
     }
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-        if (j >= count) break;
-        if (f32) static_cast<float *>(out)[(int64_t)s[j] * H + o] = sum[j];
-        else
-            static_cast<__nv_bfloat16 *>(out)[(int64_t)s[j] * H + o] = __float2bfloat16_rn(sum[j]);
+    const int64_t at = (int64_t)s * H + o;
+    if (f32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = sum;
+    } else {
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(sum.x, sum.y),
+                             hi = __floats2bfloat162_rn(sum.z, sum.w);
+        st8(static_cast<__nv_bfloat16 *>(out) + at,
+            make_uint2(*reinterpret_cast<const uint32_t *>(&lo),
+                       *reinterpret_cast<const uint32_t *>(&hi)));
     }
 }
 
@@ -331,7 +343,8 @@ __global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
     const int tid = threadIdx.x, lane = tid & 31;
     griddep_wait();
     griddep_launch_dependents();
-    route<kThreads>(a.idx, n, a.E, kRows, rt);
+    route<kThreads>(a.idx, n, a.E, kRows, rt,
+                    reinterpret_cast<uint16_t *>(lists + Routing::bytes(n, a.E) / 2));
     const int chunks = (a.H + 255) / 256, words = (a.H + 127) / 128;
     for (int u = blockIdx.x * (kThreads / 32) + (tid >> 5); u < a.S * chunks;
          u += gridDim.x * (kThreads / 32)) {
@@ -378,7 +391,7 @@ struct LayerArgs {
     uint8_t *h;           // MXFP4: codes [parts, 64, F / 2]; bf16 [parts, 32, F]
     uint8_t *h_scales;    // MXFP4: [ceil(F / 128), parts, 32, 4, 4]
     float *y;             // [n, H]
-    uint32_t *arrived;    // [ceil(H / 128), 4, S] experts whose share of these outputs is there
+    uint32_t *arrived;    // [ceil(H / 128), S] experts whose share of these outputs is there
     uint8_t *out;
     int S, K, E, H, F;
     int parts;            // that there is room for
@@ -414,6 +427,18 @@ __device__ __forceinline__ void copy_2d(void *dst, const CUtensorMap *map, uint6
     asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
                  "[%0], [%1, {%3, %4}], [%2];" ::"r"(smem_u32(dst)),
                  "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+                 : "memory");
+}
+
+// Four rows of a map of single rows.
+__device__ __forceinline__ void gather_rows(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                            const int (&row)[4])
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+                 ".mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]),
+                 "r"(row[3])
                  : "memory");
 }
 
@@ -634,7 +659,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
     constexpr bool kFirst = UP && !MX;
     if (kFirst) griddep_wait();
     if (!UP) load_weights(a.topk_w, n, weights);
-    route<kThreads>(a.idx, n, a.E, kRows, rt);  // has barriers
+    route<kThreads>(a.idx, n, a.E, kRows, rt, reinterpret_cast<uint16_t *>(ring));  // has barriers
     if (!UP) {
         for (int s = tid; s < a.S; s += kThreads) {
             int k = 0;
@@ -668,6 +693,11 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
             for (int t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
                 const Tile c = walk(t);
                 const int cols = columns_of(c.rows);
+                int token[2][4];  // rows of x, the last one again in the places of none
+                if (!MX && UP && !is_weights)
+#pragma unroll
+                    for (int x = 0; x < kRows; ++x)
+                        token[x / 4][x % 4] = rt.order[c.row + min(x, c.rows - 1)] / a.K;
                 for (int b = 0; b < blocks; ++b, ++j) {
                     // the time until the launch before is done counts for no wait's limit
                     if (is_weights && !kFirst && j == stages) griddep_wait();
@@ -696,10 +726,12 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                             copy_3d(stage, &maps.a, bar, b * 64, m, c.e);
                         }
                     } else if (!MX && UP) {
-                        mbar_arrive_expect_tx(bar, c.rows * 128);
-                        for (int x = 0; x < c.rows; ++x)
-                            copy_2d(rows + x * 128, &maps.b[0], bar, b * 64,
-                                    rt.order[c.row + x] / a.K);
+                        // Four rows a copy: with one each, 16 tokens of 2 of 8 experts
+                        // (5120, 832) took 76 us instead of 55.
+                        mbar_arrive_expect_tx(bar, c.rows == 1 ? 128 : c.rows > 4 ? 1024 : 512);
+                        if (c.rows == 1) copy_2d(rows, &maps.b[0], bar, b * 64, token[0][0]);
+                        else gather_rows(rows, &maps.b[0], bar, b * 64, token[0]);
+                        if (c.rows > 4) gather_rows(rows + 512, &maps.b[0], bar, b * 64, token[1]);
                     } else {
                         mbar_arrive_expect_tx(bar, cols * 128 + (MX ? kScales : 0));
                         copy_2d(rows, &maps.b[c.rows > kRows / 2], bar, b * (MX ? 128 : 64),
@@ -860,8 +892,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
             }
-            if (UP) ok = agree(ok);
-            if (!ok) break;
+            if (!agree(ok)) break;
             if constexpr (UP) {
                 // the gate of an output here, its up 16 (or 8) lanes on
                 const bool gate = MX ? lane < 16 : (lane & 8) == 0;
@@ -876,43 +907,31 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 store_h<MX>(a, c, box, me);
                 join();  // the box has been read
             } else {
-                // Each warp stores its outputs and counts them for itself: the warps
-                // need not meet.  A token's outputs are summed by the warp that brings the
-                // last of its experts, which spreads the sums over the call: summed for all
-                // 32 tokens by the last expert's they took 55 us at its end.
+                // A token's outputs are summed by the CTA that brings the last of its
+                // experts, which spreads the sums over the call (by the last expert's CTA
+                // for all tokens they took 55 us at the end of 32), by a warp all 128 of
+                // them: little code, which a call's end meets for the first time.
                 const int o = c.m * kTile + (MX ? 4 * lane + q : 32 * q + lane);
                 if (o < a.H)
 #pragma unroll
                     for (int x = 0; x < kRows; ++x)
                         if (x < c.rows) a.y[(int64_t)rt.order[c.row + x] * a.H + o] = sum[x];
-                __syncwarp();
+                __threadfence();
+                join();
                 int token = 0;
                 bool last = false;
-                __threadfence();
-                if (lane < c.rows) {
-                    token = rt.order[c.row + lane] / a.K;
-                    last = atomicAdd(a.arrived + (c.m * 4 + q) * a.S + token, 1u) + 1 ==
+                if (lane < 2 && q + 4 * lane < c.rows) {  // entries q and q + 4
+                    token = rt.order[c.row + q + 4 * lane] / a.K;
+                    last = atomicAdd(a.arrived + c.m * a.S + token, 1u) + 1 ==
                            (uint32_t)valid[token];
                 }
                 uint32_t ready = __ballot_sync(0xffffffffu, last);
                 if (ready) __threadfence();
-                while (ready) {
-                    int s[kTokens], count = 0, from = 0;
-#pragma unroll
-                    for (int j = 0; j < kTokens; ++j) {
-                        if (ready) {
-                            from = __ffs(ready) - 1;
-                            ready &= ready - 1;
-                            ++count;
-                        }
-                        s[j] = __shfl_sync(0xffffffffu, token, from);
-                    }
-                    if (o >= a.H) continue;
-                    if (count == 1)
-                        sum_entries<1>(a.y, weights, rt.place, a.K, a.H, o, s, 1, a.out, a.f32);
-                    else
-                        sum_entries<kTokens>(a.y, weights, rt.place, a.K, a.H, o, s, count, a.out,
-                                             a.f32);
+                for (; ready; ready &= ready - 1) {
+                    const int s = __shfl_sync(0xffffffffu, token, __ffs(ready) - 1);
+                    if (c.m * kTile + 4 * lane < a.H)
+                        sum_entries(a.y, weights, rt.place, a.K, a.H, c.m * kTile + 4 * lane, s,
+                                    a.out, a.f32);
                 }
             }
         }
@@ -1010,7 +1029,7 @@ struct Places {
         arrived = take(counters(S, H) * 4);
         bytes = at;
     }
-    static int64_t counters(int64_t S, int64_t H) { return (H + kTile - 1) / kTile * 4 * S; }
+    static int64_t counters(int64_t S, int64_t H) { return (H + kTile - 1) / kTile * S; }
 };
 
 struct LayerCall {
@@ -1062,7 +1081,7 @@ int layer_mxfp4(const LayerCall &c, LayerArgs a, cudaStream_t stream)
                    {3, {H, down_words, E}, {H * 4, down_words * H * 4}, {kTile, 2, 1}});
     if (e == cudaSuccess) e = encode_mx_rows(down, a.h, a.h_scales, a.parts, a.F);
     static KernelCache kc;
-    const size_t smem = Routing::bytes(a.S * a.K, a.E);
+    const size_t smem = Routing::bytes(a.S * a.K, a.E) + (size_t)a.E * (kThreads / 32) * 2;
     if (e == cudaSuccess) e = prepare_kernel(split_kernel, smem, kThreads, kc, nullptr);
     if (e == cudaSuccess) {
         const SplitArgs s = {c.x, a.idx, ws + at.x, reinterpret_cast<uint32_t *>(ws + at.x_scales),
