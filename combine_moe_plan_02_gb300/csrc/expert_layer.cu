@@ -14,7 +14,8 @@
 // 64 KB of weights in flight a CTA), and begins before the launch waits for the one before
 // it (nothing there writes weights).  A second warp copies the rows that they meet, one
 // thread issues the matrix instructions (tcgen05, weights on the M side, entries on the N
-// side: nothing is spent on a weight outside the tensor core), four warps read the sums.
+// side: nothing is spent on a weight outside the tensor core), four warps read a tile's
+// sums and four others the next one's.
 // A token's outputs are summed over k by the CTA that brings the last of its experts.
 // Tiles are dealt out in turn: taken from a counter, 32 tokens of 64 experts (7168, 2048,
 // MXFP4) take 257 instead of 262 us, one token of 8 40 instead of 39.
@@ -51,7 +52,8 @@ namespace {
 constexpr int kMaxEntries = 1024;    // S * K
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxWidth = 16384;     // H, F
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;        // two groups of four storing warps take tiles by turns
+constexpr int kSplitThreads = 256;
 constexpr int kRows = 8;             // entries of a tile
 constexpr int kTile = 128;           // weight rows of a tile
 constexpr int kCodesA = kTile * 128; // of weights in a stage: 128 bytes of each row
@@ -60,7 +62,7 @@ constexpr int kMaxStages = 10;
 constexpr int kScaleAt = 128;        // first TMEM column of the scales, after the accumulators
 constexpr int kTmemCols = 256;       // so that two CTAs fit an SM
 constexpr int kSmem = 115712;        // of shared memory, likewise
-constexpr int kBoxBytes = kRows * kTile / 2 * 4;  // h of a tile
+constexpr int kBoxBytes = 2 * kRows * kTile / 2 * 4;  // h of a tile of each group
 // What depends on the weights' type: elements of a stage, rows that stand for one of h
 // and the columns they take (one of x takes as many with MXFP4, one with bf16), bytes of
 // the rows in a stage, and accumulators.
@@ -116,7 +118,7 @@ struct Routing {
 template <int THREADS>
 __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r, uint16_t *table)
 {
-    constexpr int kWarps = THREADS / 32, kEach = kMaxExperts / THREADS;
+    constexpr int kWarps = THREADS / 32, kEach = (kMaxExperts + THREADS - 1) / THREADS;
     __shared__ int s_sum[kWarps], s_hits[kWarps], s_parts[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (n <= 32) {
@@ -224,32 +226,30 @@ __device__ void route(const int32_t *idx, int n, int E, int rows, Routing &r, ui
     __syncthreads();
 }
 
-// The entries' weights, in shared memory.
-__device__ __forceinline__ void load_weights(const float *topk_w, int n, float *to)
-{
-    for (int i = threadIdx.x; i < n; i += blockDim.x) to[i] = __ldg(topk_w + i);
-}
-
-// out[s, o .. o + 3] = sum over the valid entries of s, in increasing k: y [S K, H] holds
-// the experts' rows by entry.  The loads are unconditional, so that eight are under way.
-__device__ __forceinline__ void sum_entries(const float *y, const float *weights,
+// out[s, o .. o + 3] = sum over the valid entries of s, in increasing k, by a whole warp,
+// each lane with its o: y [S K, H] holds the experts' rows by entry.  The loads are
+// unconditional, so that eight are under way; a lane past the row reads its end.
+__device__ __forceinline__ void sum_entries(const float *y, const float *topk_w,
                                             const int16_t *place, int K, int H, int o, int s,
                                             void *out, bool f32)
 {
     constexpr int kAtOnce = 8;
+    const int lane = threadIdx.x & 31, from = min(o, H - 4);
     float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const bool mine = lane < K && place[s * K + lane] >= 0;  // K <= 32
+    const float weight = mine ? __ldg(topk_w + s * K + lane) : 0.0f;
+    const uint32_t valid = __ballot_sync(0xffffffffu, mine);
     for (int k0 = 0; k0 < K; k0 += kAtOnce) {
         float4 v[kAtOnce];
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k)
             v[k] = __ldcg(reinterpret_cast<const float4 *>(
-                y + (int64_t)(s * K + min(k0 + k, K - 1)) * H + o));
+                y + (int64_t)(s * K + min(k0 + k, K - 1)) * H + from));
 #pragma unroll
         for (int k = 0; k < kAtOnce; ++k) {
-            const int i = s * K + min(k0 + k, K - 1);
+            const float w = __shfl_sync(0xffffffffu, weight, (k0 + k) & 31);
             // rows of entries without an expert hold anything
-            if (k0 + k < K && place[i] >= 0) {
-                const float w = weights[i];
+            if (k0 + k < K && (valid >> (k0 + k) & 1)) {
                 sum.x = fmaf(w, v[k].x, sum.x);
                 sum.y = fmaf(w, v[k].y, sum.y);
                 sum.z = fmaf(w, v[k].z, sum.z);
@@ -257,6 +257,7 @@ __device__ __forceinline__ void sum_entries(const float *y, const float *weights
             }
         }
     }
+    if (o >= H) return;
     const int64_t at = (int64_t)s * H + o;
     if (f32) {
         *reinterpret_cast<float4 *>(static_cast<float *>(out) + at) = sum;
@@ -335,7 +336,7 @@ struct SplitArgs {
 };
 
 // A warp takes 256 elements of a token and stores them for its K entries.
-__global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
+__global__ void __launch_bounds__(kSplitThreads) split_kernel(SplitArgs a)
 {
     extern __shared__ int16_t lists[];
     const int n = a.S * a.K;
@@ -343,11 +344,11 @@ __global__ void __launch_bounds__(kThreads) split_kernel(SplitArgs a)
     const int tid = threadIdx.x, lane = tid & 31;
     griddep_wait();
     griddep_launch_dependents();
-    route<kThreads>(a.idx, n, a.E, kRows, rt,
+    route<kSplitThreads>(a.idx, n, a.E, kRows, rt,
                     reinterpret_cast<uint16_t *>(lists + Routing::bytes(n, a.E) / 2));
     const int chunks = (a.H + 255) / 256, words = (a.H + 127) / 128;
-    for (int u = blockIdx.x * (kThreads / 32) + (tid >> 5); u < a.S * chunks;
-         u += gridDim.x * (kThreads / 32)) {
+    for (int u = blockIdx.x * (kSplitThreads / 32) + (tid >> 5); u < a.S * chunks;
+         u += gridDim.x * (kSplitThreads / 32)) {
         const int s = u / chunks, c = u - s * chunks, at = c * 256 + lane * 8;
         const bool in = at < a.H;
         Split sp;
@@ -550,6 +551,7 @@ struct Walk {
 struct Shared {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t acc_full[4], acc_empty[4], drain;
+    uint64_t turn[2];   // a group has read all accumulators of a tile
     uint32_t tmem;
     volatile int stop;
 };
@@ -616,10 +618,9 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     const int stages = a.stages;
-    float *box = reinterpret_cast<float *>(ring + stages * Fo::kStageBytes);  // [8][64]
+    float *box = reinterpret_cast<float *>(ring + stages * Fo::kStageBytes);  // two of [8][64]
     const int n = a.S * a.K;
-    float *weights = box + kBoxBytes / 4;                       // [n]
-    int16_t *valid = reinterpret_cast<int16_t *>(weights + n);  // [S] experts of a token
+    int16_t *valid = reinterpret_cast<int16_t *>(box + kBoxBytes / 4);  // [S] experts of a token
     Routing rt(valid + a.S, n, a.E);
     __shared__ Shared sh;
 
@@ -642,6 +643,8 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
             mbar_init(&sh.acc_full[i], 1);
             mbar_init(&sh.acc_empty[i], 4);
         }
+        mbar_init(&sh.turn[0], 4);
+        mbar_init(&sh.turn[1], 4);
         mbar_init(&sh.drain, 1);
         sh.stop = 0;
         fence_mbar_init();
@@ -658,7 +661,6 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
     // topk_idx, topk_w and the experts' weights were complete when the first one began.
     constexpr bool kFirst = UP && !MX;
     if (kFirst) griddep_wait();
-    if (!UP) load_weights(a.topk_w, n, weights);
     route<kThreads>(a.idx, n, a.E, kRows, rt, reinterpret_cast<uint16_t *>(ring));  // has barriers
     if (!UP) {
         for (int s = tid; s < a.S; s += kThreads) {
@@ -815,43 +817,50 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
         }
         __syncwarp();
     } else if (warp >= 4) {
-        const int q = warp & 3, me = tid - 128;  // this warp's quarter; of 128 threads
-        auto join = [&] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+        // this warp's quarter and group; of the group's 128 threads
+        const int q = warp & 3, group = (warp - 4) >> 2, me = (tid - 128) & 127;
+        box += group * (kBoxBytes / 8);
+        auto join = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
         // whether all four warps go on: one that gave up must not leave the others
         // at their next meeting
         auto agree = [&](bool ok) {
             uint32_t all;
             asm volatile("{\n\t.reg .pred p, q;\n\t"
                          "setp.ne.u32 p, %1, 0;\n\t"
-                         "bar.red.and.pred q, 1, 128, p;\n\t"
+                         "bar.red.and.pred q, %2, 128, p;\n\t"
                          "selp.u32 %0, 1, 0, q;\n\t}"
                          : "=r"(all)
-                         : "r"((uint32_t)ok)
+                         : "r"((uint32_t)ok), "r"(1 + group)
                          : "memory");
             return all != 0;
         };
         if (!kFirst) griddep_wait();
         griddep_launch_dependents();
         if (UP) {
-            for (int i = blockIdx.x * 128 + me; i < a.counters; i += gridDim.x * 128)
+            for (int i = blockIdx.x * 256 + tid - 128; i < a.counters; i += gridDim.x * 256)
                 a.arrived[i] = 0;
         } else {
             // tokens without an expert
             for (int s = blockIdx.x; s < a.S; s += gridDim.x) {
                 if (valid[s]) continue;
-                for (int i = me; i < a.H; i += 128) {
+                for (int i = tid - 128; i < a.H; i += 256) {
                     if (a.f32) reinterpret_cast<float *>(a.out)[(int64_t)s * a.H + i] = 0.0f;
                     else reinterpret_cast<uint16_t *>(a.out)[(int64_t)s * a.H + i] = 0;
                 }
             }
         }
-        int i = 0;  // accumulators read
-        for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const int accumulators = (blocks + a.sum_stages - 1) / a.sum_stages;  // of a tile
+        int i = group * accumulators, taken = 0;
+        for (int t = blockIdx.x + group * gridDim.x; t < tiles;
+             t += 2 * gridDim.x, i += accumulators, ++taken) {
             const Tile c = walk(t);
             float sum[kRows];
 #pragma unroll
             for (int x = 0; x < kRows; ++x) sum[x] = 0.0f;
-            bool ok = true;
+            // Not before the other group has read the tile before: a barrier that is
+            // rounds behind would look as if this round were done.
+            const int turns = taken - 1 + group;
+            bool ok = turns < 0 || wait(&sh.turn[group ^ 1], (uint32_t)turns & 1, &sh.stop);
             for (int b = 0; b < blocks && ok; b += a.sum_stages, ++i) {
                 const int buf = i % kAccs;
                 ok = wait(&sh.acc_full[buf], (uint32_t)(i / kAccs) & 1, &sh.stop);
@@ -892,6 +901,7 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
             }
+            if (lane == 0) mbar_arrive(&sh.turn[group]);
             if (!agree(ok)) break;
             if constexpr (UP) {
                 // the gate of an output here, its up 16 (or 8) lanes on
@@ -929,9 +939,8 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 if (ready) __threadfence();
                 for (; ready; ready &= ready - 1) {
                     const int s = __shfl_sync(0xffffffffu, token, __ffs(ready) - 1);
-                    if (c.m * kTile + 4 * lane < a.H)
-                        sum_entries(a.y, weights, rt.place, a.K, a.H, c.m * kTile + 4 * lane, s,
-                                    a.out, a.f32);
+                    sum_entries(a.y, a.topk_w, rt.place, a.K, a.H, c.m * kTile + 4 * lane, s,
+                                a.out, a.f32);
                 }
             }
         }
@@ -981,7 +990,7 @@ int launch_layer(const LayerMaps &maps, LayerArgs a, cudaStream_t stream)
     static KernelCache kc;
     constexpr int kStageBytes = Form<MX>::kStageBytes;
     const int n = a.S * a.K;
-    const size_t rest = 1024 + kBoxBytes + n * 4 + a.S * 2 + Routing::bytes(n, a.E);
+    const size_t rest = 1024 + kBoxBytes + a.S * 2 + Routing::bytes(n, a.E);
     const int per_tile = UP ? kTile / 2 : kTile;
     const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
     const int64_t most = tiles_m * a.parts, sms = sm_count();
@@ -1081,14 +1090,14 @@ int layer_mxfp4(const LayerCall &c, LayerArgs a, cudaStream_t stream)
                    {3, {H, down_words, E}, {H * 4, down_words * H * 4}, {kTile, 2, 1}});
     if (e == cudaSuccess) e = encode_mx_rows(down, a.h, a.h_scales, a.parts, a.F);
     static KernelCache kc;
-    const size_t smem = Routing::bytes(a.S * a.K, a.E) + (size_t)a.E * (kThreads / 32) * 2;
-    if (e == cudaSuccess) e = prepare_kernel(split_kernel, smem, kThreads, kc, nullptr);
+    const size_t smem = Routing::bytes(a.S * a.K, a.E) + (size_t)a.E * (kSplitThreads / 32) * 2;
+    if (e == cudaSuccess) e = prepare_kernel(split_kernel, smem, kSplitThreads, kc, nullptr);
     if (e == cudaSuccess) {
         const SplitArgs s = {c.x, a.idx, ws + at.x, reinterpret_cast<uint32_t *>(ws + at.x_scales),
                              a.S, a.K, a.E, a.H, a.parts};
         const int64_t units = (int64_t)a.S * ((a.H + 255) / 256), most = 2 * sm_count();
-        const int64_t grid = (units + kThreads / 32 - 1) / (kThreads / 32);
-        e = launch_pdl(split_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(kThreads),
+        const int64_t grid = (units + kSplitThreads / 32 - 1) / (kSplitThreads / 32);
+        e = launch_pdl(split_kernel, dim3((unsigned)(grid < most ? grid : most)), dim3(kSplitThreads),
                        smem, stream, s);
     }
     if (e != cudaSuccess) {
