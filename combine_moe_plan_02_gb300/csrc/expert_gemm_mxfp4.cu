@@ -32,6 +32,14 @@
 // Output.  Lane 32 j + q of the accumulator is output 4 q + j: the four warps that
 // read its quarters meet in shared memory, and whole output rows leave in 16-byte
 // stores, just those of the bucket.
+//
+// What bounds it, 64 buckets of 512 rows, 7168 -> 4096, bf16 out: 291 us (6.6 PFLOP/s; 68 %
+// of the tensor pipe's cycles) with 17.5 TB/s of operands from L2; without the token
+// operand's copies 270, without the stores 265, without the copies of scales 277, with
+// half of the products 265 us.  Buckets of 512 rows on average: 321 us, as columns come
+// in 128s; for seconds on end the power limit makes that 366 to 379.  2048 -> 7168: 197 us,
+// stores (470 MB) and operands.  4 rows in each of 256 buckets, 6144 -> 4096: 323 us (7.0
+// TB/s of weights with 128 tokens of 8 experts, 480 us).
 
 #include "pair.cuh"
 
