@@ -602,7 +602,10 @@ __device__ __forceinline__ void store_h(const LayerArgs &a, const Tile &c, const
             uint32_t u[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                // cut, not rounded: three parts of 8 bits are the whole of an f32, and the
+                // largest of them stay finite
+                const __nv_bfloat162 b = __halves2bfloat162(__float2bfloat16_rz(v[2 * k]),
+                                                            __float2bfloat16_rz(v[2 * k + 1]));
                 u[k] = *reinterpret_cast<const uint32_t *>(&b);
                 const float lo = __low2float(b), hi = __high2float(b);
                 // nothing is left of an infinity

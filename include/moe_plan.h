@@ -548,11 +548,12 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
  *   out[s] = sum over k with topk_idx[s,k] in [0, E) of topk_w[s,k] * w_down[e] h
  *   h      = silu(w_up[e, :F] x[s]) * (w_up[e, F:] x[s]),   e = topk_idx[s,k]
  * Sums and h are f32 and out is rounded once.  bf16 weights: h enters the second
- * product as two bf16 parts, 16 bits of it, or three, all of it, for f32 outputs.
- * MXFP4 weights: x and h enter the products with an error of at most 2^-23 of the
- * largest of 32 neighbours (where that is below 2^-126, as zeros); a token with an
- * infinite x or h gives NaN.  The sum over k is in increasing k.  Ids outside [0, E) give nothing; a
- * token without a valid id gives zeros.  Results are reproducible.
+ * product as three bf16 parts, all 24 bits of it.  MXFP4 weights: x and h enter the
+ * products with an error of at most 2^-23 of the largest of 32 neighbours (where that
+ * is below 2^-126, as zeros).  A token with an infinite x or h, or whose experts have
+ * infinite weights, may give NaN where the formula gives an infinity.  The sum over k
+ * is in increasing k.  Ids outside [0, E) give nothing; a token without a valid id
+ * gives zeros.  Results are reproducible.
  *
  * x         bf16 [S, H]; topk_idx int32 [S, K]; topk_w f32 [S, K]
  * w_dtype   MOE_BF16: w_up [E, 2 F, H], w_down [E, H, F] (gates before ups);

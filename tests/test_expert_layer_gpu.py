@@ -157,6 +157,22 @@ def test_nan_and_infinity_stay_in_their_token(mx):
     assert torch.equal(moe.moe_expert_layer(x, idx, args[2], *bad), moe.moe_expert_layer(x, idx, args[2], *args[3:]))
 
 
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_largest_h(sign):
+    """h = 2^128 - 2^118 is an f32, but above the largest bf16: every step is exact."""
+    import combine_moe_plan_02_gb300 as moe
+    up = torch.zeros(1, 16, 8, device="cuda")
+    up[0, 0, 0], up[0, 0, 1], up[0, 8, 0] = 2.0 ** 101, -2.0 ** 91, sign * 2.0 ** 27
+    down = torch.zeros(1, 8, 8, device="cuda")
+    down[0, 3, 0] = 2.0 ** -100
+    idx = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    out = moe.moe_expert_layer(torch.ones(1, 8, dtype=BF16, device="cuda"), idx, torch.ones(1, 1, device="cuda"),
+                               up.to(BF16), down.to(BF16), out_dtype=F32)
+    want = torch.zeros(1, 8, device="cuda")
+    want[0, 3] = sign * (2.0 ** 28 - 2.0 ** 18)
+    assert torch.equal(out, want)
+
+
 def test_scales_of_every_size():
     """Weights' scales from the smallest to 2^100, among them rows of zeros."""
     import combine_moe_plan_02_gb300 as moe
