@@ -934,8 +934,8 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
 #pragma unroll
                     for (int x = 0; x < kRows; ++x)
                         if (x < c.rows) a.y[(int64_t)rt.order[c.row + x] * a.H + o] = sum[x];
-                __threadfence();
                 join();
+                __threadfence();  // of all four warps' stores, which the join has ordered
                 int token = 0;
                 bool last = false;
                 if (lane < 2 && q + 4 * lane < c.rows) {  // entries q and q + 4
