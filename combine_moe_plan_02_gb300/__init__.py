@@ -623,6 +623,22 @@ def _pointers(*tensors: torch.Tensor):
     return map(_address, tensors)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _run(fn: str, like: torch.Tensor, *args):
+    """The C call on the device that holds `like`: a launch goes to the current
+    device, whatever device its stream is of."""
+    call = getattr(lib(), fn)
+    device = like.get_device()
+    if _current_device() == device:
+        status = call(*args)
+    else:
+        with torch.cuda.device(device):
+            status = call(*args)
+    _abi.check(fn, status)
+
+
 def _check_mx(name: str, codes: torch.Tensor, scales: torch.Tensor):
     """Raises unless codes and scales are what the kernels read; the shape of the
     values."""
@@ -684,8 +700,8 @@ def moe_quant_mxfp4(x: torch.Tensor, *, out: Optional[MxFp4] = None, stream=None
     dt = _values(x, "x", D)
     out = _mx_out(out, lead, rows, D, x.device, stream)
     px, *pout = _pointers(x, *out)
-    _abi.check("moe_quant_mxfp4", lib().moe_quant_mxfp4(
-        px, dt, lead[0] if lead else 1, rows, D, *pout, _stream(stream, x)))
+    _run("moe_quant_mxfp4", x,
+         px, dt, lead[0] if lead else 1, rows, D, *pout, _stream(stream, x))
     return out
 
 
@@ -711,8 +727,8 @@ def moe_dispatch_quant_mxfp4(x: torch.Tensor, tok_map: torch.Tensor, *,
         if width != [D]:
             raise ValueError("out must hold rows of D elements")
     px, pmap, *pout = _pointers(x, tok_map, *out)
-    _abi.check("moe_dispatch_quant_mxfp4", lib().moe_dispatch_quant_mxfp4(
-        px, dt, S, D, K, pmap, *pout, rows, _stream(stream, x)))
+    _run("moe_dispatch_quant_mxfp4", x,
+         px, dt, S, D, K, pmap, *pout, rows, _stream(stream, x))
     return out
 
 
@@ -727,8 +743,8 @@ def moe_swiglu_quant_mxfp4(u: torch.Tensor, *, out: Optional[MxFp4] = None,
     dt = _values(u, "u", F)
     out = _mx_out(out, (), rows, F, u.device, stream)
     pu, *pout = _pointers(u, *out)
-    _abi.check("moe_swiglu_quant_mxfp4", lib().moe_swiglu_quant_mxfp4(
-        pu, dt, rows, F, *pout, _stream(stream, u)))
+    _run("moe_swiglu_quant_mxfp4", u,
+         pu, dt, rows, F, *pout, _stream(stream, u))
     return out
 
 
@@ -739,9 +755,9 @@ def moe_dequant_mxfp4(q: MxFp4, *, out_dtype: torch.dtype = torch.bfloat16,
     shape = _check_mx("q", codes, scales)
     out, dt = _float_out(out, shape, out_dtype, codes.device, stream)
     pcodes, pscales, pout = _pointers(codes, scales, out)
-    _abi.check("moe_dequant_mxfp4", lib().moe_dequant_mxfp4(
-        pcodes, pscales, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], pout, dt,
-        _stream(stream, codes)))
+    _run("moe_dequant_mxfp4", codes,
+         pcodes, pscales, shape[0] if len(shape) == 3 else 1, shape[-2], shape[-1], pout, dt,
+         _stream(stream, codes))
     return out
 
 
@@ -760,8 +776,8 @@ def moe_expert_gemm_mxfp4(x: MxFp4, w: MxFp4, plan: Union[Plan, CapacityPlan], *
     _check_plan(plan, E)
     out, dt = _float_out(out, (rows, N), out_dtype, codes.device, stream)
     pc, ps, pwc, pws, pcnt, poff, pout = _pointers(codes, scales, *w, plan.cnt, plan.off, out)
-    _abi.check("moe_expert_gemm_mxfp4", lib().moe_expert_gemm_mxfp4(
-        pc, ps, rows, pwc, pws, N, D, E, pcnt, poff, pout, dt, _stream(stream, codes)))
+    _run("moe_expert_gemm_mxfp4", codes,
+         pc, ps, rows, pwc, pws, N, D, E, pcnt, poff, pout, dt, _stream(stream, codes))
     return out
 
 
@@ -812,8 +828,8 @@ def moe_expert_layer(x: torch.Tensor, topk_idx: torch.Tensor, topk_w: torch.Tens
     else:
         px, pidx, pw, pout, pws, pup, pdown = _pointers(x, topk_idx, topk_w, out, ws, w_up, w_down)
         weights = pup, None, pdown, None
-    _abi.check("moe_expert_layer", L.moe_expert_layer(
-        px, S, H, pidx, pw, K, E, F, kind, *weights, pout, dt, pws, nws, _stream(stream, x)))
+    _run("moe_expert_layer", x,
+         px, S, H, pidx, pw, K, E, F, kind, *weights, pout, dt, pws, nws, _stream(stream, x))
     return out
 
 

@@ -183,3 +183,33 @@ def test_product_binding_refuses():
         moe.moe_expert_gemm_mxfp4(rows, w, plan, out_dtype=torch.float16)
     with pytest.raises(ValueError):
         moe.moe_expert_gemm_mxfp4(rows, w, plan, out=torch.zeros(8, 32))
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """A call whose tensors are on another device than the current one switches to it."""
+    import contextlib
+
+    import combine_moe_plan_02_gb300 as moe
+    seen, entered = [], []
+
+    class Fake:
+        def moe_fake(self, *args):
+            seen.append((args, bool(entered)))
+            return 0
+
+    class Tensor:
+        def get_device(self):
+            return 2
+
+    @contextlib.contextmanager
+    def device(index):
+        entered.append(index)
+        yield
+        entered.clear()
+
+    monkeypatch.setattr(moe, "lib", Fake)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    for current, switched in ((2, False), (0, True)):
+        monkeypatch.setattr(moe, "_current_device", lambda: current)
+        moe._run("moe_fake", Tensor(), 1, 2)
+        assert seen.pop() == ((1, 2), switched) and not entered
