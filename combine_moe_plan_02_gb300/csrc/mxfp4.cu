@@ -22,8 +22,8 @@
 // Bound by memory: 4096 x 7168 bf16 rows into 8 buckets each 34 us (5.4 TB/s of reads and
 // scattered rows of codes), their values as bf16 92 us (6.4 TB/s, stores of whole lines;
 // 115 us with 32 bytes a lane), 180 M f32 weights 127 us (6.4 TB/s), the activation of
-// 32768 x 4096 48 us (6.3 TB/s).  With 64-bit divisions for each unit instead of the walk
-// the dispatch took 37, the weights 132 and the activation 59 us.
+// 32768 x 4096 47.6 us (6.4 TB/s; f32 78 us, 7.3 TB/s).  With 64-bit divisions for each
+// unit instead of the walk the dispatch took 37, the weights 132 and the activation 59 us.
 
 #include "common.cuh"
 
@@ -97,6 +97,31 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *f)
     return r;
 }
 
+// The fast division gives 0 for divisors above 2^126, which 1 + exp(-gate) is below a gate
+// of -87.3, and exp(-gate) itself leaves f32 at -88.7.
+constexpr float kFarGate = -80.0f;
+
+// h = silu(gate) * up of such gates: gate exp(gate) up, as 1 + exp(-gate) is exp(-gate) to
+// 115 bits, with the exponential in two halves, one on either side of `up`, so that no step
+// leaves f32 before the result does.  Off by 2^-20, or 2^-16 below -174, where a half is
+// subnormal.  The gates are read again, one by one: they are rare, and kept until here they
+// would cost all others registers.  (32768 x 2048 bf16: 47.6 us with and without; with halves
+// for every gate instead 52 us.)
+template <typename T>
+__device__ __forceinline__ void far_gates(const T *gates, uint32_t F, float (&h)[kLane])
+{
+#pragma unroll 1
+    for (int i = 0; i < kLane; ++i) {
+        const float gate = (float)gates[i];
+        if (gate >= kFarGate || isnan(gate)) continue;
+        const float half = expf(0.5f * gate);
+        const float v = gate * half * (float)gates[F + i] * half;
+#pragma unroll
+        for (int k = 0; k < kLane; ++k)
+            if (k == i) h[k] = v;
+    }
+}
+
 // A walk over (row, chunk) by all warps of the grid, without a division in it.
 struct Walk {
     uint32_t row, chunk, chunks, rows_on, chunks_on;
@@ -140,19 +165,26 @@ __global__ void __launch_bounds__(kThreads) quant_kernel(QuantArgs a)
             const uint8_t *p = a.x + ((int64_t)s * (GATED ? 2 * D : D) + e0) * (int)sizeof(T);
             Sixteen<T>::load(p, f);
             if (GATED) {
-                // f32 with the fast exponential and division: a few units in the
-                // last place of 24 bits (2^-17 where exp(-gate) is 2^100), where
-                // the codes that follow keep two bits
-                float up[kLane];
+                // f32 with the fast exponential and division: a few units in the last
+                // place of 24 bits (2^-16 at a gate of -80), where the codes that
+                // follow keep two bits
+                float up[kLane], low = 0.0f;
                 Sixteen<T>::load(p + (int64_t)D * (int)sizeof(T), up);
 #pragma unroll
-                for (int i = 0; i < kLane; ++i)
+                for (int i = 0; i < kLane; ++i) {
+                    low = fminf(low, f[i]);
                     f[i] = __fdividef(f[i], 1.0f + __expf(-f[i])) * up[i];
+                }
+                if (low < kFarGate) far_gates(reinterpret_cast<const T *>(p), D, f);
             }
         }
-        uint32_t top = 0;  // of the magnitudes' patterns; a NaN's is above them all
+        float most = 0.0f;  // of the magnitudes; NaN if one is
 #pragma unroll
-        for (int i = 0; i < kLane; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+        for (int i = 0; i < kLane; i += 2)
+            asm("max.NaN.f32 %0, %1, %2, %3;"
+                : "=f"(most)
+                : "f"(most), "f"(fabsf(f[i])), "f"(fabsf(f[i + 1])));
+        uint32_t top = __float_as_uint(most);  // patterns of magnitudes: a NaN's is above all
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         const int e = (int)(top >> 23);
         const uint32_t byte = e == 255 ? 255u : (uint32_t)max(e - 2, 0);

@@ -502,7 +502,8 @@ int moe_expert_gemm_wgrad(const void *dy, const void *x, int64_t rows, int64_t N
  *       [-1, packed_rows) is skipped and flagged (bit 1); other rows are left
  *       untouched
  *   moe_swiglu_quant_mxfp4    u [rows, 2 F], gates before ups:
- *       h[r, f] = u[r, f] / (1 + exp(-u[r, f])) * u[r, F + f] in f32, quantised
+ *       h[r, f] = u[r, f] / (1 + exp(-u[r, f])) * u[r, F + f] in f32, to 2^-16 of
+ *       itself, quantised; exp(-u) beyond f32's range does not cut h off
  *   moe_dequant_mxfp4         the values, [groups, rows, D] of out_dtype (exact
  *       where the value is in the type's range)
  *
