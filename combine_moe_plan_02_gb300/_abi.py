@@ -59,6 +59,7 @@ SIGNATURES = {
                                P]),
     "moe_device_errors": (I32, [P]),
     "moe_selftest_wait_timeout": (I32, [I64, P]),
+    "moe_selftest_warp_wait": (I32, [I64, I64, I64, P, P]),
     "moe_selftest_convert": (I32, [ctypes.c_uint32, I64, P, P, P]),
 }
 

@@ -500,60 +500,58 @@ expert_kernel(const __grid_constant__ Maps<MODE> maps, ExpertArgs a)
             }
             __syncwarp();
         } else if (warp == 1 && rank == 0) {
-            Ring r(stages);
-            int i = -1;  // accumulators begun, less one
-            bool ok = true;
-            // an accumulator that the storing warps have read
-            auto begin = [&] {
-                ++i;
-                if (i >= 2 && !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop))
-                    return false;
-                tc_fence_after();
-                return true;
-            };
-            auto end = [&] {
-                if (elect_one()) mma_commit(&sh.acc_full[i & 1], lead);
-                __syncwarp();
-            };
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                Tile c = tile_of<MODE>(a, sched, t);
-                if (SPLIT) take_part(c, part, split);
-                if (!begin()) break;
-                const int cols = ceil_div(c.n, kStep) * kStep;
-                const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
-                const int parts = reduction_parts<Tout, LONG>(c.blocks);
-                int p = 1, from = 0, until = c.blocks / parts;  // blocks of part 1
-                for (int b = 0; b < c.blocks; ++b) {
-                    if ((sizeof(Tout) == 4 || LONG) && b == until) {
-                        end();
-                        ++p;
-                        from = until;
-                        until = (int)((int64_t)c.blocks * p / parts);
-                        ok = begin();
-                        if (!ok) break;
-                    }
-                    if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t *sa = ring + r.at * stage_bytes;
-                    const int len = b + 1 == c.blocks ? c.last : kK;
-                    const int steps = ceil_div(len, 16);
+            // One thread waits and issues: lanes of a warp could give up a wait apart.
+            if (elect_one()) {
+                Ring r(stages);
+                int i = -1;  // accumulators begun, less one
+                bool ok = true;
+                // an accumulator that the storing warps have read
+                auto begin = [&] {
+                    ++i;
+                    if (i >= 2 &&
+                        !wait(&sh.acc_empty[i & 1], (uint32_t)(i / 2 - 1) & 1, &sh.stop))
+                        return false;
                     tc_fence_after();
-                    if (elect_one()) {
+                    return true;
+                };
+                auto end = [&] { mma_commit(&sh.acc_full[i & 1], lead); };
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                    Tile c = tile_of<MODE>(a, sched, t);
+                    if (SPLIT) take_part(c, part, split);
+                    if (!begin()) break;
+                    const int cols = ceil_div(c.n, kStep) * kStep;
+                    const uint32_t idesc = instr_desc(cols, kAMn, kBMn);
+                    const int parts = reduction_parts<Tout, LONG>(c.blocks);
+                    int p = 1, from = 0, until = c.blocks / parts;  // blocks of part 1
+                    for (int b = 0; b < c.blocks; ++b) {
+                        if ((sizeof(Tout) == 4 || LONG) && b == until) {
+                            end();
+                            ++p;
+                            from = until;
+                            until = (int)((int64_t)c.blocks * p / parts);
+                            ok = begin();
+                            if (!ok) break;
+                        }
+                        if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
+                            ok = false;
+                            break;
+                        }
+                        uint8_t *sa = ring + r.at * stage_bytes;
+                        const int len = b + 1 == c.blocks ? c.last : kK;
+                        const int steps = ceil_div(len, 16);
+                        tc_fence_after();
                         const uint64_t da = operand_desc(smem_u32(sa), kAMn);
                         const uint64_t db = operand_desc(smem_u32(sa + kABytes), kBMn);
                         for (int s = 0; s < steps; ++s)
                             mma_bf16(tmem + (i & 1) * kN, da + s * (kAMn ? 128 : 2),
                                      db + s * (kBMn ? 128 : 2), idesc, b > from || s > 0);
                         mma_commit(&sh.empty[r.at], lead);
+                        r.next();
                     }
-                    __syncwarp();
-                    r.next();
+                    if (ok) end();
                 }
-                if (ok) end();
+                mma_commit(&sh.drain, lead);  // nothing is issued after this
             }
-            if (elect_one()) mma_commit(&sh.drain, lead);  // nothing is issued after this
             __syncwarp();
         } else if (warp == 3 && MODE != kWeightGrad) {
             zero_gaps(a.out, (int64_t)a.M * (int)sizeof(Tout), a.rows, a.cnt, a.off, a.E,
@@ -580,10 +578,11 @@ expert_kernel(const __grid_constant__ Maps<MODE> maps, ExpertArgs a)
                 asm volatile("bar.sync %0, %1;" ::"r"(1 + odd), "n"(32 * JOIN) : "memory");
         };
         // whether all of them go on: one that gave up must not leave the others
-        // at their next meeting
+        // at their next meeting.  Lanes may leave a wait apart, and meet as whole warps.
         auto agree = [&](bool ok) {
-            if (JOIN == 1) return ok;
+            if (JOIN == 1) return (bool)__all_sync(0xffffffffu, ok);
             uint32_t all;
+            __syncwarp();
             asm volatile("{\n\t.reg .pred p, q;\n\t"
                          "setp.ne.u32 p, %1, 0;\n\t"
                          "bar.red.and.pred q, %2, %3, p;\n\t"
@@ -641,7 +640,7 @@ expert_kernel(const __grid_constant__ Maps<MODE> maps, ExpertArgs a)
                 bool ok = true;
                 for (int p = c.n ? reduction_parts<Tout, LONG>(c.blocks) : 0; p > 0 && ok; --p, ++i) {
                     const int buf = i & 1;
-                    ok = wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
+                    ok = wait_warp(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
                     if (!ok) break;
                     tc_fence_after();
                     uint32_t v[32];
@@ -726,7 +725,7 @@ expert_kernel(const __grid_constant__ Maps<MODE> maps, ExpertArgs a)
                 bool ok = true;
                 for (int p = 0; p < parts; ++p, ++i) {
                     const int buf = i & 1;
-                    ok = wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
+                    ok = wait_warp(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t acc =

@@ -406,9 +406,10 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
             asm volatile("bar.sync %0, %1;" ::"r"(1 + odd), "n"(128) : "memory");
         };
         // whether all four warps go on: one that gave up must not leave the others
-        // at their next meeting
+        // at their next meeting.  Lanes may leave a wait apart, and meet as whole warps.
         auto agree = [&](bool ok) {
             uint32_t all;
+            __syncwarp();
             asm volatile("{\n\t.reg .pred p, q;\n\t"
                          "setp.ne.u32 p, %1, 0;\n\t"
                          "bar.red.and.pred q, %2, %3, p;\n\t"

@@ -830,9 +830,10 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
         box += group * (kBoxBytes / 8);
         auto join = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + group) : "memory"); };
         // whether all four warps go on: one that gave up must not leave the others
-        // at their next meeting
+        // at their next meeting; the meeting is one of whole warps
         auto agree = [&](bool ok) {
             uint32_t all;
+            __syncwarp();
             asm volatile("{\n\t.reg .pred p, q;\n\t"
                          "setp.ne.u32 p, %1, 0;\n\t"
                          "bar.red.and.pred q, %2, 128, p;\n\t"
@@ -868,10 +869,10 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
             // Not before the other group has read the tile before: a barrier that is
             // rounds behind would look as if this round were done.
             const int turns = taken - 1 + group;
-            bool ok = turns < 0 || wait(&sh.turn[group ^ 1], (uint32_t)turns & 1, &sh.stop);
+            bool ok = turns < 0 || wait_warp(&sh.turn[group ^ 1], (uint32_t)turns & 1, &sh.stop);
             for (int b = 0; b < blocks && ok; b += a.sum_stages, ++i) {
                 const int buf = i % kAccs;
-                ok = wait(&sh.acc_full[buf], (uint32_t)(i / kAccs) & 1, &sh.stop);
+                ok = wait_warp(&sh.acc_full[buf], (uint32_t)(i / kAccs) & 1, &sh.stop);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAcc;

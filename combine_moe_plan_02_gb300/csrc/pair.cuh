@@ -179,7 +179,8 @@ __device__ __forceinline__ uint64_t now_ns()
 
 // Waits for phase `parity`; false once the limit ran out here or, with
 // `stop`, in another warp of the CTA.
-__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop)
+__device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const volatile int *stop,
+                                          uint64_t limit = kWaitLimitNs)
 {
     // reading the timer costs about as much as a block of products: probe
     // first
@@ -189,16 +190,27 @@ __device__ __forceinline__ bool wait_slow(uint64_t *bar, uint32_t parity, const 
             if (mbar_try_wait(bar, parity)) return true;
         const uint64_t t = now_ns();
         if (t0 == 0) t0 = t;
-        if ((stop && *stop) || t - t0 > kWaitLimitNs) return false;
+        if ((stop && *stop) || t - t0 > limit) return false;
     }
 }
 
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *stop)
+// For one thread: the answer is that of the thread that asks.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *stop,
+                                     uint64_t limit = kWaitLimitNs)
 {
     if (mbar_try_wait(bar, parity)) return true;
-    if (wait_slow(bar, parity, stop)) return true;
+    if (wait_slow(bar, parity, stop, limit)) return true;
     *stop = 1;
     return false;
+}
+
+// For a whole warp: lanes probe and look at the clock and at `stop` each for itself, so
+// some could give up where others see the phase complete.  All go on here or none, and
+// together, as the instructions of a whole warp (.aligned) that follow a wait ask.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *stop,
+                                          uint64_t limit = kWaitLimitNs)
+{
+    return __all_sync(0xffffffffu, wait(bar, parity, stop, limit));
 }
 
 // A place in the ring and the parity of its current round.

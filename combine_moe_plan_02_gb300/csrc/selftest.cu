@@ -8,8 +8,11 @@
 // "Draft: cco + flydsl dispatch/combine #448", Fp8BlockwiseQuant notes (the
 // fp8 cast of each scaled element) and accumulator note (bf16 rows widened
 // to f32, summed, stored back).
+//
+// And of the wait that the tcgen05 kernels' warps share (csrc/pair.cuh): lanes that would
+// give up by themselves at different times must all get one answer.
 
-#include "common.cuh"
+#include "pair.cuh"
 
 #include <cuda_fp8.h>
 
@@ -43,10 +46,46 @@ __global__ void selftest_convert_kernel(uint32_t first, int64_t groups, uint8_t 
     }
 }
 
+// Warp 0 waits for a phase that warp 1 completes `complete` ns after the start (never if
+// negative); its second half begins `late` ns late.
+__global__ void __launch_bounds__(64)
+selftest_warp_wait_kernel(uint64_t limit, int64_t complete, int64_t late, int32_t *answers)
+{
+    __shared__ uint64_t bar;
+    __shared__ volatile int stop;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        mbar_init(&bar, 1);
+        stop = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const uint64_t start = now_ns();
+    const int64_t delay = threadIdx.x < 32 ? (lane < 16 ? 0 : late) : complete;
+    // at most 2e8 ns by the host's check
+    while ((int64_t)(now_ns() - start) < delay) __nanosleep(200);
+    if (threadIdx.x < 32) answers[lane] = wait_warp(&bar, 0, &stop, limit);
+    else if (lane == 0 && complete >= 0) mbar_arrive(&bar);
+    __syncthreads();
+}
+
 } // namespace
 } // namespace moe
 
 using namespace moe;
+
+MOE_EXPORT int moe_selftest_warp_wait(int64_t limit_ns, int64_t complete_ns, int64_t late_ns,
+                                      int32_t *answers, moe_stream_t stream)
+{
+    MOE_TRACE("moe_selftest_warp_wait");
+    const int64_t most = 100000000;
+    if (limit_ns < 1000 || limit_ns > most || complete_ns < -1 || complete_ns > 2 * most ||
+        late_ns < 0 || late_ns > 2 * most || !answers)
+        return MOE_EINVAL;
+    selftest_warp_wait_kernel<<<1, 64, 0, (cudaStream_t)stream>>>((uint64_t)limit_ns, complete_ns,
+                                                                  late_ns, answers);
+    return check_launch();
+}
 
 MOE_EXPORT int moe_selftest_convert(uint32_t first, int64_t count, uint8_t *e4m3_out,
                                     uint16_t *bf16_out, moe_stream_t stream)

@@ -120,6 +120,15 @@ int moe_device_errors(uint32_t *flags);
  * CUDA context stays usable.  Asynchronous on `stream`. */
 int moe_selftest_wait_timeout(int64_t limit_ns, moe_stream_t stream);
 
+/* Self-test of the wait that the warps of the experts' products and the layer share: a
+ * warp waits, at most limit_ns (1e3 .. 1e8), for a phase that another one completes
+ * complete_ns after the start (0 .. 2e8; -1: never); half of its lanes begin late_ns
+ * later (0 .. 2e8).  answers: DEVICE pointer to 32 int32, 1 for a lane that saw the phase
+ * complete and goes on, 0 for one that gave up; all lanes agree.  Sets no error bit;
+ * asynchronous on `stream`. */
+int moe_selftest_warp_wait(int64_t limit_ns, int64_t complete_ns, int64_t late_ns,
+                           int32_t *answers, moe_stream_t stream);
+
 /* Self-test of the number-format conversions the kernels use [mori #448:
  * Fp8BlockwiseQuant notes (the fp8 cast of each scaled element) and the
  * accumulator note (f32 sums stored back as bf16)]: for i in [0, count) the
