@@ -60,6 +60,7 @@ SIGNATURES = {
     "moe_device_errors": (I32, [P]),
     "moe_selftest_wait_timeout": (I32, [I64, P]),
     "moe_selftest_warp_wait": (I32, [I64, I64, I64, P, P]),
+    "moe_selftest_layer_ctas": (I32, [I64, I64, I32, I32, I64, I32, P]),
     "moe_selftest_convert": (I32, [ctypes.c_uint32, I64, P, P, P]),
 }
 

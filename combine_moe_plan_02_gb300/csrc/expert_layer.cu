@@ -66,7 +66,6 @@ constexpr int kScales = 2 * 512;     // of 128 rows in a stage, or places for th
 constexpr int kMaxStages = 10;
 constexpr int kScaleAt = 128;        // first TMEM column of the scales, after the accumulators
 constexpr int kTmemCols = 256;       // so that two CTAs fit an SM
-constexpr int kSmem = 115712;        // of shared memory, likewise
 constexpr int kBoxBytes = 2 * kRows * kTile / 2 * 4;  // h of a tile of each group
 // What depends on the weights' type: elements of a stage, rows that stand for one of h
 // and the columns they take (one of x takes as many with MXFP4, one with bf16), bytes of
@@ -993,35 +992,82 @@ constexpr CUtensorMapDataType kBytes = CU_TENSOR_MAP_DATA_TYPE_UINT8;
 constexpr CUtensorMapDataType kWords = CU_TENSOR_MAP_DATA_TYPE_UINT32;
 constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
 
-template <bool MX, bool UP>
-int launch_layer(const LayerMaps &maps, LayerArgs a, cudaStream_t stream)
+// Shared memory of one of two CTAs in an SM, which has 228 KB and keeps 1 KB for each,
+// less what the kernel declares: its barriers, and three sums of each warp from the ranking.
+constexpr size_t kSmem =
+    (228 << 10) / 2 - 1024 - sizeof(Shared) - 3 * (kThreads / 32) * sizeof(int);
+
+struct LaunchShape {
+    int stages, ctas;   // ctas: of an SM
+    size_t smem;
+    int64_t tiles;      // at most
+};
+
+template <bool MX, bool UP> LaunchShape launch_shape(const LayerArgs &a)
 {
-    static KernelCache kc;
     constexpr int kStageBytes = Form<MX>::kStageBytes;
-    const int n = a.S * a.K;
-    const size_t rest = 1024 + kBoxBytes + a.S * 2 + Routing::bytes(n, a.E);
+    const size_t rest = 1024 + kBoxBytes + a.S * 2 + Routing::bytes(a.S * a.K, a.E);
     const int per_tile = UP ? kTile / 2 : kTile;
-    const int64_t tiles_m = ((UP ? a.F : a.H) + per_tile - 1) / per_tile;
-    const int64_t most = tiles_m * a.parts, sms = sm_count();
+    LaunchShape r;
+    r.tiles = (int64_t)(((UP ? a.F : a.H) + per_tile - 1) / per_tile) * a.parts;
     // Two CTAs of an SM have four or five stages each.  Where the lists leave less, or
     // there is no work for two, one CTA has more of them (5 tokens of 24 experts, 1416,
     // 520, bf16: 21.1 -> 19.1 us).
     const int least = MX ? 4 : 5;
-    a.stages = (int)((kSmem - rest) / kStageBytes);
-    const int ctas = a.stages < least || most <= sms ? 1 : 2;
-    if (ctas == 1) a.stages = MX ? 7 : 9;
-    const size_t smem = rest + (size_t)a.stages * kStageBytes;
-    cudaError_t e = prepare_kernel(layer_kernel<MX, UP>, smem, kThreads, kc, nullptr);
+    r.stages = (int)((kSmem - rest) / kStageBytes);
+    r.ctas = r.stages < least || r.tiles <= sm_count() ? 1 : 2;
+    if (r.ctas == 1) r.stages = MX ? 7 : 9;
+    r.smem = rest + (size_t)r.stages * kStageBytes;
+    return r;
+}
+
+template <bool MX, bool UP>
+int launch_layer(const LayerMaps &maps, LayerArgs a, cudaStream_t stream)
+{
+    static KernelCache kc;
+    const LaunchShape l = launch_shape<MX, UP>(a);
+    a.stages = l.stages;
+    cudaError_t e = prepare_kernel(layer_kernel<MX, UP>, l.smem, kThreads, kc, nullptr);
     if (e == cudaSuccess) {
-        const int64_t room = sms * ctas;
-        e = launch_pdl(layer_kernel<MX, UP>, dim3((unsigned)(most < room ? most : room)),
-                       dim3(kThreads), smem, stream, maps, a);
+        const int64_t room = (int64_t)sm_count() * l.ctas;
+        e = launch_pdl(layer_kernel<MX, UP>, dim3((unsigned)(l.tiles < room ? l.tiles : room)),
+                       dim3(kThreads), l.smem, stream, maps, a);
     }
     if (e != cudaSuccess) {
         set_cuda_error(e);
         return MOE_ECUDA;
     }
     return check_launch();
+}
+
+// The CTAs of an SM that a call's launch counts on, and those that fit one by their shared
+// memory, registers, threads and tensor memory.  (The runtime's own count of CTAs is 1 for
+// any kernel that allocates tensor memory.)
+template <bool MX, bool UP> int launch_ctas(const LayerArgs &a, int32_t *counts)
+{
+    const LaunchShape l = launch_shape<MX, UP>(a);
+    cudaFuncAttributes f;
+    int dev = 0, smem = 0, kept = 0, regs = 0, threads = 0;
+    cudaError_t e = cudaFuncGetAttributes(&f, layer_kernel<MX, UP>);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    auto ask = [&](int *v, cudaDeviceAttr attr) {
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(v, attr, dev);
+    };
+    ask(&smem, cudaDevAttrMaxSharedMemoryPerMultiprocessor);
+    ask(&kept, cudaDevAttrReservedSharedMemoryPerBlock);
+    ask(&regs, cudaDevAttrMaxRegistersPerMultiprocessor);
+    ask(&threads, cudaDevAttrMaxThreadsPerMultiProcessor);
+    if (e != cudaSuccess) {
+        set_cuda_error(e);
+        return MOE_ECUDA;
+    }
+    int64_t most = smem / (round_up(f.sharedSizeBytes + l.smem, 128) + kept);
+    const int64_t limits[3] = {regs / (round_up(f.numRegs, 8) * kThreads), threads / kThreads,
+                               512 / kTmemCols};
+    for (int64_t v : limits) most = v < most ? v : most;
+    counts[0] = l.ctas;
+    counts[1] = (int32_t)most;
+    return MOE_OK;
 }
 
 // Parts of n entries: one for every eight of an expert and one for what is left.
@@ -1168,6 +1214,24 @@ MOE_EXPORT size_t moe_expert_layer_workspace_size(int64_t S, int64_t H, int K, i
 {
     if (!in_range(S, H, K, E, F) || (w_dtype != MOE_BF16 && w_dtype != MOE_MXFP4)) return 0;
     return (size_t)Places(w_dtype == MOE_MXFP4, S, K, E, H, F).bytes;
+}
+
+MOE_EXPORT int moe_selftest_layer_ctas(int64_t S, int64_t H, int K, int E, int64_t F, int w_dtype,
+                                       int32_t *counts)
+{
+    if (!in_range(S, H, K, E, F) || S < 1 || (w_dtype != MOE_BF16 && w_dtype != MOE_MXFP4) || !counts)
+        return MOE_EINVAL;
+    LayerArgs a = {};
+    a.S = (int)S;
+    a.K = K;
+    a.E = E;
+    a.H = (int)H;
+    a.F = (int)F;
+    a.parts = (int)most_parts(S * K, E);
+    const bool mx = w_dtype == MOE_MXFP4;
+    const int r = mx ? launch_ctas<true, true>(a, counts) : launch_ctas<false, true>(a, counts);
+    if (r != MOE_OK) return r;
+    return mx ? launch_ctas<true, false>(a, counts + 2) : launch_ctas<false, false>(a, counts + 2);
 }
 
 MOE_EXPORT int moe_expert_layer(const void *x, int64_t S, int64_t H, const int32_t *topk_idx,

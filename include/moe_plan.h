@@ -129,6 +129,12 @@ int moe_selftest_wait_timeout(int64_t limit_ns, moe_stream_t stream);
 int moe_selftest_warp_wait(int64_t limit_ns, int64_t complete_ns, int64_t late_ns,
                            int32_t *answers, moe_stream_t stream);
 
+/* Self-test of the layer's launches (moe_expert_layer of these sizes; no work is
+ * enqueued).  counts: HOST pointer to 4 int32: the CTAs of an SM that the first product's
+ * grid counts on, how many fit one, and the same for the second. */
+int moe_selftest_layer_ctas(int64_t S, int64_t H, int K, int E, int64_t F, int w_dtype,
+                            int32_t *counts);
+
 /* Self-test of the number-format conversions the kernels use [mori #448:
  * Fp8BlockwiseQuant notes (the fp8 cast of each scaled element) and the
  * accumulator note (f32 sums stored back as bf16)]: for i in [0, count) the
