@@ -34,7 +34,7 @@
 // row is the block rounded to multiples of 2^(e - 1) and less (values up to 4 units,
 // steps of at most one), the next what that left (at most half a unit) in units of
 // 2^(e - 4), and so on, each three bits further.  The eighth leaves at most 2^-23 of a,
-// about what an f32 sum does.  Each row is a column of the product, and the columns' sums
+// about what an f32 sum does, or 2^-129 where the scales end.  Each row is a column of the product, and the columns' sums
 // are added in f32.  Decoding the weights to f16 in registers for the warp-wide
 // instruction instead takes 2.7 instructions a weight: 70 us for one token of 8
 // experts (6144, 2048) and 2290 us for 32 tokens of 64 (7168, 2048).
@@ -278,7 +278,8 @@ __device__ __forceinline__ void sum_entries(const float *y, const float *topk_w,
 
 // Eight neighbouring values, four lanes a block of 32: the codes of row p (one
 // word) and the block's scale byte.  `byte` is that of row 0, 255 where the block
-// has an infinity or a NaN; rows whose scale would be below 2^-127 are zero.
+// has an infinity or a NaN.  Rows whose scale would be below 2^-127 take that: what is
+// left then is two units at most, of which the first of them leaves a quarter.
 struct Split {
     float v[8];
     int byte;
@@ -295,15 +296,14 @@ struct Split {
     }
     __device__ __forceinline__ int scale(int p) const
     {
-        return byte == 255 ? (p ? 0 : 255) : max(byte - 3 * p, 0);
+        return byte == 255 ? (p ? 0 : 255) : max(byte - 3 * p, 0);  // E8M0 ends at 2^-127
     }
     __device__ __forceinline__ uint32_t next(int p)
     {
         if (byte == 255) return p ? 0 : 0x22222222u;  // ones, times NaN
-        if (byte - 3 * p < 0) return 0;
-        const float inv = __uint_as_float((uint32_t)(254 - (byte - 3 * p)) << 23);
-        const float unit = byte - 3 * p ? __uint_as_float((uint32_t)(byte - 3 * p) << 23)
-                                        : __uint_as_float(0x00400000u);
+        const uint32_t exponent = (uint32_t)max(byte - 3 * p, 0);
+        const float inv = __uint_as_float((254u - exponent) << 23);
+        const float unit = __uint_as_float(exponent ? exponent << 23 : 0x00400000u);
         uint32_t word = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

@@ -565,8 +565,8 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
  *   h      = silu(w_up[e, :F] x[s]) * (w_up[e, F:] x[s]),   e = topk_idx[s,k]
  * Sums and h are f32 and out is rounded once.  bf16 weights: h enters the second
  * product as three bf16 parts, all 24 bits of it.  MXFP4 weights: x and h enter the
- * products with an error of at most 2^-23 of the largest of 32 neighbours (where that
- * is below 2^-126, as zeros).  A token with an infinite x or h, or whose experts have
+ * products with an error of at most 2^-23 of the largest of 32 neighbours, or 2^-129
+ * where that is more.  A token with an infinite x or h, or whose experts have
  * infinite weights, may give NaN where the formula gives an infinity.  The sum over k
  * is in increasing k.  Ids outside [0, E) give nothing; a token without a valid id
  * gives zeros.  Results are reproducible.
