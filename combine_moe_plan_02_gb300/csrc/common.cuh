@@ -315,30 +315,43 @@ __device__ __forceinline__ void st16(void *p, uint4 v)
 
 // Clears the rows that hold no entry: from cnt[e] filled rows to the end of
 // each bucket, and from off[E] to `rows`.  Called by whole warps; warp gw of W
-// takes every W-th such row.  Bounds are clamped to the buffer.
+// takes every W-th such row.  A bucket that begins outside the buffer has no such rows:
+// those up to the next one that begins inside are the bucket's before.
 __device__ __forceinline__ void zero_gaps(uint8_t *base, int64_t row_bytes, int64_t rows,
                                           const int32_t *cnt, const int64_t *off, int E, int gw,
                                           int W)
 {
     const int lane = threadIdx.x & 31;
+    const uint32_t none = (uint32_t)rows + 1;  // a start outside; rows are below 2^31
+    auto start = [&](int e) {
+        const uint64_t o = (uint64_t)__ldg(off + e);
+        return o < none ? (uint32_t)o : none;
+    };
     int64_t seen = 0;        // such rows in the groups before
     int64_t next = gw;       // the next one that this warp clears
     constexpr int kAhead = 4;  // groups of 32 buckets looked up at once
     for (int e0 = 0; e0 <= E; e0 += 32 * kAhead) {
-        int64_t first[kAhead];
+        uint32_t first[kAhead], end[kAhead];
         int n[kAhead];
+        bool outside = false;
 #pragma unroll
         for (int g = 0; g < kAhead; ++g) {
             const int e = e0 + g * 32 + lane;
-            first[g] = n[g] = 0;
+            first[g] = end[g] = (uint32_t)rows;
             if (e <= E) {
-                const int64_t b = __ldg(off + e);
-                const int64_t end = e < E ? min(__ldg(off + e + 1), rows) : rows;
-                first[g] = e < E ? b + max(__ldg(cnt + e), 0) : b;
-                first[g] = min(max(first[g], (int64_t)0), rows);
-                n[g] = (int)max(end - first[g], (int64_t)0);  // rows are below 2^31
+                const uint32_t b = start(e), c = e < E ? max(__ldg(cnt + e), 0) : 0;
+                if (e < E) end[g] = start(e + 1);
+                first[g] = min(b + c, b == none ? b : (uint32_t)rows);
+                outside |= end[g] == none;
             }
         }
+        if (outside)
+#pragma unroll
+            for (int g = 0; g < kAhead; ++g)
+                for (int e = e0 + g * 32 + lane + 2; end[g] == none; ++e)
+                    end[g] = e <= E ? start(e) : (uint32_t)rows;
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) n[g] = max((int)(end[g] - first[g]), 0);
 #pragma unroll
         for (int g = 0; g < kAhead; ++g) {
             int64_t upto = n[g];  // rows of this lane's bucket and those before it
@@ -351,7 +364,8 @@ __device__ __forceinline__ void zero_gaps(uint8_t *base, int64_t row_bytes, int6
             for (; next < seen + total; next += W) {
                 const int64_t i = next - seen;
                 const int at = __popc(__ballot_sync(0xffffffffu, upto <= i));
-                const int64_t row = __shfl_sync(0xffffffffu, first[g] + n[g] - upto, at) + i;
+                const int64_t row =
+                    __shfl_sync(0xffffffffu, (int64_t)first[g] + n[g] - upto, at) + i;
                 for (int64_t o = lane * 16; o < row_bytes; o += 512)
                     st16(base + row * row_bytes + o, make_uint4(0, 0, 0, 0));
             }

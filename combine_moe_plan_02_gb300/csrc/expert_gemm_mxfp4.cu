@@ -193,7 +193,7 @@ __device__ void build_schedule(const MxArgs &a, Schedule &s)
         int tiles = 0;
         if (e < a.E) {
             int64_t f = __ldg(a.off + e), c = __ldg(a.cnt + e);
-            if (f < 0 || c < 0 || f + c > a.rows) {
+            if (f < 0 || c < 0 || f > a.rows - c) {  // f + c may not fit
                 // never outside the rows: the bucket is left out and reported
                 atomicOr(&g_mxgemm_error, kErrExpertBucket);
                 f = c = 0;
