@@ -114,3 +114,40 @@ def test_each_value_near_the_last_scale(hidden):
     down = one_hot(n, list(range(n)), 2.0 ** 100 if hidden else 1.0)
     idx, w = torch.zeros(S, 1, dtype=torch.int32, device="cuda"), torch.ones(S, 1, device="cuda")
     check((x, idx, w, up, down))
+
+
+def small_steps(n):
+    """[n / 64 terms of a row]: 1, then 0.75 of f32's last place at 1 in each step of 64
+    elements, and their sum.  Cut off at each step, the sum stays 1."""
+    row = torch.zeros(n)
+    row[0], row[64::64] = 1.0, 0.75 * 2.0 ** -23
+    return row, 1 + (n // 64 - 1) * 0.75 * 2.0 ** -23
+
+
+# An accumulator of at most 16 steps is cut off by a last place in each; the parts are added
+# in f32, half a place each.
+def lost_at_most(n):
+    return (16 + n / 1024 / 2 + 1) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("n", [1024, 6144, 16384])
+@pytest.mark.parametrize("first", [True, False])
+def test_small_terms_of_long_sums(first, n):
+    """f32 outputs on MXFP4 weights: gates of 64, which silu leaves as they are, lifts of 1 / 64 of
+    the sum in the first product, or of 1 / 64 and the sum in the second."""
+    import combine_moe_plan_02_gb300 as moe
+    row, want = small_steps(n)
+    H, F = (n, 32) if first else (32, n)
+    up, down = torch.zeros(1, 2 * F, H, device="cuda"), torch.zeros(1, H, F, device="cuda")
+    up[0, :F, 0] = 64.0
+    if first:
+        up[0, F:] = row.cuda() / 64
+        down[0, torch.arange(F), torch.arange(F)] = 1.0
+    else:
+        up[0, F:, 0] = 1 / 64
+        down[0] = row.cuda()
+    x = torch.ones(2, H, dtype=BF16, device="cuda")
+    idx, w = torch.zeros(2, 1, dtype=torch.int32, device="cuda"), torch.ones(2, 1, device="cuda")
+    out = moe.moe_expert_layer(x, idx, w, moe.moe_quant_mxfp4(up), moe.moe_quant_mxfp4(down), out_dtype=F32)
+    off = (out[:, :32].to(F64) - want).abs().max()
+    assert float(off) <= lost_at_most(n), (float(off) * 2 ** 23, (want - 1) * 2 ** 23)
