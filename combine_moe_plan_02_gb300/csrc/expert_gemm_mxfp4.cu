@@ -5,7 +5,7 @@
 // with x and w E2M1 codes under E8M0 scales of 32 elements (csrc/mxfp4.cu has the
 // format).  The block-scaled matrix instruction (kind::mxf4) takes codes and
 // scales as they are: codes from shared memory, scales from tensor memory; sums
-// are f32, rounded once to the output's type.
+// are f32, for f32 outputs in parts of 4096 elements, rounded once to the output's type.
 //
 // Weight rows are the M side (256 TMEM lanes of a pair of CTAs), tokens the N
 // side (128 or 256 columns), as in csrc/expert_gemm.cu, whose pairs, warps and
@@ -66,6 +66,13 @@ constexpr int kScaleAt = 384;       // first column of the scales
 constexpr int kScaleCols = 24;      // of a block: 2 x (4 + 8)
 constexpr int kTmemCols = 512;
 constexpr int64_t kLongest = 32768;
+// Blocks of an accumulator of f32 outputs, 64 steps.  Sums lose nothing while all terms lie
+// within 24 bits of the largest sum; where a row's scales are spread further each step of 64
+// elements cuts low bits off.  Scales of 2^10 and 2^20 leave 2.9e-7 and 1.3e-6 of the result
+// (2-norm, 32768 elements; plain f32 sums 2.0e-7 and 3.7e-7; one accumulator 2.9e-6 and
+// 1.0e-5).  A part costs 0.3 us of a pair, in which the accumulators' shared columns are
+// read: 32768 x 7168 -> 4096 takes 370 us with two parts, 362 with one, 395 with four.
+constexpr int kPart = 16;
 
 __device__ uint32_t g_mxgemm_error;  // kErrExpertTimeout | kErrExpertBucket
 
@@ -290,7 +297,11 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
     const int stages = narrow ? kMaxStages : kStages;
     const int blocks = ceil_div(a.K, kK);
 
+    // In f32 a storing thread holds up to 128 sums.  The block starts with 384 x
+    // 168 = 64512 registers, which 128 x 72 + 256 x 216 are too.
+    constexpr bool kSums = sizeof(Tout) == 4;
     if (warp < 4) {
+        if (kSums) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0 || warp == 2) {
             const bool weights = warp == 0;
             if (elect_one()) {
@@ -346,19 +357,30 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
             // copies of scales, four products) is close to what bounds the kernel.
             if (elect_one()) {
                 Ring r(stages);
-                int i = 0;  // tiles begun
+                int i = 0;  // accumulators begun
                 bool ok = true;
                 const uint32_t scale_cols = narrow ? 16 : kScaleCols;
-                for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+                for (int t = pair; t < tiles && ok; t += pairs) {
                     const Tile c = tile_of(a, sched, t);
-                    // the columns that this accumulator shares with the one before have
-                    // been read, and all of the one before that
-                    if (i > 0 && !wait(&sh.acc_free, (uint32_t)(i - 1) & 1, &sh.stop)) break;
-                    tc_fence_after();
-                    const uint32_t acc = tmem + (i & 1) * kAccTwo;
+                    uint32_t acc = 0;
+                    int next = 0;  // first block of the next accumulator
                     const uint32_t low = instr_desc(c.cols, 0), high = instr_desc(c.cols, 1);
                     const bool wide = c.cols == kN;
                     for (int b = 0; b < blocks; ++b) {
+                        const bool fresh = b == next;
+                        if (fresh) {
+                            next = kSums ? next + kPart : blocks;
+                            if (kSums && b > 0) mma_commit(&sh.acc_full[(i - 1) & 1], 0);
+                            // the columns that this accumulator shares with the one before
+                            // have been read, and all of the one before that
+                            if (i > 0 && !wait(&sh.acc_free, (uint32_t)(i - 1) & 1, &sh.stop)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                            acc = tmem + (i & 1) * kAccTwo;
+                            ++i;
+                        }
                         if (!wait(&sh.full[r.at], r.round, &sh.stop)) {
                             ok = false;
                             break;
@@ -374,7 +396,7 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
                         copy_scales(sa, from_a);
                         copy_scales(sb, from_b);
                         if (wide) copy_scales(sb + 4, from_b + 32);
-                        mma_mxf4(acc, da, db, low, sa, sb, b > 0);
+                        mma_mxf4(acc, da, db, low, sa, sb, !fresh);
                         if (left > 64) mma_mxf4(acc, da + 2, db + 2, high, sa, sb, true);
                         if (left > 128) {
                             const uint32_t sa1 = sa + 4, sb1 = sb + (wide ? 8 : 4);
@@ -387,7 +409,7 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
                         mma_commit(&sh.empty[r.at], 0);
                         r.next();
                     }
-                    if (ok) mma_commit(&sh.acc_full[i & 1], 0);
+                    if (ok) mma_commit(&sh.acc_full[(i - 1) & 1], 0);
                 }
                 mma_commit(&sh.drain, 0);  // nothing is issued after this
             }
@@ -398,6 +420,7 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
         }
         __syncwarp();
     } else {
+        if (kSums) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         using Me = Meet<Tout>;
         const int q = warp & 3;             // this warp's quarter of the lanes
         const int odd = warp >> 2 & 1;      // its blocks of 32 columns: even or odd ones
@@ -420,27 +443,18 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
             return all != 0;
         };
         const uint32_t free_at = addr_in(&sh.acc_free, 0);
+        const int parts = kSums ? ceil_div(blocks, kPart) : 1;  // of a tile's reduction
         int i = 0;
-        for (int t = pair; t < tiles; t += pairs, ++i) {
+        for (int t = pair; t < tiles; t += pairs) {
             const Tile c = tile_of(a, sched, t);
-            const int buf = i & 1;
-            if (!agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop))) break;
-            tc_fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccTwo;
             const int count = c.cols / 64, used = ceil_div(c.to, 4);
             const int m = c.m0 + rank * kLanes;
-            // This warp's blocks, the shared columns first: the last ones of
-            // accumulator 0, the first ones of accumulator 1.  The first two are read
-            // before anything is stored; that covers what is shared.
-            auto block = [&](int k) { return 2 * (buf ? k : count - 1 - k) + odd; };
-            uint32_t two[2][32];
-            tmem_load(acc + block(0) * 32, two[0]);
-            tmem_load(acc + block(1) * 32, two[1]);
-            tmem_wait(two[0]);
-            tmem_wait(two[1]);
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_at(free_at);
+            // what the next tile or part needs of this accumulator is in registers
+            auto hand_on = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(free_at);
+            };
             auto store = [&](int jj, const uint32_t(&v)[32]) {
                 const int before = (jj >> 2) * 128 + (jj & 3);  // token of x: before + 4 x
                 join();  // what was here has been read
@@ -479,12 +493,73 @@ mxgemm_kernel(const __grid_constant__ MxMaps maps, MxArgs a)
                     st16(a.out + ((int64_t)(c.n0 + token) * a.M + first) * (int)sizeof(Tout), o);
                 }
             };
-            store(block(0), two[0]);
-            store(block(1), two[1]);
-            for (int k = 2; k < count; ++k) {
-                tmem_load(acc + block(k) * 32, two[0]);
+            // This warp's blocks, the columns that the accumulators share first: the last
+            // ones of accumulator 0, the first ones of accumulator 1.
+            if (kSums && parts > 1) {
+                uint32_t sum[kN / 64][32];  // f32
+#pragma unroll
+                for (int k = 0; k < kN / 64; ++k)
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) sum[k][x] = 0;
+                bool ok = true;
+                for (int p = 0; p < parts; ++p, ++i) {
+                    const int buf = i & 1;
+                    ok = wait_warp(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccTwo + odd * 32;
+                    // two blocks, half of one added while the next half is read
+                    auto take = [&](int k, int l) {
+                        uint32_t v[2][16];
+                        tmem_load(acc + k * 64, v[0]);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            tmem_wait(v[h & 1]);
+                            if (h < 3)
+                                tmem_load(acc + (h < 1 ? k : l) * 64 + (h + 1) % 2 * 16, v[(h + 1) & 1]);
+                            uint32_t *to = sum[h < 2 ? k : l] + h % 2 * 16;
+#pragma unroll
+                            for (int x = 0; x < 16; ++x)
+                                to[x] = __float_as_uint(__uint_as_float(to[x]) +
+                                                        __uint_as_float(v[h & 1][x]));
+                        }
+                    };
+                    if (buf == 0 && count == 4) {
+                        take(3, 2);
+                        hand_on();
+                        take(1, 0);
+                    } else {
+                        take(0, 1);
+                        hand_on();
+                        if (count == 4) take(2, 3);
+                    }
+                }
+                if (!agree(ok)) break;
+#pragma unroll
+                for (int k = 0; k < kN / 64; ++k)
+                    if (k < count) store(2 * k + odd, sum[k]);
+            } else {
+                const int buf = i & 1;
+                if (!agree(wait(&sh.acc_full[buf], (uint32_t)(i / 2) & 1, &sh.stop))) break;
+                tc_fence_after();
+                ++i;
+                const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kAccTwo;
+                // The first two are read before anything is stored; that covers what is
+                // shared.
+                auto block = [&](int k) { return 2 * (buf ? k : count - 1 - k) + odd; };
+                uint32_t two[2][32];
+                tmem_load(acc + block(0) * 32, two[0]);
+                tmem_load(acc + block(1) * 32, two[1]);
                 tmem_wait(two[0]);
-                store(block(k), two[0]);
+                tmem_wait(two[1]);
+                hand_on();
+                store(block(0), two[0]);
+                store(block(1), two[1]);
+                for (int k = 2; k < count; ++k) {
+                    tmem_load(acc + block(k) * 32, two[0]);
+                    tmem_wait(two[0]);
+                    store(block(k), two[0]);
+                }
             }
         }
     }

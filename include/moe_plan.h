@@ -541,9 +541,12 @@ int moe_dequant_mxfp4(const uint8_t *codes, const uint8_t *scales, int64_t group
  * The experts' product with rows and weights in MXFP4:
  *   y[r, n] = sum_d x[r, d] * w[e, n, d]      for r in bucket e of a plan
  * with the values that codes and scales stand for, f32 sums, rounded once to the
- * output's type (MOE_BF16 or MOE_F32).  Output rows in no bucket are zero; such
- * rows and experts without rows are never used, whatever they hold.  A bucket
- * outside [0, rows) is left out and flagged (bit 5); buckets must not overlap.
+ * output's type (MOE_BF16 or MOE_F32).  Sums are exact while all terms lie within 24
+ * bits of the largest; beyond, each step of 64 elements cuts off less than 2^-23 of
+ * its sum, in f32 outputs of sums over 4096 elements, which are then added in f32.
+ * Output rows in no bucket are zero; such rows and experts without rows are never
+ * used, whatever they hold.  A bucket outside [0, rows) is left out and flagged (bit
+ * 5); buckets must not overlap.
  *
  * x_codes [rows, D / 2], x_scales [ceil(D / 128), rows, 4]; w_codes [E, N, D / 2],
  * w_scales [E, ceil(D / 128), N, 4]: as moe_dispatch_quant_mxfp4,
@@ -563,7 +566,9 @@ int moe_expert_gemm_mxfp4(const uint8_t *x_codes, const uint8_t *x_scales, int64
  * weights):
  *   out[s] = sum over k with topk_idx[s,k] in [0, E) of topk_w[s,k] * w_down[e] h
  *   h      = silu(w_up[e, :F] x[s]) * (w_up[e, F:] x[s]),   e = topk_idx[s,k]
- * Sums and h are f32 and out is rounded once.  bf16 weights: h enters the second
+ * Sums and h are f32 and out is rounded once; each step of 64 elements (MXFP4 weights; 16
+ * for bf16) cuts off less than 2^-23 of a sum, in f32 outputs of sums over 1024 (128)
+ * elements, which are then added in f32.  bf16 weights: h enters the second
  * product as three bf16 parts, all 24 bits of it.  MXFP4 weights: x and h enter the
  * products with an error of at most 2^-23 of the largest of 32 neighbours, or 2^-129
  * where that is more.  A token with an infinite x or h, or whose experts have
