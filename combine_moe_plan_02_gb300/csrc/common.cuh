@@ -313,6 +313,19 @@ __device__ __forceinline__ void st16(void *p, uint4 v)
                  : "memory");
 }
 
+// silu(gate) * up for gates below this: exp(-gate) leaves f32 at -88.7, where up may bring
+// the product back.
+constexpr float kFarGate = -80.0f;
+
+// gate exp(gate) up, as 1 + exp(-gate) is exp(-gate) to 115 bits, with the exponential in
+// two halves, one on either side of `up`, so that no step leaves f32 before the result does.
+// Off by 2^-20, or 2^-16 below -174, where a half is subnormal.
+__device__ __forceinline__ float far_gate(float gate, float up)
+{
+    const float half = expf(0.5f * gate);
+    return gate * half * up * half;
+}
+
 // Clears the rows that hold no entry: from cnt[e] filled rows to the end of
 // each bucket, and from off[E] to `rows`.  Called by whole warps; warp gw of W
 // takes every W-th such row.  A bucket that begins outside the buffer has no such rows:

@@ -919,7 +919,9 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                 for (int x = 0; x < kRows; ++x) {
                     const float up = __shfl_down_sync(0xffffffffu, sum[x], MX ? 16 : 8);
                     if (gate && x < c.rows)
-                        box[x * 64 + f] = sum[x] / (1.0f + expf(-sum[x])) * up;
+                        box[x * 64 + f] = sum[x] < kFarGate
+                                              ? far_gate(sum[x], up)
+                                              : sum[x] / (1.0f + expf(-sum[x])) * up;
                 }
                 join();
                 store_h<MX>(a, c, box, me);

@@ -97,25 +97,18 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *f)
     return r;
 }
 
-// The fast division gives 0 for divisors above 2^126, which 1 + exp(-gate) is below a gate
-// of -87.3, and exp(-gate) itself leaves f32 at -88.7.
-constexpr float kFarGate = -80.0f;
-
-// h = silu(gate) * up of such gates: gate exp(gate) up, as 1 + exp(-gate) is exp(-gate) to
-// 115 bits, with the exponential in two halves, one on either side of `up`, so that no step
-// leaves f32 before the result does.  Off by 2^-20, or 2^-16 below -174, where a half is
-// subnormal.  The gates are read again, one by one: they are rare, and kept until here they
-// would cost all others registers.  (32768 x 2048 bf16: 47.6 us with and without; with halves
-// for every gate instead 52 us.)
+// h of gates below kFarGate: the fast division gives 0 for divisors above 2^126, which
+// 1 + exp(-gate) is below -87.3.  The gates are read again, one by one: they are rare, and kept
+// until here they would cost all others registers.  (32768 x 2048 bf16: 47.6 us with and
+// without; with the exponential in halves for every gate 52 us.)
 template <typename T>
 __device__ __forceinline__ void far_gates(const T *gates, uint32_t F, float (&h)[kLane])
 {
 #pragma unroll 1
     for (int i = 0; i < kLane; ++i) {
         const float gate = (float)gates[i];
-        if (gate >= kFarGate || isnan(gate)) continue;
-        const float half = expf(0.5f * gate);
-        const float v = gate * half * (float)gates[F + i] * half;
+        if (!(gate < kFarGate)) continue;
+        const float v = far_gate(gate, (float)gates[F + i]);
 #pragma unroll
         for (int k = 0; k < kLane; ++k)
             if (k == i) h[k] = v;
