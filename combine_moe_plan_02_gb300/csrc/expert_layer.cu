@@ -946,7 +946,10 @@ layer_kernel(const __grid_constant__ LayerMaps maps, LayerArgs a)
                            (uint32_t)valid[token];
                 }
                 uint32_t ready = __ballot_sync(0xffffffffu, last);
-                if (ready) __threadfence();
+                if (ready) {
+                    __threadfence();
+                    __syncwarp();  // what the counting lanes saw, all lanes may read
+                }
                 for (; ready; ready &= ready - 1) {
                     const int s = __shfl_sync(0xffffffffu, token, __ffs(ready) - 1);
                     sum_entries(a.y, a.topk_w, rt.place, a.K, a.H, c.m * kTile + 4 * lane, s,
