@@ -34,10 +34,10 @@
 // row is the block rounded to multiples of 2^(e - 1) and less (values up to 4 units,
 // steps of at most one), the next what that left (at most half a unit) in units of
 // 2^(e - 4), and so on, each three bits further.  The eighth leaves at most 2^-23 of a,
-// about what an f32 sum does, or 2^-129 where the scales end.  Each row is a column of the product, and the columns' sums
-// are added in f32.  Decoding the weights to f16 in registers for the warp-wide
-// instruction instead takes 2.7 instructions a weight: 70 us for one token of 8
-// experts (6144, 2048) and 2290 us for 32 tokens of 64 (7168, 2048).
+// about what an f32 sum does, or 2^-129 where the scales end.  Each row is a column of the
+// product, and the columns' sums are added in f32.  Decoding the weights to f16 in registers
+// for the warp-wide instruction instead takes 2.7 instructions a weight: 70 us for one token
+// of 8 experts (6144, 2048) and 2290 us for 32 tokens of 64 (7168, 2048).
 //
 // The instruction wants the scales of 128 rows and 128 elements as words in 32 lanes
 // x 4 columns of tensor memory, row 32 j + q in column j of lane q, and a copy from
