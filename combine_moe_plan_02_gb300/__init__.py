@@ -709,7 +709,8 @@ def moe_dispatch_quant_mxfp4(x: torch.Tensor, tok_map: torch.Tensor, *,
                              out: Optional[MxFp4] = None, stream=None) -> MxFp4:
     """Rows [S, D] (bf16 or f32) to MXFP4 in the K packed rows of each token.
     Without `out` there are S * K packed rows, rounded up to a multiple of 4 as
-    moe_expert_gemm_mxfp4 asks."""
+    moe_expert_gemm_mxfp4 asks; a padded plan has E * capacity rows, given as
+    `out`."""
     if x.dim() != 2 or tok_map.dim() != 2:
         raise ValueError("x must be [S, D] and tok_map [S, K]")
     S, D = x.shape
